@@ -37,8 +37,9 @@ L2_BYTES = 129 * 1000 * 1000
 FALLBACK_HBM_GBS = 6800.0
 METRIC = "µs/call and achieved HBM GB/s (% of roofline) for Q4/Q5 skinny GEMM, T=1..8"
 MAX_T = 64
-KERNEL_SOURCES = sorted(f for f in os.listdir(os.path.join(ROOT, "weight_only_groupwise_gb300", "csrc"))
-                        if f.endswith((".cu", ".cuh", ".h")))
+# The device code and work split of the projection kernels (not the library's other kernels or its
+# host runtime, whose changes leave the captured traffic valid).
+KERNEL_SOURCES = ["nq_common.cuh", "nq_proj.cuh", "nq_tc.cuh"]
 
 
 # ---------------------------------------------------------------- ranks
