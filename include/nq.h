@@ -384,6 +384,138 @@ nq_status nq_program_info(const nq_program* prog, int64_t out[4]);
  * ignored. The recorded buffers are untouched. */
 void nq_program_destroy(nq_program* prog);
 
+/* ---------------------------------------------------------------- serving step: paged KV cache */
+
+/*
+ * What a decode, verify or prompt step needs around the projections: where the step's tokens go
+ * in a paged KV cache, their attention over it, and the choice of the next token. The pages run a
+ * paged KV pool with pages of 64 tokens ("ninfer-ext" README, the KV streaming section) without
+ * describing its tables, layouts or kernels: all are this library's definition.
+ *
+ * Lengths, tables and settings are DEVICE arrays that no call copies to the host, so that a step can be
+ * captured in a CUDA graph and replayed as the requests grow. The calls follow the conventions
+ * above (asynchronous on `stream`, arguments checked on the host before anything is launched,
+ * programmatic dependent launch with every read and write after the preceding kernel) with these
+ * differences: element pointers need 16-byte alignment, index arrays that of their type; strides
+ * are in elements. Values inside device arrays cannot be checked on the host: each call says
+ * what an unusable one does; none reads or writes outside the arrays it was given.
+ */
+
+enum { NQ_BF16 = 0, NQ_FP16 = 1, NQ_FP32 = 2 };   /* dtype arguments */
+
+/* Most requests of one call. */
+#define NQ_MAX_REQUESTS 8192
+
+/*
+ * A paged KV cache: two tensors of 16-bit elements, K and V, with the same strides. Row `j` of
+ * request r, KV head h is at block_table[r][j / page] * block_stride + (j % page) * row_stride +
+ * h * head_stride, `dim` elements that lie together. Any order of page rows and heads will do
+ * ([block][row][head][dim] and [block][head][row][dim] among them, K and V as halves of one
+ * tensor too).
+ *   page   keys of a block: 16, 32, 64, 128 or 256;  dim  64, 128 or 256
+ *   strides: multiples of 8, at least dim, below 2^38; num_blocks up to 2^28; heads up to 1024
+ */
+typedef struct nq_kv_cache {
+    void* K;
+    void* V;
+    long long block_stride, row_stride, head_stride;
+    int num_blocks, page, heads, dim;
+} nq_kv_cache;
+
+/*
+ * nq_page_tables: the step's block tables and slot maps, from the requests' lengths, in one
+ * launch. Request r has lens[r] tokens in the cache and brings new_lens[r] more; the step's
+ * tokens lie flat, request after request.
+ *   lens, new_lens  int32 [R]
+ *   free_blocks     int32 [free_capacity], of which the first *num_free (device int32) are free
+ *   block_table     int32 [R][max_blocks] with rows table_stride apart, read and extended: the
+ *                   blocks that request r lacks for its new tokens are taken from the front of the
+ *                   free list, in request order, and written behind those it owns
+ *                   (ceil(lens / page)); other entries are left alone
+ *   q_start         int32 [R + 1], written: the request's first token in the flat order
+ *   kv_lens         int32 [R], written: lens + new_lens, or 0 for a refused request
+ *   positions       int32 [max_tokens], written: each token's position in its request
+ *   slots           int64 [max_tokens], written: block * page + row of each token (nq_kv_append)
+ *   counts          int32 [3], written: tokens, blocks taken from the free list, requests refused
+ * A request is refused, and its tokens get position and slot -1, when a length is negative, when
+ * it needs more than max_blocks blocks, when its tokens pass max_tokens, or when it needs blocks
+ * and the needs of the requests up to it, refused ones among them, pass the free list. Entries
+ * past the last token are -1 too. The caller drops counts[1] ids from the front of its list.
+ * 0 <= R <= NQ_MAX_REQUESTS; max_tokens <= 2^28; max_blocks <= 2^24. R = 0 needs max_tokens = 0 and
+ * writes nothing.
+ */
+nq_status nq_page_tables(const int* lens, const int* new_lens, int R, const int* free_blocks, int free_capacity,
+                         const int* num_free, int page, int* block_table, long long table_stride, int max_blocks,
+                         int* q_start, int* kv_lens, int* positions, int64_t* slots, int max_tokens, int* counts,
+                         void* stream);
+
+/*
+ * nq_kv_append: store the step's keys and values through the slot map: token t's K row
+ * ([heads][dim], k + t * k_stride) and V row go to slot slots[t] = block * page + row. A slot
+ * outside the cache (-1) stores nothing. Two tokens with one slot: either may win. The 16-bit
+ * elements are copied as they are. k and v must not overlap the cache.
+ */
+nq_status nq_kv_append(const void* k, long long k_stride, const void* v, long long v_stride, const int64_t* slots,
+                       int tokens, const nq_kv_cache* cache, void* stream);
+
+/*
+ * nq_attn_paged: causal attention of the step's new tokens over the paged cache, which holds
+ * their own keys and values already (nq_kv_append):
+ *   O[t, h] = sum_j softmax_j(scale * q[t, h] . K[j, h / G]) V[j, h / G],  G = q_heads / heads,
+ * for token i of request r at position p = kv_lens[r] - n + i (n = q_start[r+1] - q_start[r])
+ * over the keys 0 <= j <= p with window == 0, else those with j > p - window or j < sinks: a sliding
+ * window whose first `sinks` tokens stay visible. A token that sees no key (p < 0) gets zeros, and so do the rows
+ * from q_start[R] to `tokens`.
+ *   q    [tokens][q_heads][dim], tokens q_stride apart; out the same with out_stride, written; must not
+ *        overlap an input
+ *   dtype NQ_BF16 or NQ_FP16: q, out and the cache
+ *   scale > 0 and finite; 0 <= window, sinks <= 2^30; sinks need a window
+ *   tokens <= 2^23; 1 <= G <= 128; max_blocks * page <= 2^30
+ * Scores, softmax statistics and sums are fp32; the probabilities are rounded to the 16-bit type
+ * for their product with V, O once at the end. Table entries of pages that no new token sees are
+ * not used (a window's old pages may have been given back) apart from those that share a tile of
+ * 128 keys with seen ones, which may be any number; an entry outside the cache reads as rows of
+ * zeros. Cache rows that no new token sees may hold anything, NaN included. A NaN or infinity in
+ * a V row that one of a tile's tokens sees reaches the other tokens of that tile (up to 128 / G
+ * consecutive ones), as 0 * NaN does in a plain product.
+ * q_start is clamped to 0..tokens and taken as non-decreasing, kv_lens to 0..max_blocks * page.
+ * One launch over all SMs and one that joins query tiles whose keys were spread over several;
+ * deterministic for a given device. Uses a library workspace of about 40 MB, allocated on the
+ * first call (or by nq_attn_reserve, before stream capture) and shared like the projections'
+ * workspace: order the calls of one device on one stream.
+ */
+nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* cache, const int* block_table,
+                        long long table_stride, int max_blocks, const int* q_start, const int* kv_lens, int R,
+                        int tokens, int q_heads, float scale, int window, int sinks, int dtype, void* out,
+                        long long out_stride, void* stream);
+
+/* nq_attn_reserve: allocate the current device's attention workspace now. */
+nq_status nq_attn_reserve(void);
+
+/*
+ * nq_sample: the next token of each of B rows of logits [B][V] (dtype NQ_BF16, NQ_FP16 or NQ_FP32;
+ * rows `stride` apart), from given random numbers: noise fp32 [B][V] (rows noise_stride apart),
+ * independent Exp(1) variates. With l the row's logits (NaN counts as -inf), T its temperature and
+ *   d_i = (l_i - max l) / T   (0 where l_i is the maximum),
+ * tokens are ordered by logit, descending, equal ones by index, ascending, and kept by, in turn:
+ *   top_k  the first top_k                                          (<= 0: all)
+ *   top_p  those whose mass of exp(d) before them is below top_p times the mass of the tokens that
+ *          top_k kept                                               (>= 1: all)
+ *   min_p  those with d >= log(min(min_p, 1)), i.e. at least min_p times as likely as the first
+ *                                                                   (<= 0: all)
+ * the first token always. The row's token is the kept one with the highest d_i - log(noise_i), the
+ * lowest index among equals: token i with probability exp(d_i) over the kept ones' sum.
+ *   temperature, top_p, min_p  fp32 [B], top_k int32 [B]; each may be NULL (1, all, all, all)
+ *   temperature <= 0 or NaN: the first token; noise is then not read
+ *   tokens  int32 [B], written; -1 for a row with no logit above -inf
+ * Tokens of -inf logits are never kept. Masses are summed in 2^-30 of the first token's weight, as
+ * integers: the result does not depend on the order of summation. 1 <= V <= 524160; B <= 2^20. Logits need
+ * the alignment of their type only. Noise is read at kept tokens only.
+ */
+nq_status nq_sample(const void* logits, int dtype, long long stride, const float* noise, long long noise_stride,
+                    int B, int V, const float* temperature, const int* top_k, const float* top_p, const float* min_p,
+                    int* tokens, void* stream);
+
 /* ---------------------------------------------------------------- runtime */
 
 /*

@@ -10,6 +10,7 @@
 
 #include "nq.h"
 #include "nq_launch.h"
+#include "nq_step.h"
 
 using namespace nq;
 
@@ -242,6 +243,7 @@ struct DevState {
     long long tc_tickets = 0, tc_floats = 0;
     float* tc_gate = nullptr;   // fp32 gate outputs of a tensor-core SwiGLU call, [T][N]
     long long tc_gate_floats = 0;
+    uint8_t* attn_ws = nullptr;  // paged attention: [err: 256 B][split records][(max, sum)][partials]
 };
 
 constexpr int kMaxDevices = 64;
@@ -843,6 +845,33 @@ int reserve_grouped_workspace(int bits, const nq_group* groups, int count, int T
     return reserve_grouped(bits, groups, count, T, K);
 }
 
+int step_device(StepDevice* out) {
+    DevState* d = nullptr;
+    const nq_status st = current_device(&d, nullptr);
+    if (st != NQ_OK) return st;
+    std::lock_guard<std::mutex> lk(g_mu);
+    *out = {d->sms, g_pdl, g_wait_ns};
+    return NQ_OK;
+}
+
+int attn_workspace(uint8_t** ws) {
+    DevState* d = nullptr;
+    const nq_status st = current_device(&d, nullptr);
+    if (st != NQ_OK) return st;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!d->attn_ws) {
+        void* p = nullptr;
+        if (cudaMalloc(&p, attn_ws_bytes(d->sms)) != cudaSuccess) return NQ_ERR_CUDA;
+        if (cudaMemset(p, 0, kAttnErrBytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+            cudaFree(p);
+            return NQ_ERR_CUDA;
+        }
+        d->attn_ws = static_cast<uint8_t*>(p);
+    }
+    *ws = d->attn_ws;
+    return NQ_OK;
+}
+
 unsigned long long workspace_epoch() { return g_ws_epoch.load(); }
 }  // namespace nq
 
@@ -1001,10 +1030,17 @@ nq_status nq_device_error(void) {
     const nq_status st_static = noalloc_take_error(dev);
     if (st_static == NQ_ERR_CUDA) return st_static;
     std::lock_guard<std::mutex> lk(g_mu);
-    if (!d->ws) return st_static;
+    int attn_err = 0;
+    if (d->attn_ws) {
+        if (cudaMemcpy(&attn_err, d->attn_ws, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return NQ_ERR_CUDA;
+        if (attn_err && (cudaMemset(d->attn_ws, 0, kAttnErrBytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess))
+            return NQ_ERR_CUDA;
+    }
+    const nq_status st_other = attn_err ? NQ_ERR_TIMEOUT : st_static;
+    if (!d->ws) return st_other;
     int err = 0;
     if (cudaMemcpy(&err, d->ws, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return NQ_ERR_CUDA;
-    if (err == 0) return st_static;
+    if (err == 0) return st_other;
     if (cudaMemset(d->ws, 0, ws_partials_off(d->tickets_cap)) != cudaSuccess ||
         (d->tc_ws && cudaMemset(d->tc_ws, 0, (size_t)d->tc_tickets * 4) != cudaSuccess) ||
         cudaDeviceSynchronize() != cudaSuccess)
@@ -1017,7 +1053,7 @@ void nq_shutdown(void) {
     int cur = 0;
     cudaGetDevice(&cur);
     for (int i = 0; i < kMaxDevices; ++i) {
-        if (!g_dev[i].ws && !g_dev[i].tc_ws && !g_dev[i].tc_gate) continue;
+        if (!g_dev[i].ws && !g_dev[i].tc_ws && !g_dev[i].tc_gate && !g_dev[i].attn_ws) continue;
         cudaSetDevice(i);
         cudaDeviceSynchronize();
         cudaFree(g_dev[i].ws);
@@ -1029,6 +1065,8 @@ void nq_shutdown(void) {
         cudaFree(g_dev[i].tc_gate);
         g_dev[i].tc_gate = nullptr;
         g_dev[i].tc_gate_floats = 0;
+        cudaFree(g_dev[i].attn_ws);
+        g_dev[i].attn_ws = nullptr;
         ++g_ws_epoch;
     }
     cudaSetDevice(cur);

@@ -1,0 +1,136 @@
+// Instantiations and host side of the paged attention call (nq_attn.cuh): argument checks, the
+// caches' tensor maps and the two launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "nq.h"
+#include "nq_attn.cuh"
+#include "nq_launch.h"
+
+namespace nq {
+
+int check_kv_cache(const nq_kv_cache* c);
+long long kv_cache_span(const nq_kv_cache* c);
+
+namespace {
+
+template <int D, bool BF16>
+cudaError_t attn_launch(const AttnArgs& a, int sms, cudaStream_t stream, bool pdl) {
+    auto kern = attn_kernel<D, BF16>;
+    static thread_local int set_for_device = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (set_for_device != dev) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnGeo<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        set_for_device = dev;
+    }
+    cudaError_t e = step_launch(kern, dim3(sms), dim3(kAttnThreads), AttnGeo<D>::kSmem, stream, pdl, 1, a);
+    if (e != cudaSuccess) return e;
+    return step_launch(attn_join_kernel<D, BF16>, dim3(sms, kJoinRowsY), dim3(kJoinWarps * 32), 0, stream, pdl, 1, a);
+}
+
+template <bool BF16>
+cudaError_t attn_launch_dim(int dim, const AttnArgs& a, int sms, cudaStream_t stream, bool pdl) {
+    switch (dim) {
+        case 64: return attn_launch<64, BF16>(a, sms, stream, pdl);
+        case 128: return attn_launch<128, BF16>(a, sms, stream, pdl);
+        default: return attn_launch<256, BF16>(a, sms, stream, pdl);
+    }
+}
+
+bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+bool meet(const void* a, long long na, const void* b, long long nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+}  // namespace
+
+}  // namespace nq
+
+using namespace nq;
+
+extern "C" {
+
+nq_status nq_attn_reserve(void) {
+    StepDevice d;
+    const int st = step_device(&d);
+    if (st != NQ_OK) return st;
+    uint8_t* ws = nullptr;
+    if (!tensor_maps_available()) return NQ_ERR_CUDA;
+    return attn_workspace(&ws);
+}
+
+nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* cache, const int* block_table,
+                        long long table_stride, int max_blocks, const int* q_start, const int* kv_lens, int R,
+                        int tokens, int q_heads, float scale, int window, int sinks, int dtype, void* out,
+                        long long out_stride, void* stream) {
+    int st = check_kv_cache(cache);
+    if (st != NQ_OK) return st;
+    if (R < 0 || R > kAttnMaxRequests || tokens < 0 || tokens > (1 << 23) || max_blocks < 0 || table_stride < max_blocks)
+        return NQ_ERR_SHAPE;
+    if (q_heads < 1 || q_heads % cache->heads != 0 || q_heads / cache->heads > kAttnRows) return NQ_ERR_SHAPE;
+    if ((long long)max_blocks * cache->page > (1 << 30)) return NQ_ERR_SHAPE;
+    if (window < 0 || window > (1 << 30) || sinks < 0 || sinks > (1 << 30) || (sinks > 0 && window == 0))
+        return NQ_ERR_SHAPE;
+    if (dtype != NQ_BF16 && dtype != NQ_FP16) return NQ_ERR_SHAPE;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return NQ_ERR_SHAPE;
+    const long long row = (long long)q_heads * cache->dim;
+    if (q_stride < row || out_stride < row) return NQ_ERR_SHAPE;
+    if (tokens == 0) return NQ_OK;
+    if (!q || !out || !q_start || (R > 0 && (!kv_lens || (max_blocks > 0 && !block_table)))) return NQ_ERR_NULL;
+    if (mis16(q) || mis16(out) || q_stride % 8 || out_stride % 8) return NQ_ERR_ALIGN;
+    for (const void* p : {(const void*)block_table, (const void*)q_start, (const void*)kv_lens})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return NQ_ERR_ALIGN;
+    const long long ob = ((tokens - 1) * out_stride + row) * 2, span = kv_cache_span(cache);
+    if (meet(out, ob, q, ((tokens - 1) * q_stride + row) * 2) || meet(out, ob, cache->K, span) ||
+        meet(out, ob, cache->V, span) || meet(out, ob, q_start, (R + 1) * 4ll) || meet(out, ob, kv_lens, R * 4ll) ||
+        (R > 0 && meet(out, ob, block_table, ((R - 1) * table_stride + max_blocks) * 4)))
+        return NQ_ERR_ALIAS;
+    StepDevice d;
+    st = step_device(&d);
+    if (st != NQ_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (R == 0 || cache->num_blocks == 0 || max_blocks == 0)   // no key anywhere
+        return cudaMemset2DAsync(out, out_stride * 2, 0, row * 2, tokens, s) == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+    uint8_t* ws = nullptr;
+    st = attn_workspace(&ws);
+    if (st != NQ_OK) return st;
+
+    alignas(64) AttnArgs a;
+    if (!encode_kv_map(&a.kmap, cache->K, cache, dtype == NQ_BF16, kAttnKeys) ||
+        !encode_kv_map(&a.vmap, cache->V, cache, dtype == NQ_BF16, cache->dim == 256 ? 64 : kAttnKeys))
+        return NQ_ERR_CUDA;
+    a.q = static_cast<const uint16_t*>(q);
+    a.out = static_cast<uint16_t*>(out);
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.q_start = q_start;
+    a.kv_lens = kv_lens;
+    a.R = R;
+    a.tokens = tokens;
+    a.heads = cache->heads;
+    a.group = q_heads / cache->heads;
+    a.page_shift = 0;
+    while ((1 << a.page_shift) < cache->page) ++a.page_shift;
+    a.max_keys = max_blocks * cache->page;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.dev_err = reinterpret_cast<int*>(ws);
+    a.splits = reinterpret_cast<int4*>(ws + kAttnErrBytes);
+    a.ml = reinterpret_cast<float2*>(ws + kAttnErrBytes + (size_t)d.sms * kAttnSplitBytes);
+    a.part = reinterpret_cast<float*>(a.ml + (size_t)d.sms * 2 * kAttnRows);
+    a.wait_ns = d.wait_ns;
+    const cudaError_t e = dtype == NQ_BF16 ? attn_launch_dim<true>(cache->dim, a, d.sms, s, d.pdl)
+                                           : attn_launch_dim<false>(cache->dim, a, d.sms, s, d.pdl);
+    return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,814 @@
+// nq_attn.cuh -- attention of a chunk of new tokens over a paged KV cache (nq_attn_paged):
+//
+//   O[t, h] = sum_j softmax_j(scale q[t, h] . K[j, h / G]) V[j, h / G]
+//
+// over the keys j that token t sees: with p its position, 0 <= j <= p and, with a window W,
+// j > p - W or j < sinks. One pass over the keys with the running maximum and sum of the
+// softmax, on the fifth-generation tensor cores.
+//
+// Tiles. A query tile is 128 rows of one (request, KV head): row i is token i / G, head i % G, so
+// the G query heads of a KV head share every key that is loaded, whatever the number of new
+// tokens (one, a verify round's 8, a prompt chunk's thousands). A key tile is 128 keys, cut at
+// multiples of 128, so a page (16..256 keys) never straddles two tiles unless it holds both.
+// Keys that no row of the query tile sees are not loaded, tile by tile.
+//
+// Work split. The (query tile, key tile) pairs of the whole call, in the order request, KV head,
+// query tile, key tile, are cut into one equal range per SM (stream-K): ragged lengths and few
+// rows need no other rule. A query tile whose keys are spread over several blocks is written as
+// fp32 partials with their maxima and sums; attn_join_kernel adds them in block order, so the
+// result does not depend on timing. Every block finds its range by itself from the lengths on the
+// device: no host copy of the lengths, no plan to keep, no waits between blocks.
+//
+// Roles of a block's 12 warps (one block per SM):
+//   * warps 0..7 -- softmax: thread = row (TMEM lane) and half of the tile's 128 columns. The two
+//     halves of a row exchange maxima through shared memory. The accumulator is rescaled only
+//     when a row's maximum grows by more than 2^8 in the exponential's argument (p <= 256 stays
+//     exact enough in 16 bits, the sum is fp32); p is rounded to the 16-bit type of the cache
+//     for the second product: its error averages out below the output's own rounding.
+//   * warp 8 -- producer: TMA copies of key and value pages (a 4-D map of the cache: dim, row,
+//     head, block) into a ring of shared-memory slots, 128-byte swizzled. The page ids are the
+//     map's last coordinate: an id outside the cache reads as zeros instead of faulting, and no
+//     offset is formed in 32 bits.
+//   * warp 9 -- MMA issuer: S = Q K^T (both from shared memory), O += P V (P from TMEM, V from
+//     shared memory as the N-major operand). S is double buffered: the product of tile j + 1 is
+//     issued before that of P of tile j, so that the tensor cores work during the softmax.
+//   * warps 10, 11 -- the query tile's rows into shared memory (cp.async: rows of a tile are G-wide
+//     runs of heads at a token stride, not a box).
+// TMEM: O in columns 0..dim-1, the S buffers (P over them) in columns 256.. and 384...
+//
+// Rows of V that no row of the tile sees (past the last key, before a window) may hold anything,
+// NaN included, and 0 x NaN would reach the sum: the softmax warps zero them in shared memory.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "nq_common.cuh"
+#include "nq_step.h"
+#include "nq_tc.cuh"
+
+namespace nq {
+
+constexpr int kAttnKeys = 128;                    // keys of a tile
+constexpr int kAttnThreads = 12 * 32;
+constexpr int kAttnSoftmaxWarps = 8;
+constexpr int kAttnProducer = 8, kAttnMma = 9, kAttnLoader = 10;
+constexpr int kAttnLoaderThreads = 64;
+constexpr int kAttnMaxRequests = 8192;            // the scan's 8 bytes a request fit the tile buffers
+constexpr int kAttnSCol = 256;                    // TMEM column of the first S buffer
+constexpr int kAttnCtrlBytes = 3072;
+constexpr float kAttnLazy = 8.f;                  // log2 of the growth that forces a rescale
+
+// Shared-memory geometry for a head dimension: the K slot holds 128 keys x min(D, 128) columns,
+// the V slot as many bytes: 128 keys x D, or 64 keys x 256.
+template <int D>
+struct AttnGeo {
+    static constexpr int kDK = D < 128 ? D : 128;           // columns of a K slot
+    static constexpr int kKSlots = D / kDK;                  // K slots of a key tile
+    static constexpr int kVKeys = D == 256 ? 64 : 128;       // keys of a V slot
+    static constexpr int kVSlots = kAttnKeys / kVKeys;
+    static constexpr int kSlotBytes = kAttnKeys * kDK * 2;
+    static constexpr int kQBytes = kAttnRows * D * 2;
+    static constexpr int kSlots = D == 256 ? 5 : (D == 128 ? 6 : 8);
+    static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kAttnCtrlBytes;
+    static_assert(kSmem <= kSmemLimit, "shared memory");
+    static_assert(kVKeys * D * 2 == kSlotBytes, "one slot size");
+    static_assert(kQBytes + kSlots * kSlotBytes >= kAttnMaxRequests * 8, "room for the scan");
+};
+
+struct AttnArgs {
+    CUtensorMap kmap, vmap;
+    const uint16_t* q;
+    uint16_t* out;
+    long long q_stride, out_stride;    // between tokens, elements
+    const int* table;
+    long long table_stride;
+    const int* q_start;
+    const int* kv_lens;
+    int R, tokens, heads, group;       // heads: KV heads; group: query heads per KV head
+    int page_shift, max_keys;
+    int window, sinks;                 // window 0: none, and then no sinks
+    float scale_log2;                  // scale x log2(e)
+    float* part;                       // [2 blocks][128][D] partial accumulators
+    float2* ml;                        // [2 blocks][128] (maximum, sum)
+    int4* splits;                      // [blocks][2] split records
+    int* dev_err;
+    unsigned long long wait_ns;
+};
+
+// ---------------------------------------------------------------- the work
+
+struct AttnReq {
+    int q0, n, kv;                     // first token, new tokens, keys
+};
+
+__device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, int r) {
+    AttnReq q;
+    const int b = a.q_start[r], e = a.q_start[r + 1];
+    q.q0 = min(max(b, 0), a.tokens);
+    q.n = min(max(e, q.q0), a.tokens) - q.q0;
+    q.kv = min(max(a.kv_lens[r], 0), a.max_keys);
+    return q;
+}
+
+// A query tile: its rows, and the key tiles it reads, kt(i) = i < first ? i : i + skip.
+struct AttnTile {
+    int row0, rows;
+    int p0;                            // position of the request's first new token
+    int pf, pl;                        // positions of the first and the last row
+    int hi, lo;                        // keys seen by some row: [lo, hi) and the sinks
+    int n, first, skip;
+};
+
+__device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, const AttnReq& q, int qt) {
+    AttnTile t;
+    t.row0 = qt * kAttnRows;
+    t.rows = min(kAttnRows, q.n * a.group - t.row0);
+    t.p0 = q.kv - q.n;
+    t.pf = t.p0 + t.row0 / a.group;
+    t.pl = t.p0 + (t.row0 + t.rows - 1) / a.group;
+    t.hi = max(0, t.pl + 1);
+    t.lo = a.window > 0 ? min(max(0, t.pf - a.window + 1), t.hi) : 0;
+    const int se = min(a.sinks, t.hi);
+    const int ns = (se + kAttnKeys - 1) / kAttnKeys, lt = t.lo / kAttnKeys, ht = (t.hi + kAttnKeys - 1) / kAttnKeys;
+    if (se == 0) {
+        t.first = 0;
+        t.skip = lt;
+        t.n = ht - lt;
+    } else if (ns >= lt) {
+        t.first = 0;
+        t.skip = 0;
+        t.n = ht;
+    } else {
+        t.first = ns;
+        t.skip = lt - ns;
+        t.n = ns + ht - lt;
+    }
+    return t;
+}
+
+// A block's walk over its range of units: segments of query tiles. A tile that sees no key
+// counts one unit (its rows are zeros).
+struct AttnWalk {
+    long long left, at;                // units left, global index of the next one
+    AttnReq rq;
+    AttnTile t;
+    int r, h, qt, nqt;
+    int k0, k1, units;                 // the segment: units k0..k1 of the tile's `units`
+    __device__ __forceinline__ void enter(const AttnArgs& a) {
+        rq = attn_req(a, r);
+        nqt = (rq.n * a.group + kAttnRows - 1) / kAttnRows;
+    }
+    __device__ __forceinline__ void cut(int from) {
+        units = max(1, t.n);
+        k0 = from;
+        k1 = (int)min((long long)units, from + left);
+    }
+    __device__ __forceinline__ void start(const AttnArgs& a, const long long* upto, long long u0, long long u1) {
+        left = u1 - u0;
+        at = u0;
+        if (left <= 0) return;
+        int lo = 0, hi = a.R - 1;      // the first request whose units pass u0
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (upto[mid] > u0)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        r = lo;
+        enter(a);
+        const long long base = r > 0 ? upto[r - 1] : 0;
+        const long long per = (upto[r] - base) / a.heads;
+        h = (int)((u0 - base) / per);
+        int rem = (int)((u0 - base) - h * per);
+        for (qt = 0;; ++qt) {
+            t = attn_tile(a, rq, qt);
+            const int u = max(1, t.n);
+            if (rem < u || qt >= nqt - 1) break;
+            rem -= u;
+        }
+        cut(rem);
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next(const AttnArgs& a) {
+        left -= k1 - k0;
+        at += k1 - k0;
+        if (left <= 0) return;
+        if (++qt == nqt) {
+            qt = 0;
+            if (++h == a.heads) {
+                h = 0;
+                do {
+                    ++r;
+                    enter(a);
+                } while (nqt == 0 && r < a.R - 1);
+            }
+        }
+        t = attn_tile(a, rq, qt);
+        cut(0);
+    }
+    __device__ __forceinline__ int tiles() const { return t.n == 0 ? 0 : k1 - k0; }
+    __device__ __forceinline__ int key_tile(int j) const {
+        const int i = k0 + j;
+        return i < t.first ? i : i + t.skip;
+    }
+};
+
+// Units of a request per KV head: all query tiles' key tiles, the warp's lanes sharing long ones.
+__device__ __forceinline__ long long attn_units(const AttnArgs& a, const AttnReq& q, bool live) {
+    const int nqt = live ? (q.n * a.group + kAttnRows - 1) / kAttnRows : 0;
+    long long w = 0;
+    if (nqt <= 4)
+        for (int i = 0; i < nqt; ++i) w += max(1, attn_tile(a, q, i).n);
+    unsigned big = __ballot_sync(0xFFFFFFFFu, nqt > 4);
+    while (big) {
+        const int src = __ffs(big) - 1;
+        big &= big - 1;
+        AttnReq s;
+        s.q0 = 0;
+        s.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
+        s.kv = __shfl_sync(0xFFFFFFFFu, q.kv, src);
+        const int m = (s.n * a.group + kAttnRows - 1) / kAttnRows;
+        long long v = 0;
+        for (int i = threadIdx.x & 31; i < m; i += 32) v += max(1, attn_tile(a, s, i).n);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+        if ((int)(threadIdx.x & 31) == src) w = v;
+    }
+    return w;
+}
+
+// ---------------------------------------------------------------- instructions
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+// D (+)= A * B with both operands in shared memory; predicated like tc_mma.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate, bool issue) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"((uint32_t)issue)
+        : "memory");
+}
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzled layout: rows of 128
+// bytes hold 64 consecutive N of one K; 8 K make a 1024-byte atom (stride between groups of 8 K),
+// `panel` bytes lead to the next 64 N.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t addr, uint32_t panel) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+#define NQ_R4(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3])
+#define NQ_O4(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3])
+
+// 32 consecutive columns of the thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : NQ_O4(v, 0), NQ_O4(v, 4), NQ_O4(v, 8), NQ_O4(v, 12), NQ_O4(v, 16), NQ_O4(v, 20), NQ_O4(v, 24), NQ_O4(v, 28)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        NQ_R4(v, 0), NQ_R4(v, 4), NQ_R4(v, 8), NQ_R4(v, 12), NQ_R4(v, 16), NQ_R4(v, 20), NQ_R4(v, 24), NQ_R4(v, 28)
+        : "memory");
+}
+#undef NQ_R4
+#undef NQ_O4
+
+// The device's base-2 exponential instruction (2 ulp): the softmax's p is rounded to 16 bits.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
+// Instruction descriptor: D fp32, A and B of one 16-bit type, A K-major, B K-major or (b_mn)
+// N-major, M = 128, N = n.
+constexpr uint32_t attn_idesc(bool bf16, int n, bool b_mn) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kAttnRows >> 4) << 24);
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
+    using Geo = AttnGeo<D>;
+    constexpr int kSlots = Geo::kSlots, kKS = Geo::kKSlots, kVS = Geo::kVSlots, kDK = Geo::kDK, kVK = Geo::kVKeys;
+    extern __shared__ __align__(1024) uint8_t attn_smem[];
+    uint8_t* const qmem = attn_smem;
+    uint8_t* const ring = attn_smem + Geo::kQBytes;
+    uint8_t* const ctrl = ring + kSlots * Geo::kSlotBytes;
+    float* const red = reinterpret_cast<float*>(ctrl);                      // [2 tiles][2 halves][128]
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(ctrl + 2048);
+    // bars: full[8], empty[8], s_full[2], p_ready[2], pv_done[2], o_free, q_full, q_free, done
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 64, sfull0 = empty0 + 64, pready0 = sfull0 + 16;
+    const uint32_t pvdone0 = pready0 + 16, ofree = pvdone0 + 16, qfull = ofree + 8, qfree = qfull + 8, done = qfree + 8;
+    volatile int* const flags = reinterpret_cast<volatile int*>(ctrl + 2048 + 256);
+    // flags: [0] abort, [1] slots issued, [2] producer done, [3] TMEM base
+    long long* const warp_sums = reinterpret_cast<long long*>(ctrl + 2048 + 256 + 64);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t wait_ns = a.wait_ns;
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull0 + 8 * i, 1);
+            mbar_init(pready0 + 8 * i, kAttnSoftmaxWarps);
+            mbar_init(pvdone0 + 8 * i, 1);
+        }
+        mbar_init(ofree, kAttnSoftmaxWarps);
+        mbar_init(qfull, kAttnLoaderThreads);
+        mbar_init(qfree, 1);
+        mbar_init(done, 1);
+        // the swizzled tiles need a 1024-byte base
+        flags[0] = (smem_u32(attn_smem) & 1023u) != 0;
+        flags[1] = 0;
+        flags[2] = 0;
+        if (flags[0]) atomicOr(a.dev_err, kDevErrTimeout);
+        mbar_fence_init();
+    }
+    if (warp == 0) tmem_alloc(smem_u32(const_cast<int*>(flags) + 3), 512);
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    // Units of all requests, scanned into the ring buffers (free until the first copies).
+    long long* const upto = reinterpret_cast<long long*>(attn_smem);
+    long long total = 0;
+    for (int r0 = 0; r0 < a.R; r0 += kAttnThreads) {
+        const int r = r0 + tid;
+        AttnReq rq = {0, 0, 0};
+        if (r < a.R) rq = attn_req(a, r);
+        long long w = attn_units(a, rq, r < a.R) * a.heads;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const long long u = __shfl_up_sync(0xFFFFFFFFu, w, d);
+            if (lane >= d) w += u;
+        }
+        __syncthreads();               // the sums of the round before have been read
+        if (lane == 31) warp_sums[warp] = w;
+        __syncthreads();
+        long long before = total;
+#pragma unroll
+        for (int i = 0; i < kAttnThreads / 32; ++i) {
+            const long long s = warp_sums[i];
+            if (i < warp) before += s;
+            total += s;
+        }
+        if (r < a.R) upto[r] = before + w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)flags[3];
+    AttnWalk w;
+    // no range is empty: the join takes every block from a tile's first to its last as a part
+    const long long blocks = max(1ll, min((long long)gridDim.x, total));
+    w.start(a, upto, min(total * blockIdx.x / blocks, total), min(total * (blockIdx.x + 1) / blocks, total));
+    fence_proxy_async_smem();          // the scan's buffers go to the copy engine
+    __syncthreads();
+
+    if (warp == kAttnProducer) {
+        // ------------------------------------------------------------ producer
+        const int kb = min(1 << a.page_shift, kAttnKeys), vb = min(1 << a.page_shift, kVK);
+        const int kboxes = kAttnKeys / kb, page_mask = (1 << a.page_shift) - 1;
+        const int row_bits = __ffs(kb) - 1, vrow_bits = __ffs(vb) - 1;
+        int seq = 0;
+        bool ok = flags[0] == 0;
+        // ids of the boxes of key tile kt, one a lane (-1, which reads as zeros, past the keys)
+        auto ids = [&](const AttnWalk& k, int kt) {
+            const int key = kt * kAttnKeys + lane * kb;
+            return lane < kboxes && key < k.t.hi ? __ldg(a.table + k.r * a.table_stride + (key >> a.page_shift)) : -1;
+        };
+        auto claim = [&](uint32_t& bar, uint32_t& dst, int bytes) {
+            const int slot = seq % kSlots;
+            if (seq >= kSlots) ok = mbar_wait(empty0 + 8 * slot, ((seq / kSlots) - 1) & 1, flags, a.dev_err, wait_ns);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) return;
+            bar = full0 + 8 * slot;
+            dst = smem_u32(ring + slot * Geo::kSlotBytes);
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)bytes);
+            __syncwarp();
+            ++seq;
+        };
+        auto load_k = [&](const AttnWalk& k, int kt, int id) {
+            const int key0 = kt * kAttnKeys;
+            const int boxes = min(kboxes, (k.t.hi - key0 + kb - 1) >> row_bits);
+            for (int s = 0; s < kKS && ok; ++s) {
+                uint32_t bar = 0, dst = 0;
+                claim(bar, dst, boxes * kb * kDK * 2);
+                if (!ok) break;
+                for (int o0 = 0; o0 < boxes * (kDK / 64); o0 += 32) {
+                    const int o = o0 + lane, box = o / (kDK / 64), panel = o % (kDK / 64);
+                    const int block = __shfl_sync(0xFFFFFFFFu, id, box & 31);
+                    if (o < boxes * (kDK / 64))
+                        tma_load_4d(dst + panel * (kAttnKeys * 128) + box * kb * 128, &a.kmap, s * kDK + panel * 64,
+                                    (key0 + box * kb) & page_mask, k.h, block, bar);
+                }
+            }
+        };
+        auto load_v = [&](const AttnWalk& k, int kt, int id) {
+            for (int s = 0; s < kVS && ok; ++s) {
+                const int key0 = kt * kAttnKeys + s * kVK;
+                const int boxes = max(0, min(kVK / vb, (k.t.hi - key0 + vb - 1) >> vrow_bits));
+                uint32_t bar = 0, dst = 0;
+                claim(bar, dst, boxes * vb * D * 2);
+                if (!ok) break;
+                for (int o0 = 0; o0 < boxes * (D / 64); o0 += 32) {
+                    const int o = o0 + lane, box = o / (D / 64), panel = o % (D / 64);
+                    const int block = __shfl_sync(0xFFFFFFFFu, id, ((s * kVK + box * vb) >> row_bits) & 31);
+                    if (o < boxes * (D / 64))
+                        tma_load_4d(dst + panel * (kVK * 128) + box * vb * 128, &a.vmap, panel * 64,
+                                    (key0 + box * vb) & page_mask, k.h, block, bar);
+                }
+            }
+        };
+        for (; w.more() && ok; w.next(a)) {
+            const int n = w.tiles();
+            if (n == 0) continue;
+            int id = ids(w, w.key_tile(0)), next_id = -1;
+            if (n > 1) next_id = ids(w, w.key_tile(1));
+            load_k(w, w.key_tile(0), id);
+            for (int j = 0; j < n && ok; ++j) {
+                const int after = j + 2 < n ? ids(w, w.key_tile(j + 2)) : -1;
+                if (j + 1 < n) load_k(w, w.key_tile(j + 1), next_id);
+                if (ok) load_v(w, w.key_tile(j), id);
+                id = next_id;
+                next_id = after;
+            }
+        }
+        if (lane == 0) {
+            flags[1] = seq;
+            __threadfence_block();
+            flags[2] = 1;
+        }
+    } else if (warp == kAttnMma) {
+        // ------------------------------------------------------------ MMA issuer
+        constexpr uint32_t kIdescS = attn_idesc(BF16, kAttnKeys, false), kIdescO = attn_idesc(BF16, D, true);
+        const bool leader = elect_one();
+        const uint32_t qbase = smem_u32(qmem), ring0 = smem_u32(ring);
+        int seq = 0, g = 0, seg = 0;
+        bool ok = flags[0] == 0;
+        auto score = [&](int gt) {         // S of the tile with global count gt
+            const uint32_t s_col = tmem + kAttnSCol + kAttnKeys * (gt & 1);
+            for (int s = 0; s < kKS; ++s) {
+                const int slot = seq % kSlots;
+                ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(full0 + 8 * slot, (seq / kSlots) & 1, flags, a.dev_err, wait_ns));
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t kbase = ring0 + slot * Geo::kSlotBytes;
+#pragma unroll
+                for (int i = 0; i < kDK / 16; ++i) {
+                    const uint64_t ad = smem_desc_sw128(qbase + (s * (kDK / 64) + i / 4) * (kAttnRows * 128) + 32 * (i % 4));
+                    const uint64_t bd = smem_desc_sw128(kbase + (i / 4) * (kAttnKeys * 128) + 32 * (i % 4));
+                    tc_mma_ss(s_col, ad, bd, kIdescS, (s > 0 || i > 0) ? 1u : 0u, leader);
+                }
+                tc_commit(empty0 + 8 * slot, leader);
+                ++seq;
+            }
+            tc_commit(sfull0 + 8 * (gt & 1), leader);
+        };
+        for (; w.more() && ok; w.next(a)) {
+            const int n = w.tiles();
+            if (n == 0) continue;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(qfull, seg & 1, flags, a.dev_err, wait_ns));
+            if (!ok) break;
+            score(g);
+            for (int j = 0; j < n && ok; ++j, ++g) {
+                if (j + 1 < n) score(g + 1);
+                if (!ok) break;
+                if (j == n - 1) tc_commit(qfree, leader);
+                const int buf = g & 1;
+                ok = mbar_wait(pready0 + 8 * buf, (g >> 1) & 1, flags, a.dev_err, wait_ns);
+                if (ok && j == 0 && seg > 0) ok = mbar_wait(ofree, (seg - 1) & 1, flags, a.dev_err, wait_ns);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint32_t p_col = tmem + kAttnSCol + kAttnKeys * buf;
+                for (int s = 0; s < kVS; ++s) {
+                    const int slot = seq % kSlots;
+                    ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(full0 + 8 * slot, (seq / kSlots) & 1, flags, a.dev_err, wait_ns));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t vbase = ring0 + slot * Geo::kSlotBytes;
+#pragma unroll
+                    for (int i = 0; i < kVK / 16; ++i) {
+                        const int key = s * kVK + 16 * i;    // its half of P starts at column 64 * (key / 64)
+                        const uint32_t ac = p_col + 64 * (key / 64) + (key % 64) / 2;
+                        tc_mma(tmem, ac, smem_desc_mn128(vbase + i * 2048, kVK * 128), kIdescO,
+                               (j > 0 || s > 0 || i > 0) ? 1u : 0u, leader);
+                    }
+                    tc_commit(empty0 + 8 * slot, leader);
+                    ++seq;
+                }
+                if (ok) tc_commit(pvdone0 + 8 * buf, leader);
+            }
+            ++seg;
+        }
+        // every MMA has completed before TMEM can be freed
+        tc_commit(done, leader);
+        mbar_wait_drain(done, 0, kDrainNs);
+    } else if (warp >= kAttnLoader) {
+        // ------------------------------------------------------------ query rows
+        const int lt = tid - kAttnLoader * 32;
+        int seg = 0;
+        bool ok = flags[0] == 0;
+        for (; w.more() && ok; w.next(a)) {
+            if (w.tiles() == 0) continue;
+            if (seg > 0) ok = mbar_wait(qfree, (seg - 1) & 1, flags, a.dev_err, wait_ns);
+            if (!ok) break;
+            const uint32_t q0 = smem_u32(qmem);
+            for (int i = lt; i < w.t.rows * (D / 8); i += kAttnLoaderThreads) {
+                const int row = i / (D / 8), c = i % (D / 8), at = w.t.row0 + row;
+                const int t = at / a.group, hq = w.h * a.group + (at - t * a.group);
+                cp_async16(q0 + (c / 8) * (kAttnRows * 128) + row * 128 + (((c % 8) ^ (row & 7)) << 4),
+                           a.q + (w.rq.q0 + t) * a.q_stride + hq * D + c * 8);
+            }
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            mbar_arrive(qfull);
+            ++seg;
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        // pv_done of a buffer may be waited for in any of its phases or in none: S of tile g is full
+        // only after the products of tile g - 2 and all before it (one thread commits both).
+        // These warps never leave their loops early: after an abort the waits return at once, and
+        // the pairs' barriers stay matched.
+        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
+        const float c = a.scale_log2;
+        int g = 0, seg = 0, seq = 0;
+        int4 split0 = make_int4(-1, 0, 0, 0);
+        int split_last = 0;
+        for (; w.more(); w.next(a)) {
+            const AttnTile& t = w.t;
+            const int n = w.tiles();
+            const bool whole = w.k0 == 0 && w.k1 == w.units;
+            const bool valid = row < t.rows;
+            const int at = t.row0 + min(row, t.rows - 1);
+            const int token = at / a.group, hq = w.h * a.group + at - token * a.group;
+            if (w.k0 == 0 && !whole) {
+                // the last unit's owner: ranges begin at floor(total c / blocks)
+                const long long last = w.at + w.units - 1;
+                split0 = make_int4(w.r, w.h, w.qt, t.rows);
+                split_last = (int)(((last + 1) * blocks - 1) / total);
+            }
+            uint16_t* const orow = a.out + (w.rq.q0 + token) * a.out_stride + (long long)hq * D + half * (D / 2);
+            if (n == 0) {                  // no key is seen
+                if (valid)
+#pragma unroll
+                    for (int i = 0; i < D / 2; i += 8) *reinterpret_cast<uint4*>(orow + i) = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            const bool active = 32 * quarter < t.rows;
+            const int p = t.p0 + token;
+            const int jlo = a.window > 0 ? p - a.window + 1 : 0;
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int j = 0; j < n; ++j, ++g) {
+                const int buf = g & 1, key0 = w.key_tile(j) * kAttnKeys;
+                const uint32_t s_col = lane_base + kAttnSCol + kAttnKeys * buf + 64 * half;
+                ok = mbar_wait(sfull0 + 8 * buf, (g >> 1) & 1, flags, a.dev_err, wait_ns);
+                tc_fence_after();
+                if (active) {
+                    uint32_t v[64];
+                    tmem_ld32(s_col, v);
+                    tmem_ld32(s_col + 32, v + 32);
+                    tmem_wait_ld();
+                    if (key0 + kAttnKeys - 1 > t.pf || (a.window > 0 && key0 < t.pl - a.window + 1)) {
+                        const int kk = key0 + 64 * half, above = p - kk, below = jlo - kk, sink = a.sinks - kk;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i > above || (i < below && i >= sink)) v[i] = 0xFF800000u;
+                    }
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+                    float* const x = red + (g & 1) * 256;
+                    x[half * 128 + row] = mx;
+                    named_bar_sync(1 + quarter, 64);
+                    mx = fmaxf(fmaxf(mx, x[(half ^ 1) * 128 + row]), m);
+                    // keep the old maximum while the new one is within 2^kAttnLazy of it
+                    const bool grow = valid && mx > m && !((mx - m) * c <= kAttnLazy);
+                    if (j > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+                        const float f = grow ? exp2_fast((m - mx) * c) : 1.f;
+                        mbar_wait(pvdone0 + 8 * (buf ^ 1), ((g - 1) >> 1) & 1, flags, a.dev_err, wait_ns);
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < D / 2; i += 32) {
+                            uint32_t o[32];
+                            const uint32_t col = lane_base + half * (D / 2) + i;
+                            tmem_ld32(col, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(col, o);
+                        }
+                        l *= f;
+                    }
+                    if (grow) m = mx;
+                    const float off = m == -INFINITY ? 0.f : -m * c;
+                    uint32_t pk[32];
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        const float e0 = exp2_fast(fmaf(__uint_as_float(v[i]), c, off));
+                        const float e1 = exp2_fast(fmaf(__uint_as_float(v[i + 1]), c, off));
+                        s0 += e0;
+                        s1 += e1;
+                        pk[i / 2] = pack16<BF16>(e0, e1);
+                    }
+                    l += s0 + s1;
+                    tmem_st32(s_col, pk);
+                    tmem_wait_st();
+                }
+                // V rows that no row sees: zeros
+                // (seen are the keys below the sinks and lo .. hi - 1)
+                if (key0 + kAttnKeys > t.hi || min(t.lo, key0 + kAttnKeys) > max(key0, a.sinks)) {
+                    // the V slots of tile j: after K of the first tile, each tile's V follows the next tile's K
+                    // (the tile before is waited for first: a slot's barrier may be one fill behind otherwise)
+                    if (j > 0) ok = mbar_wait(pvdone0 + 8 * (buf ^ 1), ((g - 1) >> 1) & 1, flags, a.dev_err, wait_ns) && ok;
+                    const int v0 = seq + kKS + j * (kKS + kVS) + (j + 1 < n ? kKS : 0);
+                    for (int s = 0; s < kVS; ++s)
+                        ok = mbar_wait(full0 + 8 * ((v0 + s) % kSlots), ((v0 + s) / kSlots) & 1, flags, a.dev_err, wait_ns) && ok;
+                    if (ok) {
+                        for (int i = tid; i < kAttnKeys * (D / 8); i += kAttnSoftmaxWarps * 32) {
+                            const int key = i / (D / 8), ch = i % (D / 8), abs = key0 + key;
+                            if (abs >= t.hi || (abs < t.lo && abs >= a.sinks)) {
+                                uint8_t* const slot = ring + ((v0 + key / kVK) % kSlots) * Geo::kSlotBytes;
+                                *reinterpret_cast<uint4*>(slot + (ch / 8) * (kVK * 128) + (key % kVK) * 128 + (ch % 8) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_if(pready0 + 8 * buf, lane == 0);
+            }
+            seq += n * (kKS + kVS);
+            // the tile's rows: finished, or a partial with its maximum and sum
+            ok = mbar_wait(pvdone0 + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, flags, a.dev_err, wait_ns);
+            tc_fence_after();
+            if (active) {
+                float* const x = red + (g & 1) * 256;
+                x[half * 128 + row] = l;
+                named_bar_sync(1 + quarter, 64);
+                l += x[(half ^ 1) * 128 + row];
+                named_bar_sync(1 + quarter, 64);   // the next tile's maxima use the same buffer
+                const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
+                float* const prow = a.part + ((size_t)slot * kAttnRows + row) * D + half * (D / 2);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int i = 0; i < D / 2; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(lane_base + half * (D / 2) + i, o);
+                    tmem_wait_ld();
+                    if (valid && ok) {
+                        if (whole) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                uint4 u;
+                                u.x = pack16<BF16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                                u.y = pack16<BF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                                u.z = pack16<BF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                                u.w = pack16<BF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                                *reinterpret_cast<uint4*>(orow + i + e) = u;
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4*>(prow + i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        }
+                    }
+                }
+                if (!whole && valid && half == 0) a.ml[slot * kAttnRows + row] = make_float2(m, l);
+            }
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_if(ofree, lane == 0);
+            ++seg;
+        }
+        if (tid == 0) {
+            a.splits[2 * blockIdx.x] = split0;
+            a.splits[2 * blockIdx.x + 1] = make_int4(split_last, 0, 0, 0);
+        }
+    }
+
+    if (flags[0] && tid == 0) {
+        // Aborted: wait (bounded) for the producer to stop, then for its last copy into each slot.
+        const uint64_t t0 = global_timer_ns();
+        while (!flags[2] && global_timer_ns() - t0 < 2 * kDrainNs) {
+        }
+        const int issued = flags[1];
+        for (int j = issued > kSlots ? issued - kSlots : 0; j < issued; ++j)
+            mbar_wait_drain(full0 + 8 * (j % kSlots), (j / kSlots) & 1, kDrainNs);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- the join
+
+constexpr int kJoinWarps = 8;
+constexpr int kJoinRowsY = 16;     // blocks of a split's rows
+
+// Adds the partials of the query tiles that were split over several blocks, in block order:
+// O = sum_i 2^(c (m_i - M)) O_i / sum_i 2^(c (m_i - M)) l_i. Block (x, y) takes rows y, y + 16, ...
+// of the tile that block x of the attention kernel opened; its warps share the partials. The same
+// blocks write zeros to the output rows past the last request's.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+    __shared__ float acc[kJoinWarps][D];
+    __shared__ float sums[kJoinWarps];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kPer = D / 32;       // columns of a lane
+    const int4 s = a.splits[2 * blockIdx.x];
+    if (s.x >= 0) {
+        const int last = a.splits[2 * blockIdx.x + 1].x, count = last - (int)blockIdx.x + 1;
+        const AttnReq rq = attn_req(a, s.x);
+        const float c = a.scale_log2;
+        auto slot = [&](int i) { return 2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0); };
+        for (int row = blockIdx.y; row < s.w; row += kJoinRowsY) {
+            float m = -INFINITY;
+            for (int i = lane; i < count; i += 32) m = fmaxf(m, a.ml[slot(i) * kAttnRows + row].x);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            if (m == -INFINITY) m = 0.f;
+            float o[kPer], l = 0.f;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+            for (int i = warp; i < count; i += kJoinWarps) {
+                const float2 ml = a.ml[slot(i) * kAttnRows + row];
+                const float f = exp2_fast((ml.x - m) * c);
+                const float* src = a.part + ((size_t)slot(i) * kAttnRows + row) * D;
+                l += f * ml.y;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) o[e] += f * src[e * 32 + lane];
+            }
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[warp][e * 32 + lane] = o[e];
+            if (lane == 0) sums[warp] = l;
+            __syncthreads();
+            if (tid < D / 2) {
+                float x = 0.f, y = 0.f, total = 0.f;
+#pragma unroll
+                for (int i = 0; i < kJoinWarps; ++i) {
+                    x += acc[i][2 * tid];
+                    y += acc[i][2 * tid + 1];
+                    total += sums[i];
+                }
+                const float inv = total == 0.f ? 0.f : 1.f / total;
+                const int at = s.z * kAttnRows + row, token = at / a.group, hq = s.y * a.group + at - token * a.group;
+                reinterpret_cast<uint32_t*>(a.out + (rq.q0 + token) * a.out_stride + (long long)hq * D)[tid] =
+                    pack16<BF16>(x * inv, y * inv);
+            }
+            __syncthreads();
+        }
+    }
+    const int end = min(max(a.q_start[a.R], 0), a.tokens), chunks = a.heads * a.group * (D / 8);
+    for (int t = end + blockIdx.x + gridDim.x * blockIdx.y; t < a.tokens; t += gridDim.x * gridDim.y)
+        for (int i = tid; i < chunks; i += kJoinWarps * 32)
+            reinterpret_cast<uint4*>(a.out + t * a.out_stride)[i] = make_uint4(0, 0, 0, 0);
+}
+
+}  // namespace nq

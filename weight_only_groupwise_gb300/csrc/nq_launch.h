@@ -7,6 +7,7 @@
 #include "nq_tc.cuh"
 
 struct nq_group;
+struct nq_kv_cache;
 
 namespace nq {
 
@@ -18,6 +19,8 @@ bool encode_x_map(CUtensorMap* map, const void* X, int T, int K, int TP);
 bool tensor_maps_available();
 bool encode_weight_maps(CUtensorMap* wmap, CUtensorMap* smap, const void* W, const void* S, int bits, int K, int N,
                         int TP);
+// The tensor map of a paged cache's K or V tensor (16-bit elements, boxes of min(page, rows) keys).
+bool encode_kv_map(CUtensorMap* map, void* base, const nq_kv_cache* c, bool bf16, int rows);
 cudaError_t launch_tc_proj(int bits, const TcArgs& a, cudaStream_t stream, bool pdl);
 cudaError_t launch_tc_proj_fp4(const TcArgs& a, cudaStream_t stream, bool pdl);
 // The two launches of a SwiGLU block (mode kTcOutGate, then kTcOutSwiglu), 4- or 5-bit codes

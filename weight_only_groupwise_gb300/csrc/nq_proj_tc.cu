@@ -5,6 +5,7 @@
 
 #include <mutex>
 
+#include "nq.h"
 #include "nq_launch.h"
 
 namespace nq {
@@ -75,6 +76,22 @@ bool encode_weight_maps(CUtensorMap* wmap, CUtensorMap* smap, const void* W, con
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
            fn(smap, CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<void*>(S), sdims, sstr, sbox, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One of a paged cache's two tensors as a 4-D map {dim, page rows, heads, blocks} with the
+// cache's own strides; a box is 64 columns (a 128-byte swizzled row) of min(page, rows) keys of
+// one head and block. A block id outside the cache reads as zeros.
+bool encode_kv_map(CUtensorMap* map, void* base, const nq_kv_cache* c, bool bf16, int rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)c->dim, (cuuint64_t)c->page, (cuuint64_t)c->heads, (cuuint64_t)c->num_blocks};
+    const cuuint64_t strides[3] = {(cuuint64_t)c->row_stride * 2, (cuuint64_t)c->head_stride * 2,
+                                   (cuuint64_t)c->block_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(c->page < rows ? c->page : rows), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -23,6 +23,13 @@ class NqGroup(ctypes.Structure):
     _fields_ = [("Wq", ctypes.c_void_p), ("S", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("N", ctypes.c_int)]
 
 
+class NqKvCache(ctypes.Structure):
+    """struct nq_kv_cache of include/nq.h."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("block_stride", ctypes.c_longlong),
+                ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong), ("num_blocks", ctypes.c_int),
+                ("page", ctypes.c_int), ("heads", ctypes.c_int), ("dim", ctypes.c_int)]
+
+
 class NqError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(msg)
@@ -106,6 +113,14 @@ def lib() -> ctypes.CDLL:
             getattr(L, f).restype = I
         L.nq_program_destroy.argtypes = [P]
         L.nq_program_destroy.restype = None
+        LL, F = ctypes.c_longlong, ctypes.c_float
+        L.nq_page_tables.argtypes = [P, P, I, P, I, P, I, P, LL, I, P, P, P, P, I, P, P]
+        L.nq_kv_append.argtypes = [P, LL, P, LL, P, I, P, P]
+        L.nq_attn_paged.argtypes = [P, LL, P, P, LL, I, P, P, I, I, I, F, I, I, I, P, LL, P]
+        L.nq_attn_reserve.argtypes = []
+        L.nq_sample.argtypes = [P, I, LL, P, LL, I, I, P, P, P, P, P, P]
+        for f in ("nq_sample", "nq_page_tables", "nq_kv_append", "nq_attn_paged", "nq_attn_reserve"):
+            getattr(L, f).restype = I
         for f in ("nq_pack_q4", "nq_pack_q5", "nq_gemm_q4", "nq_gemm_q5", "nq_gemm_q4_noalloc", "nq_swiglu_q4",
                   "nq_swiglu_q5", "nq_reserve", "nq_device_error", "nq_plan_info", "nq_plan_cluster_info"):
             getattr(L, f).restype = I
@@ -438,6 +453,162 @@ class Program:
             pass
 
 
+# ---------------------------------------------------------------- serving step
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _dev(t, name: str, dtype, ndim: int) -> torch.Tensor:
+    """A CUDA tensor of this type and rank whose last dimension lies together."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.dim() != ndim or (
+            t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel() > 0):
+        raise ValueError(f"{name} must be a {ndim}-d CUDA tensor of {dtype}, its last dimension contiguous")
+    return t
+
+
+def _flat(t, name: str, dtype, n: int) -> torch.Tensor:
+    """A contiguous 1-d CUDA tensor of n elements."""
+    _dev(t, name, dtype, 1)
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
+    return t
+
+
+def _token_rows(t, name: str, dtype, heads: int, dim: int) -> int:
+    """Checks a [tokens][heads][dim] tensor whose token rows lie together; returns the stride
+    between tokens."""
+    _dev(t, name, dtype, 3)
+    if t.shape[1] != heads or t.shape[2] != dim or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must be [tokens][{heads}][{dim}] with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _kv_cache(k_cache, v_cache) -> NqKvCache:
+    """The paged cache given as two [num_blocks][page][heads][dim] tensors of equal strides (for a
+    cache stored [num_blocks][heads][page][dim], pass cache.transpose(1, 2))."""
+    if k_cache.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("k_cache must be bfloat16 or float16")
+    _dev(k_cache, "k_cache", k_cache.dtype, 4)
+    _dev(v_cache, "v_cache", k_cache.dtype, 4)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have one shape and the same strides")
+    blocks, page, heads, dim = k_cache.shape
+    bs, rs, hs, _ = k_cache.stride()
+    # the stride of a dimension of one element means nothing
+    return NqKvCache(k_cache.data_ptr(), v_cache.data_ptr(), bs if blocks > 1 else max(bs, dim), rs,
+                     hs if heads > 1 else dim, blocks, page, heads, dim)
+
+
+def _rows2(t, name: str, rows: int) -> int:
+    """The stride between the rows of an int32 [rows][n] table."""
+    _dev(t, name, torch.int32, 2)
+    if t.shape[0] != rows:
+        raise ValueError(f"{name} must have {rows} rows, not {t.shape[0]}")
+    return t.stride(0) if rows > 1 else max(t.shape[1], 1)
+
+
+def page_tables(lens, new_lens, free_blocks, num_free, block_table, page: int, max_tokens: int, out=None, stream=None):
+    """Block tables and slot maps of a step from the requests' lengths (nq_page_tables): extends
+    block_table in place from the free list and returns (q_start [R+1], kv_lens [R],
+    positions [max_tokens], slots [max_tokens], counts [3]: tokens, blocks taken, requests
+    refused). All tensors int32 on the GPU (slots int64); `out`: the five outputs, to be reused."""
+    i32 = torch.int32
+    R = lens.numel()
+    _flat(lens, "lens", i32, R)
+    _flat(new_lens, "new_lens", i32, R)
+    _dev(free_blocks, "free_blocks", i32, 1)
+    _flat(num_free, "num_free", i32, 1)
+    stride = _rows2(block_table, "block_table", R)
+    if out is None:
+        dev = lens.device
+        out = (torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev),
+               torch.empty(max_tokens, dtype=i32, device=dev), torch.empty(max_tokens, dtype=torch.int64, device=dev),
+               torch.empty(3, dtype=i32, device=dev))
+    q_start, kv_lens, positions, slots, counts = out
+    _flat(q_start, "q_start", i32, R + 1)
+    _flat(kv_lens, "kv_lens", i32, R)
+    _flat(positions, "positions", i32, max_tokens)
+    _flat(slots, "slots", torch.int64, max_tokens)
+    _flat(counts, "counts", i32, 3)
+    _check(lib().nq_page_tables(lens.data_ptr(), new_lens.data_ptr(), R, free_blocks.data_ptr(), free_blocks.numel(),
+                                num_free.data_ptr(), page, block_table.data_ptr(), stride, block_table.shape[1],
+                                q_start.data_ptr(), kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+                                max_tokens, counts.data_ptr(), _stream(stream)))
+    return out
+
+
+def kv_append(k, v, slots, k_cache, v_cache, stream=None) -> None:
+    """Store new keys and values [tokens][heads][dim] at slots [tokens] (int64; block * page + row,
+    -1 for none) of the paged cache [num_blocks][page][heads][dim] (nq_kv_append)."""
+    c = _kv_cache(k_cache, v_cache)
+    ks = _token_rows(k, "k", k_cache.dtype, c.heads, c.dim)
+    vs = _token_rows(v, "v", k_cache.dtype, c.heads, c.dim)
+    tokens = k.shape[0]
+    if v.shape[0] != tokens:
+        raise ValueError("k and v must have the same number of tokens")
+    _flat(slots, "slots", torch.int64, tokens)
+    _check(lib().nq_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), tokens, ctypes.byref(c),
+                              _stream(stream)))
+
+
+def attn_paged(q, k_cache, v_cache, block_table, q_start, kv_lens, scale: float = None, window: int = 0,
+               sinks: int = 0, out=None, stream=None):
+    """Causal attention of a step's new tokens q [tokens][q_heads][dim] over the paged cache
+    [num_blocks][page][heads][dim] (nq_attn_paged): block_table [R][max_blocks], q_start [R+1]
+    and kv_lens [R] (int32, as page_tables gives them). scale defaults to dim ** -0.5; window > 0
+    limits a token to the last `window` keys and the first `sinks`. Returns out [tokens][q_heads][dim]."""
+    c = _kv_cache(k_cache, v_cache)
+    dt = k_cache.dtype
+    _dev(q, "q", dt, 3)
+    tokens, heads, dim = q.shape
+    if dim != c.dim:
+        raise ValueError(f"q has head dimension {dim}, the cache {c.dim}")
+    qs = _token_rows(q, "q", dt, heads, dim)
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=dt, device=q.device)
+    os_ = _token_rows(out, "out", dt, heads, dim)
+    if out.shape[0] != tokens:
+        raise ValueError("out must have q's shape")
+    R = kv_lens.numel()
+    _flat(kv_lens, "kv_lens", torch.int32, R)
+    _flat(q_start, "q_start", torch.int32, R + 1)
+    stride = _rows2(block_table, "block_table", R)
+    _check(lib().nq_attn_paged(q.data_ptr(), qs, ctypes.byref(c), block_table.data_ptr(), stride, block_table.shape[1],
+                               q_start.data_ptr(), kv_lens.data_ptr(), R, tokens, heads,
+                               dim ** -0.5 if scale is None else scale, window, sinks, _DTYPES[dt], out.data_ptr(), os_,
+                               _stream(stream)))
+    return out
+
+
+def attn_reserve() -> None:
+    """Allocate the attention workspace now (before stream capture)."""
+    _check(lib().nq_attn_reserve())
+
+
+def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
+    """The next token of each row of logits [B][V] (bfloat16, float16 or float32) with the row's
+    temperature, top_k, top_p and min_p ([B] tensors, None for none) and noise [B][V] (float32,
+    independent Exp(1) variates: `torch.empty_like(...).exponential_()`); see nq_sample. Returns
+    int32 tokens [B], -1 for a row without a candidate."""
+    if logits.dtype not in _DTYPES:
+        raise ValueError("logits must be bfloat16, float16 or float32")
+    _dev(logits, "logits", logits.dtype, 2)
+    _dev(noise, "noise", torch.float32, 2)
+    if noise.shape != logits.shape:
+        raise ValueError("noise must have the shape of logits")
+    B, V = logits.shape
+    if out is None:
+        out = torch.empty(B, dtype=torch.int32, device=logits.device)
+    _flat(out, "out", torch.int32, B)
+    settings = []
+    for t, name in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
+        settings.append(None if t is None else
+                        _flat(t, name, torch.int32 if name == "top_k" else torch.float32, B).data_ptr())
+    _check(lib().nq_sample(logits.data_ptr(), _DTYPES[logits.dtype], logits.stride(0) if B > 1 else V, noise.data_ptr(),
+                           noise.stride(0) if B > 1 else V, B, V, *settings, out.data_ptr(), _stream(stream)))
+    return out
+
+
 # ---------------------------------------------------------------- runtime / plan
 
 def reserve(T_max: int, K_max: int, N_max: int) -> None:
@@ -542,3 +713,5 @@ nq_pack_fp4, nq_gemm_fp4, nq_dequant_fp4_debug = pack_fp4, gemm_fp4, dequant_fp4
 nq_swiglu_fp4 = swiglu_fp4
 nq_reserve, nq_device_error, nq_shutdown, nq_wait_limit = reserve, device_error, shutdown, wait_limit
 nq_plan_info, nq_plan_segments = plan_info, plan_segments
+nq_page_tables, nq_kv_append, nq_attn_paged, nq_attn_reserve = page_tables, kv_append, attn_paged, attn_reserve
+nq_sample = sample
