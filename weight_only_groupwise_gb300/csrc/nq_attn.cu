@@ -29,7 +29,7 @@ cudaError_t attn_launch(const AttnArgs& a, int sms, cudaStream_t stream, bool pd
     }
     cudaError_t e = step_launch(kern, dim3(sms), dim3(kAttnThreads), AttnGeo<D>::kSmem, stream, pdl, 1, a);
     if (e != cudaSuccess) return e;
-    return step_launch(attn_join_kernel<D, BF16>, dim3(sms, kJoinRowsY), dim3(kJoinWarps * 32), 0, stream, pdl, 1, a);
+    return step_launch(attn_join_kernel<D, BF16>, dim3(sms, kJoinBlocksY), dim3(kJoinThreads), 0, stream, pdl, 1, a);
 }
 
 template <bool BF16>
@@ -102,12 +102,12 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     if (st != NQ_OK) return st;
 
     alignas(64) AttnArgs a;
-    if (!encode_kv_map(&a.kmap, cache->K, cache, dtype == NQ_BF16, kAttnKeys) ||
+    if (!encode_q_map(&a.qmap, q, q_stride, cache->dim, q_heads, tokens, q_heads / cache->heads,
+                      kAttnRows / (q_heads / cache->heads), dtype == NQ_BF16) ||
+        !encode_kv_map(&a.kmap, cache->K, cache, dtype == NQ_BF16, kAttnKeys) ||
         !encode_kv_map(&a.vmap, cache->V, cache, dtype == NQ_BF16, cache->dim == 256 ? 64 : kAttnKeys))
         return NQ_ERR_CUDA;
-    a.q = static_cast<const uint16_t*>(q);
     a.out = static_cast<uint16_t*>(out);
-    a.q_stride = q_stride;
     a.out_stride = out_stride;
     a.table = block_table;
     a.table_stride = table_stride;
@@ -117,6 +117,7 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     a.tokens = tokens;
     a.heads = cache->heads;
     a.group = q_heads / cache->heads;
+    a.tile_tokens = kAttnRows / a.group;
     a.page_shift = 0;
     while ((1 << a.page_shift) < cache->page) ++a.page_shift;
     a.max_keys = max_blocks * cache->page;

@@ -6,9 +6,10 @@
 // j > p - W or j < sinks. One pass over the keys with the running maximum and sum of the
 // softmax, on the fifth-generation tensor cores.
 //
-// Tiles. A query tile is 128 rows of one (request, KV head): row i is token i / G, head i % G, so
-// the G query heads of a KV head share every key that is loaded, whatever the number of new
-// tokens (one, a verify round's 8, a prompt chunk's thousands). A key tile is 128 keys, cut at
+// Tiles. A query tile is the G query heads of floor(128 / G) tokens of one (request, KV head), up
+// to 128 rows: row i is token i / G, head i % G, so the heads share every key that is loaded,
+// whatever the number of new tokens (one, a verify round's 8, a prompt chunk's thousands), and
+// a tile is one box of q as [token][head][dim]. A key tile is 128 keys, cut at
 // multiples of 128, so a page (16..256 keys) never straddles two tiles unless it holds both.
 // Keys that no row of the query tile sees are not loaded, tile by tile.
 //
@@ -19,7 +20,7 @@
 // result does not depend on timing. Every block finds its range by itself from the lengths on the
 // device: no host copy of the lengths, no plan to keep, no waits between blocks.
 //
-// Roles of a block's 12 warps (one block per SM):
+// Roles of a block's 11 warps (one block per SM):
 //   * warps 0..7 -- softmax: thread = row (TMEM lane) and half of the tile's 128 columns. The two
 //     halves of a row exchange maxima through shared memory. The accumulator is rescaled only
 //     when a row's maximum grows by more than 2^8 in the exponential's argument (p <= 256 stays
@@ -32,8 +33,8 @@
 //   * warp 9 -- MMA issuer: S = Q K^T (both from shared memory), O += P V (P from TMEM, V from
 //     shared memory as the N-major operand). S is double buffered: the product of tile j + 1 is
 //     issued before that of P of tile j, so that the tensor cores work during the softmax.
-//   * warps 10, 11 -- the query tile's rows into shared memory (cp.async: rows of a tile are G-wide
-//     runs of heads at a token stride, not a box).
+//   * warp 10 -- the query tile into shared memory, one TMA box a 64-column panel. Rows past the
+//     tile's own (other requests' tokens, or zeros) are computed and dropped.
 // TMEM: O in columns 0..dim-1, the S buffers (P over them) in columns 256.. and 384...
 //
 // Rows of V that no row of the tile sees (past the last key, before a window) may hold anything,
@@ -51,10 +52,9 @@
 namespace nq {
 
 constexpr int kAttnKeys = 128;                    // keys of a tile
-constexpr int kAttnThreads = 12 * 32;
+constexpr int kAttnThreads = 11 * 32;
 constexpr int kAttnSoftmaxWarps = 8;
 constexpr int kAttnProducer = 8, kAttnMma = 9, kAttnLoader = 10;
-constexpr int kAttnLoaderThreads = 64;
 constexpr int kAttnMaxRequests = 8192;            // the scan's 8 bytes a request fit the tile buffers
 constexpr int kAttnSCol = 256;                    // TMEM column of the first S buffer
 constexpr int kAttnCtrlBytes = 3072;
@@ -78,19 +78,19 @@ struct AttnGeo {
 };
 
 struct AttnArgs {
-    CUtensorMap kmap, vmap;
-    const uint16_t* q;
+    CUtensorMap qmap, kmap, vmap;      // qmap: {dim, query heads, tokens}, boxes of 64 x group x tile_tokens
     uint16_t* out;
-    long long q_stride, out_stride;    // between tokens, elements
+    long long out_stride;              // between tokens, elements
     const int* table;
     long long table_stride;
     const int* q_start;
     const int* kv_lens;
     int R, tokens, heads, group;       // heads: KV heads; group: query heads per KV head
+    int tile_tokens;                   // tokens of a query tile: 128 / group
     int page_shift, max_keys;
     int window, sinks;                 // window 0: none, and then no sinks
     float scale_log2;                  // scale x log2(e)
-    float* part;                       // [2 blocks][128][D] partial accumulators
+    float* part;                       // [2 blocks][D][128 rows] partial accumulators
     float2* ml;                        // [2 blocks][128] (maximum, sum)
     int4* splits;                      // [blocks][2] split records
     int* dev_err;
@@ -112,40 +112,39 @@ __device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, int r) {
     return q;
 }
 
-// A query tile: its rows, and the key tiles it reads, kt(i) = i < first ? i : i + skip.
+// A query tile: its tokens, and the key tiles it reads, kt(i) = i < first ? i : i + skip.
 struct AttnTile {
-    int row0, rows;
-    int p0;                            // position of the request's first new token
-    int pf, pl;                        // positions of the first and the last row
+    int token0, rows;                  // first token in the request, rows (tokens x group)
+    int pf, pl;                        // positions of the first and the last token
     int hi, lo;                        // keys seen by some row: [lo, hi) and the sinks
     int n, first, skip;
 };
 
+__device__ __forceinline__ int attn_tiles(const AttnArgs& a, const AttnReq& q) {
+    return (q.n + a.tile_tokens - 1) / a.tile_tokens;
+}
+
 __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, const AttnReq& q, int qt) {
     AttnTile t;
-    t.row0 = qt * kAttnRows;
-    t.rows = min(kAttnRows, q.n * a.group - t.row0);
-    t.p0 = q.kv - q.n;
-    t.pf = t.p0 + t.row0 / a.group;
-    t.pl = t.p0 + (t.row0 + t.rows - 1) / a.group;
+    t.token0 = qt * a.tile_tokens;
+    const int tokens = min(a.tile_tokens, q.n - t.token0);
+    t.rows = tokens * a.group;
+    t.pf = q.kv - q.n + t.token0;
+    t.pl = t.pf + tokens - 1;
     t.hi = max(0, t.pl + 1);
     t.lo = a.window > 0 ? min(max(0, t.pf - a.window + 1), t.hi) : 0;
     const int se = min(a.sinks, t.hi);
     const int ns = (se + kAttnKeys - 1) / kAttnKeys, lt = t.lo / kAttnKeys, ht = (t.hi + kAttnKeys - 1) / kAttnKeys;
-    if (se == 0) {
-        t.first = 0;
-        t.skip = lt;
-        t.n = ht - lt;
-    } else if (ns >= lt) {
-        t.first = 0;
-        t.skip = 0;
-        t.n = ht;
-    } else {
-        t.first = ns;
-        t.skip = lt - ns;
-        t.n = ns + ht - lt;
-    }
+    // the sinks' tiles and the window's, one range if they meet
+    t.first = se > 0 && ns < lt ? ns : 0;
+    t.skip = se == 0 || ns < lt ? lt - t.first : 0;
+    t.n = ht - t.skip;
     return t;
+}
+
+// Units of a query tile (0 past the last).
+__device__ __forceinline__ int attn_tile_units(const AttnArgs& a, const AttnReq& q, int qt, int nqt) {
+    return qt < nqt ? max(1, attn_tile(a, q, qt).n) : 0;
 }
 
 // A block's walk over its range of units: segments of query tiles. A tile that sees no key
@@ -158,13 +157,14 @@ struct AttnWalk {
     int k0, k1, units;                 // the segment: units k0..k1 of the tile's `units`
     __device__ __forceinline__ void enter(const AttnArgs& a) {
         rq = attn_req(a, r);
-        nqt = (rq.n * a.group + kAttnRows - 1) / kAttnRows;
+        nqt = attn_tiles(a, rq);
     }
     __device__ __forceinline__ void cut(int from) {
         units = max(1, t.n);
         k0 = from;
         k1 = (int)min((long long)units, from + left);
     }
+    // Whole warps call this: the lanes look for the first tile together.
     __device__ __forceinline__ void start(const AttnArgs& a, const long long* upto, long long u0, long long u1) {
         left = u1 - u0;
         at = u0;
@@ -179,17 +179,29 @@ struct AttnWalk {
         }
         r = lo;
         enter(a);
-        const long long base = r > 0 ? upto[r - 1] : 0;
-        const long long per = (upto[r] - base) / a.heads;
+        const long long base = r > 0 ? upto[r - 1] : 0, per = (upto[r] - base) / a.heads;
         h = (int)((u0 - base) / per);
-        int rem = (int)((u0 - base) - h * per);
-        for (qt = 0;; ++qt) {
-            t = attn_tile(a, rq, qt);
-            const int u = max(1, t.n);
-            if (rem < u || qt >= nqt - 1) break;
-            rem -= u;
+        long long rem = (u0 - base) - h * per;
+        const int lane = threadIdx.x & 31;
+        for (qt = 0;; qt += 32) {
+            const int u = attn_tile_units(a, rq, qt + lane, nqt);
+            long long x = u;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+                if (lane >= d) x += y;
+            }
+            const unsigned past = __ballot_sync(0xFFFFFFFFu, x > rem);
+            if (past || qt + 32 >= nqt) {
+                const int src = past ? __ffs(past) - 1 : 0;
+                rem -= __shfl_sync(0xFFFFFFFFu, x - u, src);
+                qt += src;
+                break;
+            }
+            rem -= __shfl_sync(0xFFFFFFFFu, x, 31);
         }
-        cut(rem);
+        t = attn_tile(a, rq, qt);
+        cut((int)rem);
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
     __device__ __forceinline__ void next(const AttnArgs& a) {
@@ -218,11 +230,11 @@ struct AttnWalk {
 
 // Units of a request per KV head: all query tiles' key tiles, the warp's lanes sharing long ones.
 __device__ __forceinline__ long long attn_units(const AttnArgs& a, const AttnReq& q, bool live) {
-    const int nqt = live ? (q.n * a.group + kAttnRows - 1) / kAttnRows : 0;
+    const int nqt = live ? attn_tiles(a, q) : 0;
     long long w = 0;
-    if (nqt <= 4)
+    if (nqt <= 2)
         for (int i = 0; i < nqt; ++i) w += max(1, attn_tile(a, q, i).n);
-    unsigned big = __ballot_sync(0xFFFFFFFFu, nqt > 4);
+    unsigned big = __ballot_sync(0xFFFFFFFFu, nqt > 2);
     while (big) {
         const int src = __ffs(big) - 1;
         big &= big - 1;
@@ -230,7 +242,7 @@ __device__ __forceinline__ long long attn_units(const AttnArgs& a, const AttnReq
         s.q0 = 0;
         s.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
         s.kv = __shfl_sync(0xFFFFFFFFu, q.kv, src);
-        const int m = (s.n * a.group + kAttnRows - 1) / kAttnRows;
+        const int m = attn_tiles(a, s);
         long long v = 0;
         for (int i = threadIdx.x & 31; i < m; i += 32) v += max(1, attn_tile(a, s, i).n);
 #pragma unroll
@@ -298,6 +310,33 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+    return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Bits 0..n-1 of 64, for any n.
+__device__ __forceinline__ uint64_t low_bits(int n) {
+    return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
+}
+
 __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <bool BF16>
@@ -334,7 +373,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 64, sfull0 = empty0 + 64, pready0 = sfull0 + 16;
     const uint32_t pvdone0 = pready0 + 16, ofree = pvdone0 + 16, qfull = ofree + 8, qfree = qfull + 8, done = qfree + 8;
     volatile int* const flags = reinterpret_cast<volatile int*>(ctrl + 2048 + 256);
-    // flags: [0] abort, [1] slots issued, [2] producer done, [3] TMEM base
+    // flags: [0] abort, [1] slots issued, [2] producer done, [3] TMEM base, [4] query tiles issued (-1: not done)
     long long* const warp_sums = reinterpret_cast<long long*>(ctrl + 2048 + 256 + 64);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -350,13 +389,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             mbar_init(pvdone0 + 8 * i, 1);
         }
         mbar_init(ofree, kAttnSoftmaxWarps);
-        mbar_init(qfull, kAttnLoaderThreads);
+        mbar_init(qfull, 1);
         mbar_init(qfree, 1);
         mbar_init(done, 1);
         // the swizzled tiles need a 1024-byte base
         flags[0] = (smem_u32(attn_smem) & 1023u) != 0;
         flags[1] = 0;
         flags[2] = 0;
+        flags[4] = -1;
         if (flags[0]) atomicOr(a.dev_err, kDevErrTimeout);
         mbar_fence_init();
     }
@@ -539,27 +579,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         // every MMA has completed before TMEM can be freed
         tc_commit(done, leader);
         mbar_wait_drain(done, 0, kDrainNs);
-    } else if (warp >= kAttnLoader) {
-        // ------------------------------------------------------------ query rows
-        const int lt = tid - kAttnLoader * 32;
+    } else if (warp == kAttnLoader) {
+        // ------------------------------------------------------------ query tiles
         int seg = 0;
         bool ok = flags[0] == 0;
         for (; w.more() && ok; w.next(a)) {
             if (w.tiles() == 0) continue;
             if (seg > 0) ok = mbar_wait(qfree, (seg - 1) & 1, flags, a.dev_err, wait_ns);
             if (!ok) break;
-            const uint32_t q0 = smem_u32(qmem);
-            for (int i = lt; i < w.t.rows * (D / 8); i += kAttnLoaderThreads) {
-                const int row = i / (D / 8), c = i % (D / 8), at = w.t.row0 + row;
-                const int t = at / a.group, hq = w.h * a.group + (at - t * a.group);
-                cp_async16(q0 + (c / 8) * (kAttnRows * 128) + row * 128 + (((c % 8) ^ (row & 7)) << 4),
-                           a.q + (w.rq.q0 + t) * a.q_stride + hq * D + c * 8);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(qfull, (uint32_t)(a.tile_tokens * a.group * D * 2));
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    tma_load_3d(smem_u32(qmem) + i * (kAttnRows * 128), &a.qmap, 64 * i, w.h * a.group,
+                                w.rq.q0 + w.t.token0, qfull);
             }
-            cp_async_wait_all();
-            fence_proxy_async_smem();
-            mbar_arrive(qfull);
+            __syncwarp();
             ++seg;
         }
+        if (lane == 0) flags[4] = seg;
     } else {
         // ------------------------------------------------------------ softmax
         // pv_done of a buffer may be waited for in any of its phases or in none: S of tile g is full
@@ -569,7 +607,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
         const float c = a.scale_log2;
-        int g = 0, seg = 0, seq = 0;
+        const int row_token = row / a.group, row_head = row - row_token * a.group;
+        int g = 0, seq = 0;
         int4 split0 = make_int4(-1, 0, 0, 0);
         int split_last = 0;
         for (; w.more(); w.next(a)) {
@@ -577,15 +616,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             const int n = w.tiles();
             const bool whole = w.k0 == 0 && w.k1 == w.units;
             const bool valid = row < t.rows;
-            const int at = t.row0 + min(row, t.rows - 1);
-            const int token = at / a.group, hq = w.h * a.group + at - token * a.group;
             if (w.k0 == 0 && !whole) {
                 // the last unit's owner: ranges begin at floor(total c / blocks)
                 const long long last = w.at + w.units - 1;
                 split0 = make_int4(w.r, w.h, w.qt, t.rows);
                 split_last = (int)(((last + 1) * blocks - 1) / total);
             }
-            uint16_t* const orow = a.out + (w.rq.q0 + token) * a.out_stride + (long long)hq * D + half * (D / 2);
+            uint16_t* const orow = a.out + (w.rq.q0 + t.token0 + row_token) * a.out_stride +
+                                   (long long)(w.h * a.group + row_head) * D + half * (D / 2);
             if (n == 0) {                  // no key is seen
                 if (valid)
 #pragma unroll
@@ -593,8 +631,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                 continue;
             }
             const bool active = 32 * quarter < t.rows;
-            const int p = t.p0 + token;
-            const int jlo = a.window > 0 ? p - a.window + 1 : 0;
+            const int p = t.pf + row_token;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = 0; j < n; ++j, ++g) {
@@ -608,14 +645,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     tmem_ld32(s_col + 32, v + 32);
                     tmem_wait_ld();
                     if (key0 + kAttnKeys - 1 > t.pf || (a.window > 0 && key0 < t.pl - a.window + 1)) {
-                        const int kk = key0 + 64 * half, above = p - kk, below = jlo - kk, sink = a.sinks - kk;
+                        // the row's keys among the thread's 64, one bit each
+                        const int kk = key0 + 64 * half;
+                        uint64_t see = low_bits(p - kk + 1);
+                        if (a.window > 0) see &= ~low_bits(p - a.window + 1 - kk) | low_bits(a.sinks - kk);
+                        const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (i > above || (i < below && i >= sink)) v[i] = 0xFF800000u;
+                        for (int i = 0; i < 32; ++i) {
+                            v[i] = (s0 & (1u << i)) ? v[i] : 0xFF800000u;
+                            v[32 + i] = (s1 & (1u << i)) ? v[32 + i] : 0xFF800000u;
+                        }
                     }
-                    float mx = -INFINITY;
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+                    for (int i = 0; i < 64; i += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(v[i + e]), __uint_as_float(v[i + 4 + e])));
+                    float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     float* const x = red + (g & 1) * 256;
                     x[half * 128 + row] = mx;
                     named_bar_sync(1 + quarter, 64);
@@ -641,16 +688,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     if (grow) m = mx;
                     const float off = m == -INFINITY ? 0.f : -m * c;
                     uint32_t pk[32];
-                    float s0 = 0.f, s1 = 0.f;
+                    const uint64_t cc = pack2(__float_as_uint(c), __float_as_uint(c));
+                    const uint64_t oo = pack2(__float_as_uint(off), __float_as_uint(off));
+                    uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int i = 0; i < 64; i += 2) {
-                        const float e0 = exp2_fast(fmaf(__uint_as_float(v[i]), c, off));
-                        const float e1 = exp2_fast(fmaf(__uint_as_float(v[i + 1]), c, off));
-                        s0 += e0;
-                        s1 += e1;
+                        const float2 x2 = unpack2(fma2(pack2(v[i], v[i + 1]), cc, oo));
+                        const float e0 = exp2_fast(x2.x), e1 = exp2_fast(x2.y);
+                        sum[(i / 2) & 3] = add2(sum[(i / 2) & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
                         pk[i / 2] = pack16<BF16>(e0, e1);
                     }
-                    l += s0 + s1;
+                    const float2 s2 = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                    l += s2.x + s2.y;
                     tmem_st32(s_col, pk);
                     tmem_wait_st();
                 }
@@ -664,13 +713,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     for (int s = 0; s < kVS; ++s)
                         ok = mbar_wait(full0 + 8 * ((v0 + s) % kSlots), ((v0 + s) / kSlots) & 1, flags, a.dev_err, wait_ns) && ok;
                     if (ok) {
-                        for (int i = tid; i < kAttnKeys * (D / 8); i += kAttnSoftmaxWarps * 32) {
-                            const int key = i / (D / 8), ch = i % (D / 8), abs = key0 + key;
-                            if (abs >= t.hi || (abs < t.lo && abs >= a.sinks)) {
-                                uint8_t* const slot = ring + ((v0 + key / kVK) % kSlots) * Geo::kSlotBytes;
-                                *reinterpret_cast<uint4*>(slot + (ch / 8) * (kVK * 128) + (key % kVK) * 128 + (ch % 8) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                            }
+                        // keys b0..b1-1 of the tile lie between the sinks and the window, e0.. past the last key
+                        const int b0 = max(0, a.sinks - key0), b1 = min(kAttnKeys, t.lo - key0);
+                        const int e0 = max(0, min(kAttnKeys, t.hi - key0)), nb = max(0, b1 - b0);
+                        for (int i = tid; i < (nb + kAttnKeys - e0) * (D / 8); i += kAttnSoftmaxWarps * 32) {
+                            const int at = i / (D / 8), ch = i % (D / 8), key = at < nb ? b0 + at : e0 + at - nb;
+                            uint8_t* const slot = ring + ((v0 + key / kVK) % kSlots) * Geo::kSlotBytes;
+                            *reinterpret_cast<uint4*>(slot + (ch / 8) * (kVK * 128) + (key % kVK) * 128 + (ch % 8) * 16) =
+                                make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
                     }
@@ -690,7 +740,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                 l += x[(half ^ 1) * 128 + row];
                 named_bar_sync(1 + quarter, 64);   // the next tile's maxima use the same buffer
                 const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
-                float* const prow = a.part + ((size_t)slot * kAttnRows + row) * D + half * (D / 2);
+                float* const pcol = a.part + ((size_t)slot * D + half * (D / 2)) * kAttnRows + row;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                 for (int i = 0; i < D / 2; i += 32) {
@@ -710,8 +760,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                             }
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4*>(prow + i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            for (int e = 0; e < 32; ++e) pcol[(i + e) * kAttnRows] = __uint_as_float(o[e]);
                         }
                     }
                 }
@@ -720,7 +769,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             tc_fence_before();
             __syncwarp();
             mbar_arrive_if(ofree, lane == 0);
-            ++seg;
         }
         if (tid == 0) {
             a.splits[2 * blockIdx.x] = split0;
@@ -736,6 +784,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const int issued = flags[1];
         for (int j = issued > kSlots ? issued - kSlots : 0; j < issued; ++j)
             mbar_wait_drain(full0 + 8 * (j % kSlots), (j / kSlots) & 1, kDrainNs);
+        while (flags[4] < 0 && global_timer_ns() - t0 < 4 * kDrainNs) {
+        }
+        if (flags[4] > 0) mbar_wait_drain(qfull, (flags[4] - 1) & 1, kDrainNs);
     }
     tc_fence_before();
     __syncthreads();
@@ -747,67 +798,87 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
 
 // ---------------------------------------------------------------- the join
 
-constexpr int kJoinWarps = 8;
-constexpr int kJoinRowsY = 16;     // blocks of a split's rows
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocksY = 16;   // blocks of a split's items
+constexpr int kJoinParts = 8;      // most threads that share an item's partials
 
 // Adds the partials of the query tiles that were split over several blocks, in block order:
-// O = sum_i 2^(c (m_i - M)) O_i / sum_i 2^(c (m_i - M)) l_i. Block (x, y) takes rows y, y + 16, ...
-// of the tile that block x of the attention kernel opened; its warps share the partials. The same
-// blocks write zeros to the output rows past the last request's.
+// O = sum_i 2^(c (m_i - M)) O_i / sum_i 2^(c (m_i - M)) l_i. An item is 8 columns of a row; blocks
+// (x, *) share the items of the tile that block x of the attention kernel opened, neighbouring lanes
+// taking neighbouring rows (partials are stored column by column). Up to 8 threads share an
+// item's partials, each with a running maximum, so that few rows with many partials are read in
+// parallel. Bound by latency: two rounds of loads. The same blocks write zeros to the output rows
+// past the last request's.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnArgs a) {
-    __shared__ float acc[kJoinWarps][D];
-    __shared__ float sums[kJoinWarps];
+__global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+    __shared__ float acc[kJoinThreads][11];    // 8 columns, maximum, sum (odd stride: no bank conflicts)
     grid_launch_dependents();
     grid_dependency_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kPer = D / 32;       // columns of a lane
+    const int tid = threadIdx.x;
     const int4 s = a.splits[2 * blockIdx.x];
     if (s.x >= 0) {
-        const int last = a.splits[2 * blockIdx.x + 1].x, count = last - (int)blockIdx.x + 1;
+        const int last = a.splits[2 * blockIdx.x + 1].x, count = last - (int)blockIdx.x + 1, rows = s.w;
         const AttnReq rq = attn_req(a, s.x);
         const float c = a.scale_log2;
-        auto slot = [&](int i) { return 2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0); };
-        for (int row = blockIdx.y; row < s.w; row += kJoinRowsY) {
-            float m = -INFINITY;
-            for (int i = lane; i < count; i += 32) m = fmaxf(m, a.ml[slot(i) * kAttnRows + row].x);
+        const int parts = count >= 8 ? 8 : (count >= 4 ? 4 : 2), per = kJoinThreads / parts;
+        const int part = tid / per, items = rows * (D / 8);
+        for (int i0 = blockIdx.y * per; i0 < items; i0 += kJoinBlocksY * per) {
+            const int item = i0 + tid % per, group = item / rows, row = item - group * rows;
+            float m = -INFINITY, l = 0.f, o[8];
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            if (m == -INFINITY) m = 0.f;
-            float o[kPer], l = 0.f;
+            for (int e = 0; e < 8; ++e) o[e] = 0.f;
+            if (item < items) {
+#pragma unroll 2
+                for (int i = part; i < count; i += parts) {
+                    const int slot = 2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0);
+                    const float2 ml = a.ml[slot * kAttnRows + row];
+                    const float* src = a.part + ((size_t)slot * D + group * 8) * kAttnRows + row;
+                    float v[8];
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-            for (int i = warp; i < count; i += kJoinWarps) {
-                const float2 ml = a.ml[slot(i) * kAttnRows + row];
-                const float f = exp2_fast((ml.x - m) * c);
-                const float* src = a.part + ((size_t)slot(i) * kAttnRows + row) * D;
-                l += f * ml.y;
+                    for (int e = 0; e < 8; ++e) v[e] = src[e * kAttnRows];
+                    const float mx = fmaxf(m, ml.x), ref = mx == -INFINITY ? 0.f : mx;
+                    const float f = exp2_fast((m - ref) * c), fi = exp2_fast((ml.x - ref) * c);
+                    l = l * f + ml.y * fi;
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) o[e] += f * src[e * 32 + lane];
+                    for (int e = 0; e < 8; ++e) o[e] = o[e] * f + v[e] * fi;
+                    m = mx;
+                }
             }
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[warp][e * 32 + lane] = o[e];
-            if (lane == 0) sums[warp] = l;
+            for (int e = 0; e < 8; ++e) acc[tid][e] = o[e];
+            acc[tid][8] = m;
+            acc[tid][9] = l;
             __syncthreads();
-            if (tid < D / 2) {
-                float x = 0.f, y = 0.f, total = 0.f;
+            if (tid < per && item < items) {
+                float mx = -INFINITY;
+                for (int i = 0; i < parts; ++i) mx = fmaxf(mx, acc[i * per + tid][8]);
+                if (mx == -INFINITY) mx = 0.f;
+                float total = 0.f;
 #pragma unroll
-                for (int i = 0; i < kJoinWarps; ++i) {
-                    x += acc[i][2 * tid];
-                    y += acc[i][2 * tid + 1];
-                    total += sums[i];
+                for (int e = 0; e < 8; ++e) o[e] = 0.f;
+                for (int i = 0; i < parts; ++i) {
+                    const float* x = acc[i * per + tid];
+                    const float f = exp2_fast((x[8] - mx) * c);
+                    total += f * x[9];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] += f * x[e];
                 }
                 const float inv = total == 0.f ? 0.f : 1.f / total;
-                const int at = s.z * kAttnRows + row, token = at / a.group, hq = s.y * a.group + at - token * a.group;
-                reinterpret_cast<uint32_t*>(a.out + (rq.q0 + token) * a.out_stride + (long long)hq * D)[tid] =
-                    pack16<BF16>(x * inv, y * inv);
+                const int token = row / a.group, head = s.y * a.group + row - token * a.group;
+                uint4 u;
+                u.x = pack16<BF16>(o[0] * inv, o[1] * inv);
+                u.y = pack16<BF16>(o[2] * inv, o[3] * inv);
+                u.z = pack16<BF16>(o[4] * inv, o[5] * inv);
+                u.w = pack16<BF16>(o[6] * inv, o[7] * inv);
+                *reinterpret_cast<uint4*>(a.out + (rq.q0 + s.z * a.tile_tokens + token) * a.out_stride +
+                                          (long long)head * D + group * 8) = u;
             }
             __syncthreads();
         }
     }
     const int end = min(max(a.q_start[a.R], 0), a.tokens), chunks = a.heads * a.group * (D / 8);
     for (int t = end + blockIdx.x + gridDim.x * blockIdx.y; t < a.tokens; t += gridDim.x * gridDim.y)
-        for (int i = tid; i < chunks; i += kJoinWarps * 32)
+        for (int i = tid; i < chunks; i += kJoinThreads)
             reinterpret_cast<uint4*>(a.out + t * a.out_stride)[i] = make_uint4(0, 0, 0, 0);
 }
 

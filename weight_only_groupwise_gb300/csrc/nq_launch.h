@@ -19,7 +19,9 @@ bool encode_x_map(CUtensorMap* map, const void* X, int T, int K, int TP);
 bool tensor_maps_available();
 bool encode_weight_maps(CUtensorMap* wmap, CUtensorMap* smap, const void* W, const void* S, int bits, int K, int N,
                         int TP);
-// The tensor map of a paged cache's K or V tensor (16-bit elements, boxes of min(page, rows) keys).
+// The tensor maps of paged attention: the queries, and a paged cache's K or V tensor (16-bit elements, boxes of min(page, rows) keys).
+bool encode_q_map(CUtensorMap* map, const void* q, long long stride, int dim, int heads, int tokens, int group,
+                  int box_tokens, bool bf16);
 bool encode_kv_map(CUtensorMap* map, void* base, const nq_kv_cache* c, bool bf16, int rows);
 cudaError_t launch_tc_proj(int bits, const TcArgs& a, cudaStream_t stream, bool pdl);
 cudaError_t launch_tc_proj_fp4(const TcArgs& a, cudaStream_t stream, bool pdl);

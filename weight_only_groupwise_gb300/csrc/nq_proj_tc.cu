@@ -95,6 +95,21 @@ bool encode_kv_map(CUtensorMap* map, void* base, const nq_kv_cache* c, bool bf16
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries [tokens][heads][dim] as a 3-D map {dim, heads, tokens}: a box is 64 columns (a 128-byte
+// swizzled row) of `group` heads of `box_tokens` tokens; tokens past the last read as zeros.
+bool encode_q_map(CUtensorMap* map, const void* q, long long stride, int dim, int heads, int tokens, int group,
+                  int box_tokens, bool bf16) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)box_tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(q),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_tc_proj(int bits, const TcArgs& a, cudaStream_t stream, bool pdl) {
     if (bits == kFp4) return launch_tc_proj_fp4(a, stream, pdl);
     switch (a.p.TP) {
