@@ -5,19 +5,26 @@
 // cumulative sum decides the token, so rounding moves the choice only where two scores are
 // within an ulp of each other.
 //
-// Kept tokens are a prefix of the row's order (logit descending, index ascending), so a row needs
-// a cut, not a sort: a histogram of the distance to the maximum finds the bin that holds the
-// cut. If few tokens lie up to that bin they are gathered, sorted and settled by one block; else
-// the cut is refined over the bits of the logits' ordered integers (at most three more
-// histograms) and a last pass over the row takes the argmax.
-//
-// Weights are summed as 2^-30 fixed point in integers (two 32-bit halves in the histogram): sums
-// are exact and do not depend on the order of the atomics.
-//
 // A row is a thread-block cluster, a slice of the row a block, kept in shared memory when it fits
-// (one read of the logits from memory); histograms and results cross through distributed shared
-// memory. Bound by the latency of these few steps for few rows, by the logits' (and, unfiltered,
-// the noise's) bytes for many.
+// (one read of the logits from memory). Three ways through a row:
+//   * no top-k and no top-p: the cluster's maximum, then one pass that takes the argmax. The score
+//     is first estimated with the fast logarithm; only tokens that could beat the thread's best
+//     are scored exactly.
+//   * a cut that few tokens pass (the common case): kept tokens are a prefix of the row's order
+//     (logit descending, index ascending). Every block sorts its threads' maxima; the k-th of
+//     them bounds the block's k-th token from below, so the tokens from there up, little more than k,
+//     hold its first k. They are handed to one block, which sorts them and settles the row: one
+//     barrier of the cluster. top-p alone tries the same with k = 64 if those can hold the share.
+//   * a cut among many tokens: a histogram of counts and weights over the cluster, by the distance
+//     to the maximum, finds the cut's bin; its tokens are sorted by one block, which gives the cut
+//     as (logit, index). A bin of more tokens than that block can sort (far tails, many equal
+//     logits) is cut again by the bits of the logits' ordered integers, at most three times. Then
+//     the pass of the first way over the tokens inside the cut.
+// Weights are summed as 2^-30 fixed point in integers (two 16-bit halves in the histograms), or
+// by each thread in a fixed order: no sum depends on the order of atomics.
+//
+// Bound by the latency of these few steps for few rows, by instructions per token for many (the
+// logits' bytes alone would take a fraction of it).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -41,7 +48,9 @@ typedef unsigned long long u64;
 constexpr int kSaThreads = 512;
 constexpr int kSaWarps = kSaThreads / 32;
 constexpr int kSaBins = 2048;
-constexpr int kSaList = 2 * kSaThreads;        // tokens the gathering block can sort
+constexpr int kSaPer = kSaBins / kSaThreads;   // bins of a thread
+constexpr int kSaList = 4 * kSaThreads;        // tokens the settling block can sort
+constexpr int kSaTryP = 48;                    // tokens a block hands over for top-p alone
 constexpr int kSaMaxCluster = 8;
 constexpr int kSaMaxSlice = 65535;             // 16-bit halves of the weights sum below 2^32
 constexpr int kSaMaxVocab = kSaMaxSlice / 16 * 16 * kSaMaxCluster;
@@ -73,16 +82,40 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
+// (value, lowest index) as one ordered integer.
+__device__ __forceinline__ u64 ranked(uint32_t key, int i) { return ((u64)key << 32) | (0xFFFFFFFFu - (uint32_t)i); }
+__device__ __forceinline__ int index_of(u64 v) { return (int)(0xFFFFFFFFu - (uint32_t)v); }
 
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+// The least integer that is not below p * w (0 < p < 1; at least 1: the first token is always
+// kept), by integers: fp64 runs at a small fraction of the integer rate.
+__device__ __forceinline__ u64 share_of(float p, u64 w) {
+    if (!(p > 0.f)) return 1;
+    const uint32_t u = __float_as_uint(p), ex = u >> 23;
+    const u64 mant = ex ? (u & 0x7FFFFFu) | 0x800000u : u & 0x7FFFFFu;
+    const int shift = 150 - (int)(ex ? ex : 1);      // p = mant * 2^-shift, shift >= 24
+    if (shift > 100) return 1;
+    const unsigned __int128 v = (unsigned __int128)mant * w, one = (unsigned __int128)1 << shift;
+    const u64 t = (u64)((v + one - 1) >> shift);
+    return t > 0 ? t : 1;
+}
 
 struct Found {             // the bin of a cut: counts and weights of the tokens before it and in it
     int bin, before, count, total;
     u64 before_w, total_w;
     int by_count;          // the cut was looked for by count (else by weight)
     int none;              // no cut
+};
+
+struct Share {             // what a block hands to the settling one besides its first tokens
+    float weight, listed_weight;   // sums of its tokens' weights and of the handed ones, for its own maximum
+    float top;             // its maximum
+    int count;             // tokens handed over
+    uint32_t low;          // its other tokens lie below this key (0: there are none)
+    int fail;              // its first tokens do not fit
+};
+
+struct Cut {               // kept: tokens whose (key, index) rank is at least this; their weight
+    u64 rank, mass;
 };
 
 struct SaShared {
@@ -92,10 +125,40 @@ struct SaShared {
     u64 part_w[2][kSaMaxCluster];
     u64 warp[kSaWarps];
     u64 warp_w[kSaWarps];
+    Share share[kSaMaxCluster];
     Found found;
-    unsigned listed;
-    u64 scalar;
+    Cut cut;
+    uint32_t bound;
+    int listed, verdict;
 };
+
+__device__ __forceinline__ void unpack_chunk(const uint4& u, float (&x)[4], float) {
+    x[0] = __uint_as_float(u.x);
+    x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z);
+    x[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void unpack_chunk(const uint4& u, float (&x)[8], __nv_bfloat16) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void unpack_chunk(const uint4& u, float (&x)[8], __half) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename T>
 struct Row {
@@ -107,23 +170,16 @@ struct Row {
     int chunks;
     // Chunk c: E consecutive tokens from first(c), those outside the slice as -inf.
     __device__ __forceinline__ int first(int c) const { return begin - lead + c * E; }
-    __device__ __forceinline__ void from_global(int c, T (&x)[E]) const {
+    __device__ __forceinline__ uint4 from_global(int c) const {
         const int i0 = first(c);
-        if (i0 >= begin && i0 + E <= end) {
-            *reinterpret_cast<uint4*>(x) = __ldg(reinterpret_cast<const uint4*>(base + i0));
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = i0 + e >= begin && i0 + e < end ? base[i0 + e] : T(-INFINITY);
-        }
-    }
-    __device__ __forceinline__ void load(int c, uint32_t (&key)[E]) const {
+        if (i0 >= begin && i0 + E <= end) return __ldg(reinterpret_cast<const uint4*>(base + i0));
         alignas(16) T x[E];
-        if (smem)
-            *reinterpret_cast<uint4*>(x) = reinterpret_cast<const uint4*>(smem)[c];
-        else
-            from_global(c, x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) key[e] = order_key(as_float(x[e]));
+        for (int e = 0; e < E; ++e) x[e] = i0 + e >= begin && i0 + e < end ? base[i0 + e] : T(-INFINITY);
+        return *reinterpret_cast<const uint4*>(x);
+    }
+    __device__ __forceinline__ void load(int c, float (&x)[E]) const {
+        unpack_chunk(smem ? reinterpret_cast<const uint4*>(smem)[c] : from_global(c), x, T());
     }
 };
 
@@ -137,9 +193,12 @@ __device__ __forceinline__ u64 block_max(u64 v, SaShared& s) {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s.warp[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = s.warp[0];
+    v = s.warp[threadIdx.x & (kSaWarps - 1)];
 #pragma unroll
-    for (int i = 1; i < kSaWarps; ++i) v = s.warp[i] > v ? s.warp[i] : v;
+    for (int d = kSaWarps / 2; d > 0; d >>= 1) {
+        const u64 o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
+        v = o > v ? o : v;
+    }
     return v;
 }
 
@@ -175,8 +234,163 @@ __device__ __forceinline__ void block_scan(u64& x, u64& y, u64& tx, u64& ty, SaS
     y += by;
 }
 
+// Bitonic sort, descending, of N consecutive values a thread: partners in the thread, in the warp
+// (shuffles), and only then through shared memory (`buf`, N values a thread).
+template <int N, typename U>
+__device__ __forceinline__ void block_sort(U (&v)[N], U* buf) {
+    const int tid = threadIdx.x;
+    auto pick = [](U a, U b, bool larger) { return (a > b) == larger ? a : b; };
+    for (int len = 2; len <= kSaThreads * N; len *= 2)
+        for (int d = len / 2; d > 0; d /= 2) {
+            if (d >= 32 * N) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < N; ++j) buf[tid * N + j] = v[j];
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int i = tid * N + j;
+                    v[j] = pick(v[j], buf[i ^ d], ((i & d) == 0) == ((i & len) == 0));
+                }
+            } else if (d >= N) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int i = tid * N + j;
+                    v[j] = pick(v[j], __shfl_xor_sync(0xFFFFFFFFu, v[j], d / N), ((i & d) == 0) == ((i & len) == 0));
+                }
+            } else {
+#pragma unroll
+                for (int dd = 1; dd < N; dd *= 2)
+                    if (d == dd) {
+#pragma unroll
+                        for (int j = 0; j < N; ++j)
+                            if ((j & dd) == 0) {
+                                const U a = v[j], b = v[j | dd];
+                                const bool desc = ((tid * N + j) & len) == 0;
+                                v[j] = pick(a, b, desc);
+                                v[j | dd] = pick(a, b, !desc);
+                            }
+                    }
+            }
+        }
+    __syncthreads();
+}
+
+// (l - top) / T from e = top - l: a quotient by the reciprocal with one correction is the rounded
+// one away from the ends of the range of T, where the division itself is used.
+struct Scaler {
+    float temp, inv;
+    bool usual;
+    __device__ __forceinline__ explicit Scaler(float t) : temp(t), inv(1.f / t), usual(t >= 1e-6f && t <= 1e6f) {}
+    __device__ __forceinline__ float operator()(float e) const {
+        if (!usual || !(e < 1e30f)) return -e / temp;
+        const float q = e * inv;
+        return -fmaf(fmaf(-q, temp, e), inv, q);
+    }
+};
+
+// A token's weight in 2^-30 of the maximum's, from e = top - l, for sums over many tokens.
+struct Weigher {
+    float c;
+    __device__ __forceinline__ explicit Weigher(float temp) : c(-1.4426950408889634f * fminf(1.f / temp, 1e30f)) {}
+    __device__ __forceinline__ float exp(float e) const {
+        float y;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(e * c));
+        return y;
+    }
+    __device__ __forceinline__ unsigned operator()(float e) const { return __float2uint_rn(exp(e) * kSaOne); }
+};
+
+struct Settings {
+    float p, floor_d;
+    int k;
+    bool by_k, by_p;
+};
+
+// The settling block: the row's token from the cluster's first tokens (n of them, gathered in
+// s.list), N a thread. Returns the token, or -1 if top-p alone cannot be settled among them.
+template <int N>
+__device__ __forceinline__ int settle(SaShared& s, int n, float m, uint32_t bound, u64 mass, const Settings& o,
+                                      const Scaler& scaled, const float* noise) {
+    const int tid = threadIdx.x;
+    u64 v[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = tid * N + j < n ? s.list[tid * N + j] : 0;
+    block_sort<N>(v, s.list);
+    const uint32_t top = order_key(m);
+    const int last = o.by_k ? min(n, o.k) : n;             // tokens that may be kept
+    float d[N], z[N];
+    u64 wt[N], x = 0, y = 0, unused, sum;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        z[j] = 1.f;
+        d[j] = 0.f;
+        wt[j] = 0;
+        if (tid * N + j < last) {
+            const uint32_t key = (uint32_t)(v[j] >> 32);
+            z[j] = __ldg(noise + index_of(v[j]));
+            if (key != top) d[j] = scaled(m - key_value(key));
+            wt[j] = (u64)rintf(expf(d[j]) * kSaOne);
+        }
+        y += wt[j];
+    }
+    const u64 own = y;
+    block_scan(x, y, unused, sum, s);
+    y -= own;
+    const u64 target = o.by_p ? share_of(o.p, o.by_k ? sum : mass) : ~0ull;
+    u64 best = 0;
+    bool reached = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int at = tid * N + j;
+        if (at < last) {
+            if (at == 0 || (y < target && d[j] >= o.floor_d)) {
+                const u64 c = ranked(order_key(d[j] - logf(z[j])), index_of(v[j]));
+                best = c > best ? c : best;
+            }
+            y += wt[j];
+            // the cut has to lie among tokens that no block has kept back
+            reached |= (uint32_t)(v[j] >> 32) >= bound && y >= target;
+        }
+    }
+    best = block_max(best, s);
+    const bool settled = o.by_k || bound == 0 || __syncthreads_or(reached);
+    return settled ? index_of(best) : -1;
+}
+
+// The cut among the n tokens of its bin (in s.list), which follow `before` tokens of weight
+// before_w: the k-th token, or the last whose weight before it is below the target.
+template <int N>
+__device__ __forceinline__ Cut cut_in_bin(SaShared& s, int n, uint32_t top, float m, int k, int before, u64 before_w,
+                                          u64 target, const Weigher& weight) {
+    const int tid = threadIdx.x;
+    u64 v[N], wt[N], x = 0, y = 0, unused, sum;
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = tid * N + j < n ? s.list[tid * N + j] : 0;
+    block_sort<N>(v, s.list);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const uint32_t key = (uint32_t)(v[j] >> 32);
+        wt[j] = 0;
+        if (tid * N + j < n) wt[j] = weight(key == top ? 0.f : m - key_value(key));
+        y += wt[j];
+    }
+    const u64 own = y;
+    block_scan(x, y, unused, sum, s);
+    y += before_w - own;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int at = tid * N + j;
+        const bool here = k > 0 ? before + at + 1 == k : y < target && (y + wt[j] >= target || at == n - 1);
+        y += wt[j];
+        if (at < n && here) s.cut = {v[j], y};
+    }
+    __syncthreads();
+    return s.cut;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kSaThreads) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t sa_slice[];
     __shared__ SaShared s;
     cg::cluster_group cl = cg::this_cluster();
@@ -185,7 +399,6 @@ __global__ void __launch_bounds__(kSaThreads) sample_kernel(const SampleArgs a) 
     const int r = blockIdx.x / C;
     constexpr int E = Row<T>::E;
 
-    if (tid == 0) s.listed = 0;
     grid_launch_dependents();
     grid_dependency_wait();
 
@@ -200,9 +413,10 @@ __global__ void __launch_bounds__(kSaThreads) sample_kernel(const SampleArgs a) 
     const float temp = a.temperature ? a.temperature[r] : 1.f;
     const float p = a.top_p ? a.top_p[r] : 1.f, least = a.min_p ? a.min_p[r] : 0.f;
     const int k = a.top_k ? a.top_k[r] : 0;
+    const bool by_k = k > 0 && k < a.V, by_p = p < 1.f, greedy = !(temp > 0.f);
     const float floor_d = least > 0.f ? logf(fminf(least, 1.f)) : -INFINITY;
 
-    // exchange: every block's value to every block of the cluster
+    // exchange: every block's values to every block of the cluster
     int turn = 0;
     auto exchange = [&](u64 v, u64 w) {
         turn ^= 1;
@@ -221,72 +435,198 @@ __global__ void __launch_bounds__(kSaThreads) sample_kernel(const SampleArgs a) 
         for (int i = 1; i < C; ++i) v = s.part[turn][i] > v ? s.part[turn][i] : v;
         return v;
     };
+    const Scaler scaled(temp);
+    const Weigher weight(temp);
+    const Settings set = {p, floor_d, k, by_k, by_p};
 
-    // The maximum, its lowest index; the slice goes to shared memory on the way.
-    u64 best = 0;
+    // The slice goes to shared memory (all copies in flight at once); every thread's maximum.
     if (a.resident) {
         for (int c = tid; c < row.chunks; c += kSaThreads) {
-            alignas(16) T x[E];
-            row.from_global(c, x);
-            reinterpret_cast<uint4*>(sa_slice)[c] = *reinterpret_cast<const uint4*>(x);
+            const int i0 = row.first(c);
+            if (i0 >= row.begin && i0 + E <= row.end)
+                cp_async16(smem_u32(sa_slice) + c * 16, row.base + i0);
+            else
+                reinterpret_cast<uint4*>(sa_slice)[c] = row.from_global(c);
         }
-        row.smem = sa_slice;    // each thread reads back its own chunks until the next barrier
+        cp_async_wait_all();
+        row.smem = sa_slice;               // threads read back what they copied themselves
     }
+    float high = -INFINITY;
     for (int c = tid; c < row.chunks; c += kSaThreads) {
-        uint32_t key[E];
-        row.load(c, key);
-        const int i0 = row.first(c);
+        float x[E];
+        row.load(c, x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const u64 v = ((u64)key[e] << 32) | (0xFFFFFFFFu - (uint32_t)(i0 + e));
-            best = v > best ? v : best;
-        }
+        for (int e = 0; e < E; ++e) high = fmaxf(high, x[e]);   // ignores NaN
     }
-    best = cluster_max(best);
-    const uint32_t top = (uint32_t)(best >> 32);
-    const int first = (int)(0xFFFFFFFFu - (uint32_t)best);
-    if (top <= kSaNone || !(temp > 0.f)) {     // nothing to choose from, or greedy
-        if (rank == 0 && tid == 0) a.tokens[r] = top <= kSaNone ? -1 : first;
+
+    // ---------------------------------------------------------------- a cut that few tokens pass
+    const int cap = kSaList / C;
+    float top_here;
+    if (!greedy && (by_k ? k <= cap : by_p)) {
+        // at least `want` of the block's tokens are not below the want-th of its threads' maxima
+        const int want = by_k ? k : kSaTryP;
+        uint32_t key[1] = {order_key(high)};
+        block_sort<1>(key, reinterpret_cast<uint32_t*>(&s.hist[0][0]));
+        if (tid == 0) {
+            s.warp[0] = key[0];
+            s.listed = 0;
+        }
+        if (tid == want - 1) s.bound = key[0];
+        __syncthreads();
+        top_here = key_value((uint32_t)s.warp[0]);
+        const bool all = want > kSaThreads || s.bound <= kSaNone;
+        const uint32_t low = all ? kSaNone + 1 : s.bound;
+        const float low_value = key_value(low);
+        const bool inf_here = top_here == INFINITY;
+        u64* const mine = cl.map_shared_rank(&s.list[0], 0) + rank * cap;
+        float w = 0.f, lw = 0.f;
+        for (int c = tid; c < row.chunks; c += kSaThreads) {
+            float v[E], we[E];
+            row.load(c, v);
+            unsigned hit = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) hit |= v[e] >= low_value ? 1u << e : 0u;
+            if (!by_k) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    we[e] = inf_here ? (v[e] == INFINITY ? 1.f : 0.f) : weight.exp(top_here - v[e]);
+                    w += we[e] > 0.f ? we[e] : 0.f;        // not NaN
+                }
+            }
+            if (hit) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if ((hit >> e) & 1) {
+                        const int at = atomicAdd(&s.listed, 1);
+                        if (at < cap) mine[at] = ranked(order_key(v[e]), row.first(c) + e);
+                        if (!by_k) lw += we[e];
+                    }
+            }
+        }
+        // the threads' sums in a fixed order: as integers
+        u64 x = (u64)(w * kSaOne), y = (u64)(lw * kSaOne), all_w = 0, all_lw = 0;
+        if (by_k)
+            __syncthreads();
+        else
+            block_scan(x, y, all_w, all_lw, s);
+        if (tid < C) {
+            Share h;
+            h.weight = (float)all_w;
+            h.listed_weight = (float)all_lw;
+            h.top = top_here;
+            h.count = min(s.listed, cap);
+            h.low = all ? 0u : low;
+            h.fail = s.listed > cap;
+            *cl.map_shared_rank(&s.share[rank], tid) = h;
+        }
+        cl.sync();
+        float m = -INFINITY, mass = 0.f, listed = 0.f;
+        uint32_t bound = 0;
+        bool fail = false;
+        for (int i = 0; i < C; ++i) m = fmaxf(m, s.share[i].top);
+        for (int i = 0; i < C; ++i) {
+            const Share& h = s.share[i];
+            fail |= h.fail != 0;
+            bound = max(bound, h.low);
+            if (!by_k && h.weight > 0.f) {
+                const float f = h.top == m ? 1.f : expf(scaled(m - h.top));
+                mass += h.weight * f;
+                listed += h.listed_weight * f;
+            }
+        }
+        // top-p alone: the listed tokens must be able to hold the share
+        if (!by_k) fail |= listed < p * mass * 0.9999f;
+        if (!fail) {
+            if (rank == 0) {
+                // the blocks' parts, brought together (each is read before it is written over)
+                int n = 0, from = 0;
+                u64 part[kSaList / kSaThreads];
+                for (int i = 0; i < C; ++i) n += s.share[i].count;
+#pragma unroll
+                for (int j = 0; j < kSaList / kSaThreads; ++j) {
+                    int at = j * kSaThreads + tid;
+                    part[j] = 0;
+                    if (at < n) {
+                        for (from = 0; at >= s.share[from].count; ++from) at -= s.share[from].count;
+                        part[j] = s.list[from * cap + at];
+                    }
+                }
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kSaList / kSaThreads; ++j) s.list[j * kSaThreads + tid] = part[j];
+                __syncthreads();
+                int token = -1;
+                bool settled = n == 0;
+                if (n > 0) {
+                    token = n <= kSaThreads       ? settle<1>(s, n, m, bound, (u64)mass, set, scaled, noise)
+                            : n <= 2 * kSaThreads ? settle<2>(s, n, m, bound, (u64)mass, set, scaled, noise)
+                                                  : settle<4>(s, n, m, bound, (u64)mass, set, scaled, noise);
+                    settled = token >= 0;
+                }
+                if (settled && tid == 0) a.tokens[r] = token;
+                if (!by_k && tid < C) *cl.map_shared_rank(&s.verdict, tid) = settled ? 1 : 0;
+            }
+            if (by_k) return;
+            cl.sync();
+            if (s.verdict) return;
+        }
+    } else {
+        top_here = key_value((uint32_t)block_max(order_key(high), s));
+    }
+
+    // ---------------------------------------------------------------- the row's maximum
+    const uint32_t top = (uint32_t)cluster_max(order_key(top_here));
+    if (top <= kSaNone) {                          // nothing to choose from
+        if (rank == 0 && tid == 0) a.tokens[r] = -1;
         return;
     }
     const float m = key_value(top);
-    auto dist = [&](uint32_t key) { return key == top ? 0.f : (key_value(key) - m) / temp; };
-    auto weight = [&](uint32_t key) { return (unsigned)rintf(expf(dist(key)) * kSaOne); };
-    // (token score, lowest index) as one ordered integer
-    auto race = [&](float d, int i) {
-        return ((u64)order_key(d - logf(noise[i])) << 32) | (0xFFFFFFFFu - (uint32_t)i);
-    };
+    if (greedy) {
+        u64 best = 0;
+        for (int c = tid; c < row.chunks; c += kSaThreads) {
+            float x[E];
+            row.load(c, x);
+#pragma unroll
+            for (int e = E - 1; e >= 0; --e)
+                if (x[e] == m) best = max(best, ranked(top, row.first(c) + e));
+        }
+        best = cluster_max(best);
+        if (rank == 0 && tid == 0) a.tokens[r] = index_of(best);
+        return;
+    }
+    // An infinite maximum has all the mass: distances 0 and infinity.
+    const bool inf_row = m == INFINITY;
+    auto below = [&](float x) { return inf_row ? (x == INFINITY ? 0.f : INFINITY) : m - x; };
 
-    // ---------------------------------------------------------------- the cut
-    // tokens whose weight rounds to nothing need no exponential
-    const float tiny = temp * 25.f;
-    auto add = [&](unsigned bin, uint32_t key) {
+    // ---------------------------------------------------------------- a cut among many tokens
+    auto add = [&](unsigned bin, float d) {
         atomicAdd(&s.hist[0][bin], 1u);
-        if (!(m - key_value(key) > tiny)) {
-            const unsigned w = weight(key);
+        if (by_p) {
+            const unsigned w = weight(d);
             if (w & 0xFFFFu) atomicAdd(&s.hist[1][bin], w & 0xFFFFu);
             if (w >> 16) atomicAdd(&s.hist[2][bin], w >> 16);
         }
     };
     auto clear = [&]() {
         __syncthreads();
+        if (tid == 0) s.listed = 0;
         for (int i = tid; i < 3 * kSaBins; i += kSaThreads) (&s.hist[0][0])[i] = 0;
         __syncthreads();
     };
-    // The bin where the count (before `base` tokens) reaches kk, or where the weight (after
-    // `base_w`) reaches the share p of `mass` (0: of the total found here). kk <= 0: by weight. A
-    // count that is not reached turns into the search by weight.
+    // The bin where the count (with `base` tokens before the bins) reaches kk, or where the weight
+    // (with base_w before) reaches the share p of `mass` (0: of the total found here). kk <= 0: by
+    // weight. A count that is not reached turns into the search by weight.
     auto find = [&](int kk, int base, u64 base_w, u64 mass) {
         if (tid == 0) s.found.none = 1;
         cl.sync();
         const int sec = kSaBins / C, per = sec > kSaThreads ? sec / kSaThreads : 1;
         const int b0 = rank * sec + tid * per;
         const bool mine = tid * per < sec;
-        unsigned cnt[kSaBins / kSaThreads];
-        u64 wt[kSaBins / kSaThreads];
+        unsigned cnt[kSaPer];
+        u64 wt[kSaPer];
         u64 x = 0, y = 0, tx, ty;
 #pragma unroll
-        for (int i = 0; i < kSaBins / kSaThreads; ++i) {
+        for (int i = 0; i < kSaPer; ++i) {
             cnt[i] = 0;
             wt[i] = 0;
             if (mine && i < per) {
@@ -319,14 +659,13 @@ __global__ void __launch_bounds__(kSaThreads) sample_kernel(const SampleArgs a) 
         x += base;
         y += base_w;
         const bool by_count = kk > 0 && (u64)kk <= base + total;
-        double target = (double)p * (double)(mass ? mass : base_w + total_w);
-        if (!(target >= 0.5)) target = 0.5;     // the first token is always kept
-        if (by_count || p < 1.f) {
+        const u64 target = by_p ? share_of(p, mass ? mass : base_w + total_w) : ~0ull;
+        if (by_count || by_p) {
 #pragma unroll
-            for (int i = 0; i < kSaBins / kSaThreads; ++i) {
+            for (int i = 0; i < kSaPer; ++i) {
                 if (mine && i < per && cnt[i] > 0 &&
                     (by_count ? x < (u64)kk && x + cnt[i] >= (u64)kk
-                              : (double)y < target && (double)(y + wt[i]) >= target)) {
+                              : y < target && y + wt[i] >= target)) {
                     const Found f = {b0 + i, (int)x, (int)cnt[i], (int)(base + total), y, base_w + total_w, by_count, 0};
                     for (int c = 0; c < C; ++c) *cl.map_shared_rank(&s.found, c) = f;
                 }
@@ -337,214 +676,256 @@ __global__ void __launch_bounds__(kSaThreads) sample_kernel(const SampleArgs a) 
         cl.sync();
         return s.found;
     };
-    const float scale = (kSaBins / kSaRange) / fmaxf(temp, kSaLeastT);
-    auto bin_of = [&](uint32_t key) {
-        return key == top ? 0 : (int)fminf((m - key_value(key)) * scale, (float)(kSaBins - 1));
-    };
 
-    uint32_t cut = kSaNone + 1;    // kept: keys above `cut`, and the first `ties` tokens at it
-    u64 ties = ~0ull;
-    if ((k > 0 && k < a.V) || p < 1.f) {
-        clear();
-        for (int c = tid; c < row.chunks; c += kSaThreads) {
-            uint32_t key[E];
-            row.load(c, key);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (key[e] > kSaNone) add(bin_of(key[e]), key[e]);
-        }
-        const Found f = find(k, 0, 0, 0);
-        if (!f.none && f.before + f.count <= kSaList) {
-            // ------------------------------------------------------------ few: one block settles the row
+    u64 cut = ranked(kSaNone + 1, 0x7FFFFFFF);     // kept: ranks from here up
+    if (by_k || by_p) {
+        const float scale = (kSaBins / kSaRange) / fmaxf(temp, kSaLeastT);
+        // the last bin takes everything past the range
+        auto bin_of = [&](float d) { return (int)fminf(d * scale, (float)(kSaBins - 1)); };
+        auto histogram = [&]() {
+            clear();
             for (int c = tid; c < row.chunks; c += kSaThreads) {
-                uint32_t key[E];
-                row.load(c, key);
-                const int i0 = row.first(c);
+                float x[E];
+                row.load(c, x);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (key[e] > kSaNone && bin_of(key[e]) <= f.bin) {
-                        const unsigned at = atomicAdd(cl.map_shared_rank(&s.listed, 0), 1u);
-                        cl.map_shared_rank(&s.list[0], 0)[at] = ((u64)key[e] << 32) | (0xFFFFFFFFu - (uint32_t)(i0 + e));
-                    }
+                    if (x[e] > -INFINITY) add(bin_of(below(x[e])), below(x[e]));
+            }
+        };
+        histogram();
+        // The cut of the bin f, if its tokens can be sorted: all blocks hand them to the first.
+        auto sort_bin = [&](const Found& f, u64 mass) {
+            u64* const list = cl.map_shared_rank(&s.list[0], 0);
+            int* const listed = cl.map_shared_rank(&s.listed, 0);
+            for (int c = tid; c < row.chunks; c += kSaThreads) {
+                float x[E];
+                row.load(c, x);
+                unsigned hit = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) hit |= x[e] > -INFINITY && bin_of(below(x[e])) == f.bin ? 1u << e : 0u;
+                if (hit) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if ((hit >> e) & 1) list[atomicAdd(listed, 1)] = ranked(order_key(x[e]), row.first(c) + e);
+                }
             }
             cl.sync();
-            if (rank != 0) return;
-            const int n = f.before + f.count;
-            int size = 2;
-            while (size < n) size *= 2;
-            for (int i = tid; i < size; i += kSaThreads)
-                if (i >= n) s.list[i] = 0;
-            __syncthreads();
-            for (int len = 2; len <= size; len *= 2)          // descending
-                for (int d = len / 2; d > 0; d /= 2) {
-                    for (int i = tid; i < size / 2; i += kSaThreads) {
-                        const int lo = (i / d) * 2 * d + i % d, hi = lo + d;
-                        const u64 u = s.list[lo], v = s.list[hi];
-                        if ((u < v) == ((lo & len) == 0)) {
-                            s.list[lo] = v;
-                            s.list[hi] = u;
-                        }
-                    }
-                    __syncthreads();
-                }
-            u64 v[2], w[2], x = 0, y = 0, tx, ty;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = 2 * tid + i;
-                v[i] = at < n ? s.list[at] : 0;
-                w[i] = at < n && (!f.by_count || at < k) ? weight((uint32_t)(v[i] >> 32)) : 0;
-                y += w[i];
+            if (rank == 0) {
+                const u64 target = by_p ? share_of(p, mass) : ~0ull;
+                const int kk = f.by_count ? k : 0;
+                const Cut found = f.count <= kSaThreads
+                                      ? cut_in_bin<1>(s, f.count, top, m, kk, f.before, f.before_w, target, weight)
+                                      : cut_in_bin<4>(s, f.count, top, m, kk, f.before, f.before_w,
+                                                                         target, weight);
+                if (tid > 0 && tid < C) *cl.map_shared_rank(&s.cut, tid) = found;
+                if (tid == 0) s.listed = 0;
             }
-            const u64 own = y;
-            block_scan(x, y, tx, ty, s);
-            y -= own;
-            const double target = (double)p * (double)(f.by_count ? ty : f.total_w);
-            best = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = 2 * tid + i;
-                if (at < n) {
-                    const float d = dist((uint32_t)(v[i] >> 32));
-                    const bool kept = (!f.by_count || at < k) && (!(p < 1.f) || (double)y < target) && d >= floor_d;
-                    if (kept || at == 0) {
-                        const u64 c = race(d, (int)(0xFFFFFFFFu - (uint32_t)v[i]));
-                        best = c > best ? c : best;
-                    }
-                }
-                y += w[i];
-            }
-            best = block_max(best, s);
-            if (tid == 0) a.tokens[r] = (int)(0xFFFFFFFFu - (uint32_t)best);
-            return;
-        }
-        // ------------------------------------------------------------ many: refine the cut by the keys' bits
+            cl.sync();
+            return s.cut;
+        };
         // From the interval [lo, hi] of keys (tokens above: base, base_w) to one key.
-        struct Cut {
+        struct KeyCut {
             uint32_t key;
-            int before, count;
+            int before;
             u64 before_w;
         };
-        auto refine = [&](uint32_t lo, uint32_t hi, int kk, int base, u64 base_w, u64 mass, int count) {
+        auto refine = [&](uint32_t lo, uint32_t hi, int kk, int base, u64 base_w, u64 mass) {
             while (lo < hi) {
                 const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
                 clear();
                 for (int c = tid; c < row.chunks; c += kSaThreads) {
-                    uint32_t key[E];
-                    row.load(c, key);
+                    float x[E];
+                    row.load(c, x);
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (key[e] >= lo && key[e] <= hi) add((hi - key[e]) >> shift, key[e]);
+                    for (int e = 0; e < E; ++e) {
+                        const uint32_t key = order_key(x[e]);
+                        if (key >= lo && key <= hi) add((hi - key) >> shift, below(x[e]));
+                    }
                 }
                 const Found g = find(kk, base, base_w, mass);
                 if (g.none) break;             // cannot be: the interval holds the cut
                 base = g.before;
                 base_w = g.before_w;
-                count = g.count;
                 hi -= (uint32_t)g.bin << shift;
-                const uint32_t low = hi - ((1u << shift) - 1);
-                lo = low > lo && low <= hi ? low : lo;
+                const uint32_t least_key = hi - ((1u << shift) - 1);
+                lo = least_key > lo && least_key <= hi ? least_key : lo;
             }
-            return Cut{hi, base, count, base_w};
+            return KeyCut{hi, base, base_w};
         };
-        if (!f.none) {
-            // the keys of the bin
-            u64 high = 0, low = 0;
+        // The cut of the bin f by its keys' bits: one key, and the `ties` first tokens at it.
+        auto refine_bin = [&](const Found& f, u64 mass) {
+            u64 most = 0, fewest = 0;
             for (int c = tid; c < row.chunks; c += kSaThreads) {
-                uint32_t key[E];
-                row.load(c, key);
+                float x[E];
+                row.load(c, x);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (key[e] > kSaNone && bin_of(key[e]) == f.bin) {
-                        high = key[e] > high ? key[e] : high;
-                        low = (0xFFFFFFFFu - key[e]) > low ? (0xFFFFFFFFu - key[e]) : low;
+                    if (x[e] > -INFINITY && bin_of(below(x[e])) == f.bin) {
+                        const uint32_t key = order_key(x[e]);
+                        most = max(most, (u64)key);
+                        fewest = max(fewest, (u64)(0xFFFFFFFFu - key));
                     }
             }
-            high = cluster_max(high);
-            low = cluster_max(low);
-            u64 mass = f.by_count ? 0 : f.total_w;
-            Cut g = refine(0xFFFFFFFFu - (uint32_t)low, (uint32_t)high, f.by_count ? k : 0, f.before, f.before_w, mass, f.count);
-            cut = g.key;
-            u64 w = weight(cut);
+            most = cluster_max(most);
+            fewest = cluster_max(fewest);
+            const KeyCut g = refine(0xFFFFFFFFu - (uint32_t)fewest, (uint32_t)most, f.by_count ? k : 0, f.before, f.before_w, mass);
+            const u64 w = weight(g.key == top ? 0.f : below(key_value(g.key)));
+            u64 ties;
             if (f.by_count) {
                 ties = (u64)(k - g.before);
-                mass = g.before_w + ties * w;
-                if (p < 1.f) g = refine(cut, top, 0, 0, 0, mass, 0);
-            }
-            if (p < 1.f) {
+            } else {
                 // tokens at the key whose mass before is below the share
-                double target = (double)p * (double)mass;
-                if (!(target >= 0.5)) target = 0.5;
-                w = weight(g.key);
-                u64 t = 0;
-                if (w > 0 && (double)g.before_w < target) {
-                    t = (u64)((target - (double)g.before_w) / (double)w);
-                    while (t > 0 && (double)(g.before_w + (t - 1) * w) >= target) --t;
-                    while ((double)(g.before_w + t * w) < target) ++t;
+                const u64 target = share_of(p, mass);
+                ties = w > 0 && g.before_w < target ? (target - g.before_w + w - 1) / w : 0;
+            }
+            // the index of the last of them
+            const float at = key_value(g.key);
+            u64 x = 0, y = 0, tx, ty, seen = 0, last = 0;
+            for (int c = tid; c < row.chunks; c += kSaThreads) {
+                float v[E];
+                row.load(c, v);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x += v[e] == at ? 1 : 0;
+            }
+            block_scan(x, y, tx, ty, s);
+            if (C > 1) {
+                exchange(tx, 0);
+                for (int i = 0; i < rank; ++i) seen += s.part[turn][i];
+            }
+            for (int c0 = 0; c0 < row.chunks; c0 += kSaThreads) {
+                const int c = c0 + tid;
+                float v[E];
+                u64 own = 0;
+                if (c < row.chunks) {
+                    row.load(c, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[e] = -INFINITY;
                 }
-                if (g.key != cut || t < ties) ties = t;
-                cut = g.key;
+#pragma unroll
+                for (int e = 0; e < E; ++e) own += v[e] == at ? 1 : 0;
+                x = own;
+                y = 0;
+                block_scan(x, y, tx, ty, s);
+                x += seen - own;                   // tokens at the cut before this chunk
+                seen += tx;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (v[e] == at && x++ < ties) last = (u64)(row.first(c) + e) + 1;
+            }
+            last = cluster_max(last);
+            return Cut{ranked(g.key, (int)last - 1), g.before_w + ties * w};
+        };
+        auto cut_of = [&](const Found& f, u64 mass) { return f.count <= kSaList ? sort_bin(f, mass) : refine_bin(f, mass); };
+        const Found f = find(by_k ? k : 0, 0, 0, 0);
+        if (!f.none) {
+            const Cut g = cut_of(f, f.total_w);
+            cut = g.rank;
+            if (f.by_count && by_p) {
+                // the share of the mass that top-k kept: the same histogram, unless the refinement took it
+                if (f.count > kSaList) histogram();
+                const Found fp = find(0, 0, 0, g.mass);
+                if (!fp.none) cut = max(cut, cut_of(fp, g.mass).rank);
             }
         }
     }
 
     // ---------------------------------------------------------------- the race over the row
-    // Tokens at the cut are counted in index order only if some of them fall out.
-    best = 0;
-    u64 seen = 0;
-    bool ranked = false;
-    if (ties != ~0ull) {
-        u64 x = 0, y = 0, tx, ty;
-        for (int c = tid; c < row.chunks; c += kSaThreads) {
-            uint32_t key[E];
-            row.load(c, key);
+    const float cut_value = key_value((uint32_t)(cut >> 32));
+    const int cut_index = index_of(cut);
+    // First by an estimate of the score (fast logarithm, product with 1 / T), each thread its best
+    // two; then exactly, where a thread's best is within the estimate's error of the block's.
+    const float floor_e = -floor_d * temp;
+    const float floor_lo = least > 0.f ? floor_e * 0.99999f : INFINITY, floor_hi = least > 0.f ? floor_e * 1.00001f : INFINITY;
+    const bool aligned = (reinterpret_cast<uintptr_t>(noise + row.first(0)) & 15u) == 0;
+    const float step = fminf(scaled.inv, 1e30f);
+    // the kept tokens of a chunk and their noise
+    auto fetch = [&](int c, float (&v)[E], float (&z)[E]) {
+        if (c >= row.chunks) return 0u;
+        row.load(c, v);
+        const int i0 = row.first(c);
+        unsigned kept = 0, edge = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) x += key[e] == cut ? 1 : 0;
+        for (int e = 0; e < E; ++e) {              // false for NaN and -inf
+            const bool in = v[e] > cut_value || (v[e] == cut_value && i0 + e <= cut_index);
+            const float d = below(v[e]);
+            kept |= in && !(d > floor_hi) ? 1u << e : 0u;
+            edge |= d > floor_lo ? 1u << e : 0u;
         }
-        block_scan(x, y, tx, ty, s);
-        if (C > 1) {
-            exchange(tx, 0);
-            tx = 0;
-            for (int i = 0; i < C; ++i) {
-                if (i < rank) seen += s.part[turn][i];
-                tx += s.part[turn][i];
+        if (kept & edge) {                         // as near to min-p's distance as rounding reaches
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if ((edge >> e) & 1 && !(scaled(below(v[e])) >= floor_d)) kept &= ~(1u << e);
+        }
+        if (aligned && kept == (1u << E) - 1) {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                const float4 u = __ldg(reinterpret_cast<const float4*>(noise + i0 + e));
+                z[e] = u.x;
+                z[e + 1] = u.y;
+                z[e + 2] = u.z;
+                z[e + 3] = u.w;
             }
-        }
-        ranked = tx > ties;
-    }
-    for (int c0 = 0; c0 < row.chunks; c0 += kSaThreads) {
-        const int c = c0 + tid;
-        uint32_t key[E];
-        u64 x = 0, y = 0, tx, ty, own = 0;
-        if (c < row.chunks) {
-            row.load(c, key);
-        } else {
+        } else if (kept) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) key[e] = 0;
+            for (int e = 0; e < E; ++e) z[e] = (kept >> e) & 1 ? __ldg(noise + i0 + e) : 1.f;
         }
-        if (ranked) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) own += key[e] == cut ? 1 : 0;
-            x = own;
-            block_scan(x, y, tx, ty, s);
-            x += seen - own;                   // tokens at the cut before this chunk
-            seen += tx;
-        }
+        return kept;
+    };
+    auto estimate = [&](float v, float z) {
+        const float sc = fmaf(-0.6931472f, __log2f(z), -below(v) * step);
+        return sc == sc ? sc : -INFINITY;
+    };
+    float first = -INFINITY, second = -INFINITY;
+    int first_i = -1;
+    float v[E], z[E];
+    unsigned kept = fetch(tid, v, z);
+    for (int c = tid; c < row.chunks; c += kSaThreads) {
+        float vn[E], zn[E];
+        const unsigned kept_next = fetch(c + kSaThreads, vn, zn);
         const int i0 = row.first(c);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            bool kept = key[e] >= cut;
-            if (ranked && key[e] == cut) kept = x++ < ties;
-            if (kept) {
-                const float d = dist(key[e]);
-                if (d >= floor_d || i0 + e == first) {
-                    const u64 v = race(d, i0 + e);
-                    best = v > best ? v : best;
-                }
-            }
+            const float sc = estimate(v[e], z[e]);
+            const bool in = (kept >> e) & 1, over = in && (sc > first || first_i < 0);
+            second = over ? first : (in ? fmaxf(second, sc) : second);
+            first = over ? sc : first;
+            first_i = over ? i0 + e : first_i;
+        }
+        kept = kept_next;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            v[e] = vn[e];
+            z[e] = zn[e];
         }
     }
-    best = cluster_max(best);
-    if (rank == 0 && tid == 0) a.tokens[r] = (int)(0xFFFFFFFFu - (uint32_t)best);
+    // the estimate is off by less than `off` (unusual temperatures: not relied on)
+    const float lead = key_value((uint32_t)block_max(first_i < 0 ? 0 : order_key(first), s));
+    auto may_win = [&](float sc) {
+        if (!scaled.usual || lead == -INFINITY) return true;
+        return sc > -INFINITY && !(sc + (2e-3f + 4e-6f * fabsf(sc)) < lead);
+    };
+    u64 best = 0;
+    auto exact = [&](float l, float noise_i, int i) {
+        float sc = scaled(below(l)) - logf(noise_i);
+        if (sc != sc) sc = -INFINITY;
+        best = max(best, ranked(order_key(sc), i));
+    };
+    if (first_i >= 0 && may_win(first)) {
+        if (may_win(second)) {                     // more than one of the thread's tokens
+            for (int c = tid; c < row.chunks; c += kSaThreads) {
+                kept = fetch(c, v, z);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if ((kept >> e) & 1 && may_win(estimate(v[e], z[e]))) exact(v[e], z[e], row.first(c) + e);
+            }
+        } else {
+            float l = as_float(row.base[first_i]);
+            exact(l, noise[first_i], first_i);
+        }
+    }
+    const u64 winner = cluster_max(best);
+    if (rank == 0 && tid == 0) a.tokens[r] = index_of(winner);
 }
 
 template <typename T>
@@ -558,7 +939,12 @@ nq_status sample_launch(SampleArgs a, int B, const StepDevice& d, cudaStream_t s
             return NQ_ERR_CUDA;
         set_for_device = dev;
     }
+    // Eight blocks a row while every block of the call can be resident at once (two an SM); past
+    // that fewer and larger slices, up to 40000 tokens (fp32: what fits shared memory), which saves
+    // cluster barriers. Measured, mixed settings: 64 rows of 152064 bf16 74 us at 8 and 4, 94 at 2;
+    // 256 rows of 128257 fp32 199 at 8, 163 at 4, 168 at 2; top-k 50 on 256 rows of 32001 61 at 8, 16 at 1.
     int C = kSaMaxCluster;
+    while (C > 1 && (long long)B * C > 2 * d.sms && a.V / (C / 2) <= 40000) C /= 2;
     a.slice = ((a.V + C - 1) / C + 15) / 16 * 16;
     const size_t bytes = ((size_t)a.slice * sizeof(T) + 15) / 16 * 16 + 16;
     a.resident = bytes <= (size_t)kSaSliceBytes;
