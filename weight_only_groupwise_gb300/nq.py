@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -21,13 +22,6 @@ STATUS = {0: "NQ_OK", -1: "NQ_ERR_NULL", -2: "NQ_ERR_SHAPE", -3: "NQ_ERR_ALIGN",
 class NqGroup(ctypes.Structure):
     """struct nq_group of include/nq.h."""
     _fields_ = [("Wq", ctypes.c_void_p), ("S", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("N", ctypes.c_int)]
-
-
-class NqKvCache(ctypes.Structure):
-    """struct nq_kv_cache of include/nq.h."""
-    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("block_stride", ctypes.c_longlong),
-                ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong), ("num_blocks", ctypes.c_int),
-                ("page", ctypes.c_int), ("heads", ctypes.c_int), ("dim", ctypes.c_int)]
 
 
 class NqError(RuntimeError):
@@ -455,56 +449,76 @@ class Program:
 
 # ---------------------------------------------------------------- serving step
 
+# These calls are short (a few microseconds on the GPU), so the checks here touch each tensor as
+# little as they can.
+
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_KV = struct.Struct("PPqqqiiii")    # struct nq_kv_cache
 
 
-def _dev(t, name: str, dtype, ndim: int) -> torch.Tensor:
-    """A CUDA tensor of this type and rank whose last dimension lies together."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.dim() != ndim or (
-            t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel() > 0):
-        raise ValueError(f"{name} must be a {ndim}-d CUDA tensor of {dtype}, its last dimension contiguous")
-    return t
+def _raw_stream(stream) -> int:
+    """The stream's handle; None: the current stream of the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _flat(t, name: str, dtype, n: int) -> torch.Tensor:
-    """A contiguous 1-d CUDA tensor of n elements."""
-    _dev(t, name, dtype, 1)
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
-    return t
+def _flat(t, name: str, dtype, n: int) -> int:
+    """The address of a contiguous CUDA tensor of n elements."""
+    try:
+        if t.dtype is dtype and t.numel() == n and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} elements of {dtype}")
 
 
-def _token_rows(t, name: str, dtype, heads: int, dim: int) -> int:
-    """Checks a [tokens][heads][dim] tensor whose token rows lie together; returns the stride
-    between tokens."""
-    _dev(t, name, dtype, 3)
-    if t.shape[1] != heads or t.shape[2] != dim or (heads > 1 and t.stride(1) != dim):
-        raise ValueError(f"{name} must be [tokens][{heads}][{dim}] with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+def _rows(t, name: str, dtype, rows: int):
+    """(address, columns, stride between rows) of a CUDA tensor [rows][columns], its rows contiguous."""
+    try:
+        if t.dtype is dtype and t.is_cuda:
+            n, cols = t.shape
+            stride, one = t.stride()
+            if n == rows and (one == 1 or cols <= 1 or n == 0):
+                return t.data_ptr(), cols, stride if n > 1 else max(cols, 1)
+    except (AttributeError, ValueError):
+        pass
+    raise ValueError(f"{name} must be a CUDA tensor of {dtype} with {rows} rows, each contiguous")
 
 
-def _kv_cache(k_cache, v_cache) -> NqKvCache:
-    """The paged cache given as two [num_blocks][page][heads][dim] tensors of equal strides (for a
-    cache stored [num_blocks][heads][page][dim], pass cache.transpose(1, 2))."""
-    if k_cache.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError("k_cache must be bfloat16 or float16")
-    _dev(k_cache, "k_cache", k_cache.dtype, 4)
-    _dev(v_cache, "v_cache", k_cache.dtype, 4)
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache must have one shape and the same strides")
-    blocks, page, heads, dim = k_cache.shape
-    bs, rs, hs, _ = k_cache.stride()
-    # the stride of a dimension of one element means nothing
-    return NqKvCache(k_cache.data_ptr(), v_cache.data_ptr(), bs if blocks > 1 else max(bs, dim), rs,
-                     hs if heads > 1 else dim, blocks, page, heads, dim)
+def _tokens(t, name: str, dtype, heads, dim):
+    """(address, tokens, heads, stride between tokens) of a CUDA tensor [tokens][heads][dim] whose
+    token rows lie together; heads None: any."""
+    try:
+        if t.dtype is dtype and t.is_cuda:
+            n, h, d = t.shape
+            st, sh, sd = t.stride()
+            if d == dim and (heads is None or h == heads) and sd == 1 and (sh == dim or h <= 1):
+                return t.data_ptr(), n, h, st if n > 1 else h * dim
+    except (AttributeError, ValueError):
+        pass
+    raise ValueError(f"{name} must be a CUDA tensor of {dtype}, [tokens][{heads or 'heads'}][{dim}] with contiguous "
+                     "token rows")
 
 
-def _rows2(t, name: str, rows: int) -> int:
-    """The stride between the rows of an int32 [rows][n] table."""
-    _dev(t, name, torch.int32, 2)
-    if t.shape[0] != rows:
-        raise ValueError(f"{name} must have {rows} rows, not {t.shape[0]}")
-    return t.stride(0) if rows > 1 else max(t.shape[1], 1)
+def _kv_cache(k_cache, v_cache):
+    """(struct nq_kv_cache, dtype, heads, dim) of a paged cache given as two
+    [num_blocks][page][heads][dim] tensors of equal strides (for a cache stored
+    [num_blocks][heads][page][dim], pass cache.transpose(1, 2))."""
+    try:
+        dt = k_cache.dtype
+        if (dt is torch.bfloat16 or dt is torch.float16) and v_cache.dtype is dt and k_cache.is_cuda and v_cache.is_cuda:
+            shape, strides = k_cache.shape, k_cache.stride()
+            blocks, page, heads, dim = shape
+            bs, rs, hs, ds = strides
+            if ds == 1 and v_cache.shape == shape and v_cache.stride() == strides:
+                # the stride of a dimension of one element means nothing
+                return (_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), bs if blocks > 1 else max(bs, dim), rs,
+                                 hs if heads > 1 else dim, blocks, page, heads, dim), dt, heads, dim)
+    except (AttributeError, ValueError):
+        pass
+    raise ValueError("k_cache and v_cache must be CUDA tensors [num_blocks][page][heads][dim] of bfloat16 or float16 "
+                     "with one shape, the same strides and contiguous last dimensions")
 
 
 def page_tables(lens, new_lens, free_blocks, num_free, block_table, page: int, max_tokens: int, out=None, stream=None):
@@ -514,41 +528,33 @@ def page_tables(lens, new_lens, free_blocks, num_free, block_table, page: int, m
     refused). All tensors int32 on the GPU (slots int64); `out`: the five outputs, to be reused."""
     i32 = torch.int32
     R = lens.numel()
-    _flat(lens, "lens", i32, R)
-    _flat(new_lens, "new_lens", i32, R)
-    _dev(free_blocks, "free_blocks", i32, 1)
-    _flat(num_free, "num_free", i32, 1)
-    stride = _rows2(block_table, "block_table", R)
+    table, max_blocks, stride = _rows(block_table, "block_table", i32, R)
     if out is None:
         dev = lens.device
         out = (torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev),
                torch.empty(max_tokens, dtype=i32, device=dev), torch.empty(max_tokens, dtype=torch.int64, device=dev),
                torch.empty(3, dtype=i32, device=dev))
     q_start, kv_lens, positions, slots, counts = out
-    _flat(q_start, "q_start", i32, R + 1)
-    _flat(kv_lens, "kv_lens", i32, R)
-    _flat(positions, "positions", i32, max_tokens)
-    _flat(slots, "slots", torch.int64, max_tokens)
-    _flat(counts, "counts", i32, 3)
-    _check(lib().nq_page_tables(lens.data_ptr(), new_lens.data_ptr(), R, free_blocks.data_ptr(), free_blocks.numel(),
-                                num_free.data_ptr(), page, block_table.data_ptr(), stride, block_table.shape[1],
-                                q_start.data_ptr(), kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(),
-                                max_tokens, counts.data_ptr(), _stream(stream)))
+    free = free_blocks.numel()
+    _check(lib().nq_page_tables(_flat(lens, "lens", i32, R), _flat(new_lens, "new_lens", i32, R), R,
+                                _flat(free_blocks, "free_blocks", i32, free), free, _flat(num_free, "num_free", i32, 1),
+                                page, table, stride, max_blocks, _flat(q_start, "q_start", i32, R + 1),
+                                _flat(kv_lens, "kv_lens", i32, R), _flat(positions, "positions", i32, max_tokens),
+                                _flat(slots, "slots", torch.int64, max_tokens), max_tokens,
+                                _flat(counts, "counts", i32, 3), _raw_stream(stream)))
     return out
 
 
 def kv_append(k, v, slots, k_cache, v_cache, stream=None) -> None:
     """Store new keys and values [tokens][heads][dim] at slots [tokens] (int64; block * page + row,
     -1 for none) of the paged cache [num_blocks][page][heads][dim] (nq_kv_append)."""
-    c = _kv_cache(k_cache, v_cache)
-    ks = _token_rows(k, "k", k_cache.dtype, c.heads, c.dim)
-    vs = _token_rows(v, "v", k_cache.dtype, c.heads, c.dim)
-    tokens = k.shape[0]
-    if v.shape[0] != tokens:
+    cache, dt, heads, dim = _kv_cache(k_cache, v_cache)
+    kp, tokens, _, ks = _tokens(k, "k", dt, heads, dim)
+    vp, tokens_v, _, vs = _tokens(v, "v", dt, heads, dim)
+    if tokens_v != tokens:
         raise ValueError("k and v must have the same number of tokens")
-    _flat(slots, "slots", torch.int64, tokens)
-    _check(lib().nq_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), tokens, ctypes.byref(c),
-                              _stream(stream)))
+    _check(lib().nq_kv_append(kp, ks, vp, vs, _flat(slots, "slots", torch.int64, tokens), tokens, cache,
+                              _raw_stream(stream)))
 
 
 def attn_paged(q, k_cache, v_cache, block_table, q_start, kv_lens, scale: float = None, window: int = 0,
@@ -557,26 +563,19 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, kv_lens, scale: float 
     [num_blocks][page][heads][dim] (nq_attn_paged): block_table [R][max_blocks], q_start [R+1]
     and kv_lens [R] (int32, as page_tables gives them). scale defaults to dim ** -0.5; window > 0
     limits a token to the last `window` keys and the first `sinks`. Returns out [tokens][q_heads][dim]."""
-    c = _kv_cache(k_cache, v_cache)
-    dt = k_cache.dtype
-    _dev(q, "q", dt, 3)
-    tokens, heads, dim = q.shape
-    if dim != c.dim:
-        raise ValueError(f"q has head dimension {dim}, the cache {c.dim}")
-    qs = _token_rows(q, "q", dt, heads, dim)
+    cache, dt, _, dim = _kv_cache(k_cache, v_cache)
+    qp, tokens, heads, qs = _tokens(q, "q", dt, None, dim)
     if out is None:
         out = torch.empty((tokens, heads, dim), dtype=dt, device=q.device)
-    os_ = _token_rows(out, "out", dt, heads, dim)
-    if out.shape[0] != tokens:
+    op, tokens_o, _, os_ = _tokens(out, "out", dt, heads, dim)
+    if tokens_o != tokens:
         raise ValueError("out must have q's shape")
     R = kv_lens.numel()
-    _flat(kv_lens, "kv_lens", torch.int32, R)
-    _flat(q_start, "q_start", torch.int32, R + 1)
-    stride = _rows2(block_table, "block_table", R)
-    _check(lib().nq_attn_paged(q.data_ptr(), qs, ctypes.byref(c), block_table.data_ptr(), stride, block_table.shape[1],
-                               q_start.data_ptr(), kv_lens.data_ptr(), R, tokens, heads,
-                               dim ** -0.5 if scale is None else scale, window, sinks, _DTYPES[dt], out.data_ptr(), os_,
-                               _stream(stream)))
+    table, max_blocks, stride = _rows(block_table, "block_table", torch.int32, R)
+    _check(lib().nq_attn_paged(qp, qs, cache, table, stride, max_blocks, _flat(q_start, "q_start", torch.int32, R + 1),
+                               _flat(kv_lens, "kv_lens", torch.int32, R), R, tokens, heads,
+                               dim ** -0.5 if scale is None else scale, window, sinks, _DTYPES[dt], op, os_,
+                               _raw_stream(stream)))
     return out
 
 
@@ -590,22 +589,22 @@ def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, 
     temperature, top_k, top_p and min_p ([B] tensors, None for none) and noise [B][V] (float32,
     independent Exp(1) variates: `torch.empty_like(...).exponential_()`); see nq_sample. Returns
     int32 tokens [B], -1 for a row without a candidate."""
-    if logits.dtype not in _DTYPES:
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None:
         raise ValueError("logits must be bfloat16, float16 or float32")
-    _dev(logits, "logits", logits.dtype, 2)
-    _dev(noise, "noise", torch.float32, 2)
-    if noise.shape != logits.shape:
+    B, f32 = logits.shape[0], torch.float32
+    lp, V, stride = _rows(logits, "logits", logits.dtype, B)
+    np_, V_noise, noise_stride = _rows(noise, "noise", f32, B)
+    if V_noise != V:
         raise ValueError("noise must have the shape of logits")
-    B, V = logits.shape
     if out is None:
         out = torch.empty(B, dtype=torch.int32, device=logits.device)
-    _flat(out, "out", torch.int32, B)
-    settings = []
-    for t, name in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
-        settings.append(None if t is None else
-                        _flat(t, name, torch.int32 if name == "top_k" else torch.float32, B).data_ptr())
-    _check(lib().nq_sample(logits.data_ptr(), _DTYPES[logits.dtype], logits.stride(0) if B > 1 else V, noise.data_ptr(),
-                           noise.stride(0) if B > 1 else V, B, V, *settings, out.data_ptr(), _stream(stream)))
+    _check(lib().nq_sample(lp, dtype, stride, np_, noise_stride, B, V,
+                           None if temperature is None else _flat(temperature, "temperature", f32, B),
+                           None if top_k is None else _flat(top_k, "top_k", torch.int32, B),
+                           None if top_p is None else _flat(top_p, "top_p", f32, B),
+                           None if min_p is None else _flat(min_p, "min_p", f32, B),
+                           _flat(out, "out", torch.int32, B), _raw_stream(stream)))
     return out
 
 
