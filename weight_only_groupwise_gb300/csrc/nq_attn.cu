@@ -17,7 +17,7 @@ long long kv_cache_span(const nq_kv_cache* c);
 namespace {
 
 template <int D, bool BF16>
-cudaError_t attn_launch(const AttnArgs& a, int sms, cudaStream_t stream, bool pdl) {
+cudaError_t attn_launch(const AttnArgs& a, int blocks, cudaStream_t stream, bool pdl) {
     auto kern = attn_kernel<D, BF16>;
     static thread_local int set_for_device = -1;
     int dev = 0;
@@ -27,17 +27,22 @@ cudaError_t attn_launch(const AttnArgs& a, int sms, cudaStream_t stream, bool pd
         if (e != cudaSuccess) return e;
         set_for_device = dev;
     }
-    cudaError_t e = step_launch(kern, dim3(sms), dim3(kAttnThreads), AttnGeo<D>::kSmem, stream, pdl, 1, a);
+    cudaError_t e = step_launch(kern, dim3(blocks), dim3(kAttnThreads), AttnGeo<D>::kSmem, stream, pdl, 1, a);
     if (e != cudaSuccess) return e;
-    return step_launch(attn_join_kernel<D, BF16>, dim3(sms, kJoinBlocksY), dim3(kJoinThreads), 0, stream, pdl, 1, a);
+    // a block takes 32 items of a split with many parts; launched without dependent launch: waiting
+    // blocks slowed the kernel before them (one token over 4099 keys: 21.4 us with, 15.5 without)
+    const int rows = (a.tokens < a.tile_tokens ? a.tokens : a.tile_tokens) * a.group;
+    const int y = (rows * (D / 8) + 31) / 32;
+    return step_launch(attn_join_kernel<D, BF16>, dim3(blocks, y < kJoinBlocksY ? y : kJoinBlocksY), dim3(kJoinThreads), 0,
+                       stream, false, 1, a);
 }
 
 template <bool BF16>
-cudaError_t attn_launch_dim(int dim, const AttnArgs& a, int sms, cudaStream_t stream, bool pdl) {
+cudaError_t attn_launch_dim(int dim, const AttnArgs& a, int blocks, cudaStream_t stream, bool pdl) {
     switch (dim) {
-        case 64: return attn_launch<64, BF16>(a, sms, stream, pdl);
-        case 128: return attn_launch<128, BF16>(a, sms, stream, pdl);
-        default: return attn_launch<256, BF16>(a, sms, stream, pdl);
+        case 64: return attn_launch<64, BF16>(a, blocks, stream, pdl);
+        case 128: return attn_launch<128, BF16>(a, blocks, stream, pdl);
+        default: return attn_launch<256, BF16>(a, blocks, stream, pdl);
     }
 }
 
@@ -102,10 +107,21 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     if (st != NQ_OK) return st;
 
     alignas(64) AttnArgs a;
-    if (!encode_q_map(&a.qmap, q, q_stride, cache->dim, q_heads, tokens, q_heads / cache->heads,
-                      kAttnRows / (q_heads / cache->heads), dtype == NQ_BF16) ||
-        !encode_kv_map(&a.kmap, cache->K, cache, dtype == NQ_BF16, kAttnKeys) ||
-        !encode_kv_map(&a.vmap, cache->V, cache, dtype == NQ_BF16, cache->dim == 256 ? 64 : kAttnKeys))
+    const bool bf16 = dtype == NQ_BF16;
+    a.heads = cache->heads;
+    a.group = q_heads / cache->heads;
+    a.tile_tokens = kAttnRows / a.group;
+    a.gang = 1;
+    for (int g = 2; g <= a.heads && g <= d.sms; ++g)
+        if (a.heads % g == 0 && d.sms / g * g >= d.sms - d.sms / 16) a.gang = g;
+    const int blocks = d.sms / a.gang * a.gang;
+    a.few_tokens = 1;
+    while (a.few_tokens * a.group % 8 != 0) a.few_tokens *= 2;
+    if (a.few_tokens > a.tile_tokens) a.few_tokens = a.tile_tokens;
+    if (!encode_q_map(&a.qmap, q, q_stride, cache->dim, q_heads, tokens, a.group, a.tile_tokens, bf16) ||
+        !encode_q_map(&a.qfew, q, q_stride, cache->dim, q_heads, tokens, a.group, a.few_tokens, bf16) ||
+        !encode_kv_map(&a.kmap, cache->K, cache, bf16, kAttnKeys) ||
+        !encode_kv_map(&a.vmap, cache->V, cache, bf16, cache->dim == 256 ? 64 : kAttnKeys))
         return NQ_ERR_CUDA;
     a.out = static_cast<uint16_t*>(out);
     a.out_stride = out_stride;
@@ -115,9 +131,6 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     a.kv_lens = kv_lens;
     a.R = R;
     a.tokens = tokens;
-    a.heads = cache->heads;
-    a.group = q_heads / cache->heads;
-    a.tile_tokens = kAttnRows / a.group;
     a.page_shift = 0;
     while ((1 << a.page_shift) < cache->page) ++a.page_shift;
     a.max_keys = max_blocks * cache->page;
@@ -129,8 +142,8 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     a.ml = reinterpret_cast<float2*>(ws + kAttnErrBytes + (size_t)d.sms * kAttnSplitBytes);
     a.part = reinterpret_cast<float*>(a.ml + (size_t)d.sms * 2 * kAttnRows);
     a.wait_ns = d.wait_ns;
-    const cudaError_t e = dtype == NQ_BF16 ? attn_launch_dim<true>(cache->dim, a, d.sms, s, d.pdl)
-                                           : attn_launch_dim<false>(cache->dim, a, d.sms, s, d.pdl);
+    const cudaError_t e = bf16 ? attn_launch_dim<true>(cache->dim, a, blocks, s, d.pdl)
+                               : attn_launch_dim<false>(cache->dim, a, blocks, s, d.pdl);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 

@@ -13,9 +13,11 @@
 // multiples of 128, so a page (16..256 keys) never straddles two tiles unless it holds both.
 // Keys that no row of the query tile sees are not loaded, tile by tile.
 //
-// Work split. The (query tile, key tile) pairs of the whole call, in the order request, KV head,
-// query tile, key tile, are cut into one equal range per SM (stream-K): ragged lengths and few
-// rows need no other rule. A query tile whose keys are spread over several blocks is written as
+// Work split. KV heads are handled in gangs of blocks, a head a block (the largest divisor of the
+// heads that leaves at most 1/16 of the SMs without work), so that the rows of a page, which hold
+// all heads, are read from memory at about the same time. The (query tile, key tile) pairs of the
+// whole call, in the order request, gang of heads, query tile, key tile, are cut into one equal
+// range per gang (stream-K): ragged lengths and few rows need no other rule. A query tile whose keys are spread over several blocks is written as
 // fp32 partials with their maxima and sums; attn_join_kernel adds them in block order, so the
 // result does not depend on timing. Every block finds its range by itself from the lengths on the
 // device: no host copy of the lengths, no plan to keep, no waits between blocks.
@@ -33,8 +35,9 @@
 //   * warp 9 -- MMA issuer: S = Q K^T (both from shared memory), O += P V (P from TMEM, V from
 //     shared memory as the N-major operand). S is double buffered: the product of tile j + 1 is
 //     issued before that of P of tile j, so that the tensor cores work during the softmax.
-//   * warp 10 -- the query tile into shared memory, one TMA box a 64-column panel. Rows past the
-//     tile's own (other requests' tokens, or zeros) are computed and dropped.
+//   * warp 10 -- the query tile into shared memory, one TMA box a 64-column panel (small boxes where
+//     they are enough: a box of 128 rows costs a one-token call 1.5 us). Rows past the tile's own
+//     (other requests' tokens, zeros, leftovers) are computed and dropped.
 // TMEM: O in columns 0..dim-1, the S buffers (P over them) in columns 256.. and 384...
 //
 // Rows of V that no row of the tile sees (past the last key, before a window) may hold anything,
@@ -79,6 +82,7 @@ struct AttnGeo {
 
 struct AttnArgs {
     CUtensorMap qmap, kmap, vmap;      // qmap: {dim, query heads, tokens}, boxes of 64 x group x tile_tokens
+    CUtensorMap qfew;                  // the same with boxes of few_tokens
     uint16_t* out;
     long long out_stride;              // between tokens, elements
     const int* table;
@@ -86,7 +90,9 @@ struct AttnArgs {
     const int* q_start;
     const int* kv_lens;
     int R, tokens, heads, group;       // heads: KV heads; group: query heads per KV head
+    int gang;                          // blocks that take the heads of a range together
     int tile_tokens;                   // tokens of a query tile: 128 / group
+    int few_tokens;                    // tokens of a small box: the fewest whose rows are a multiple of 8
     int page_shift, max_keys;
     int window, sinks;                 // window 0: none, and then no sinks
     float scale_log2;                  // scale x log2(e)
@@ -110,6 +116,11 @@ __device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, int r) {
     q.n = min(max(e, q.q0), a.tokens) - q.q0;
     q.kv = min(max(a.kv_lens[r], 0), a.max_keys);
     return q;
+}
+
+// x / y for non-negative x and positive y, in 32 bits where they fit.
+__device__ __forceinline__ long long attn_div(long long x, long long y) {
+    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
 // A query tile: its tokens, and the key tiles it reads, kt(i) = i < first ? i : i + skip.
@@ -164,24 +175,20 @@ struct AttnWalk {
         k0 = from;
         k1 = (int)min((long long)units, from + left);
     }
+    // Begins the range u0..u1-1, whose first unit is of request r_ (units base..base + all - 1).
     // Whole warps call this: the lanes look for the first tile together.
-    __device__ __forceinline__ void start(const AttnArgs& a, const long long* upto, long long u0, long long u1) {
+    __device__ __forceinline__ void start(const AttnArgs& a, int r_, const AttnReq& rq_, long long base, long long all,
+                                          long long u0, long long u1) {
         left = u1 - u0;
         at = u0;
         if (left <= 0) return;
-        int lo = 0, hi = a.R - 1;      // the first request whose units pass u0
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (upto[mid] > u0)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        r = lo;
-        enter(a);
-        const long long base = r > 0 ? upto[r - 1] : 0, per = (upto[r] - base) / a.heads;
-        h = (int)((u0 - base) / per);
-        long long rem = (u0 - base) - h * per;
+        r = r_;
+        rq = rq_;
+        nqt = attn_tiles(a, rq);
+        const long long per = attn_div(all, a.heads / a.gang);
+        const int turn = (int)attn_div(u0 - base, per);
+        h = turn * a.gang + (int)(blockIdx.x % a.gang);
+        long long rem = (u0 - base) - turn * per;
         const int lane = threadIdx.x & 31;
         for (qt = 0;; qt += 32) {
             const int u = attn_tile_units(a, rq, qt + lane, nqt);
@@ -210,8 +217,9 @@ struct AttnWalk {
         if (left <= 0) return;
         if (++qt == nqt) {
             qt = 0;
-            if (++h == a.heads) {
-                h = 0;
+            h += a.gang;
+            if (h >= a.heads) {
+                h = (int)(blockIdx.x % a.gang);
                 do {
                     ++r;
                     enter(a);
@@ -401,44 +409,83 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         mbar_fence_init();
     }
     if (warp == 0) tmem_alloc(smem_u32(const_cast<int*>(flags) + 3), 512);
-    grid_launch_dependents();
     grid_dependency_wait();
 
-    // Units of all requests, scanned into the ring buffers (free until the first copies).
-    long long* const upto = reinterpret_cast<long long*>(attn_smem);
-    long long total = 0;
-    for (int r0 = 0; r0 < a.R; r0 += kAttnThreads) {
-        const int r = r0 + tid;
+    // The block's range of units. Up to 32 requests every warp scans by itself, one a lane; more are
+    // scanned by the block into the ring buffers (free until the first copies).
+    AttnWalk w;
+    long long total = 0, blocks;       // blocks: ranges with work
+    // no range is empty: the join takes every block from a tile's first to its last as a part
+    auto range = [&](long long& u0, long long& u1) {
+        const long long gangs = gridDim.x / a.gang, me = blockIdx.x / a.gang;
+        blocks = max(1ll, min(gangs, total));
+        u0 = min(attn_div(total * me, blocks), total);
+        u1 = min(attn_div(total * (me + 1), blocks), total);
+    };
+    long long u0, u1;
+    if (a.R <= 32) {
         AttnReq rq = {0, 0, 0};
-        if (r < a.R) rq = attn_req(a, r);
-        long long w = attn_units(a, rq, r < a.R) * a.heads;
+        if (lane < a.R) rq = attn_req(a, lane);
+        const long long mine = attn_units(a, rq, lane < a.R) * (a.heads / a.gang);
+        long long upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const long long u = __shfl_up_sync(0xFFFFFFFFu, w, d);
-            if (lane >= d) w += u;
+            const long long u = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += u;
         }
-        __syncthreads();               // the sums of the round before have been read
-        if (lane == 31) warp_sums[warp] = w;
-        __syncthreads();
-        long long before = total;
+        total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        range(u0, u1);
+        const int r = min(__popc(__ballot_sync(0xFFFFFFFFu, upto <= u0)), a.R - 1);
+        rq.q0 = __shfl_sync(0xFFFFFFFFu, rq.q0, r);
+        rq.n = __shfl_sync(0xFFFFFFFFu, rq.n, r);
+        rq.kv = __shfl_sync(0xFFFFFFFFu, rq.kv, r);
+        w.start(a, r, rq, __shfl_sync(0xFFFFFFFFu, upto - mine, r), __shfl_sync(0xFFFFFFFFu, mine, r), u0, u1);
+    } else {
+        long long* const upto = reinterpret_cast<long long*>(attn_smem);
+        for (int r0 = 0; r0 < a.R; r0 += kAttnThreads) {
+            const int r = r0 + tid;
+            AttnReq rq = {0, 0, 0};
+            if (r < a.R) rq = attn_req(a, r);
+            long long x = attn_units(a, rq, r < a.R) * (a.heads / a.gang);
 #pragma unroll
-        for (int i = 0; i < kAttnThreads / 32; ++i) {
-            const long long s = warp_sums[i];
-            if (i < warp) before += s;
-            total += s;
+            for (int d = 1; d < 32; d *= 2) {
+                const long long u = __shfl_up_sync(0xFFFFFFFFu, x, d);
+                if (lane >= d) x += u;
+            }
+            __syncthreads();           // the sums of the round before have been read
+            if (lane == 31) warp_sums[warp] = x;
+            __syncthreads();
+            long long before = total;
+#pragma unroll
+            for (int i = 0; i < kAttnThreads / 32; ++i) {
+                const long long s = warp_sums[i];
+                if (i < warp) before += s;
+                total += s;
+            }
+            if (r < a.R) upto[r] = before + x;
         }
-        if (r < a.R) upto[r] = before + w;
+        __syncthreads();
+        range(u0, u1);
+        if (u0 < u1) {
+            int lo = 0, hi = a.R - 1;  // the first request whose units pass u0
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (upto[mid] > u0)
+                    hi = mid;
+                else
+                    lo = mid + 1;
+            }
+            const long long base = lo > 0 ? upto[lo - 1] : 0;
+            w.start(a, lo, attn_req(a, lo), base, upto[lo] - base, u0, u1);
+        } else {
+            w.left = 0;
+        }
+        fence_proxy_async_smem();      // the scan's buffers go to the copy engine
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)flags[3];
-    AttnWalk w;
-    // no range is empty: the join takes every block from a tile's first to its last as a part
-    const long long blocks = max(1ll, min((long long)gridDim.x, total));
-    w.start(a, upto, min(total * blockIdx.x / blocks, total), min(total * (blockIdx.x + 1) / blocks, total));
-    fence_proxy_async_smem();          // the scan's buffers go to the copy engine
-    __syncthreads();
 
     if (warp == kAttnProducer) {
         // ------------------------------------------------------------ producer
@@ -587,12 +634,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             if (w.tiles() == 0) continue;
             if (seg > 0) ok = mbar_wait(qfree, (seg - 1) & 1, flags, a.dev_err, wait_ns);
             if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(qfull, (uint32_t)(a.tile_tokens * a.group * D * 2));
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i)
-                    tma_load_3d(smem_u32(qmem) + i * (kAttnRows * 128), &a.qmap, 64 * i, w.h * a.group,
-                                w.rq.q0 + w.t.token0, qfull);
+            // few tokens: as many small boxes as they fill
+            const int box = a.few_tokens * a.group, n = (w.t.rows + box - 1) / box;
+            const bool few = n * box <= kAttnRows && n <= 4;
+            const int rows = few ? n * box : a.tile_tokens * a.group, copies = (few ? n : 1) * (D / 64);
+            if (lane == 0) mbar_arrive_expect_tx(qfull, (uint32_t)(rows * D * 2));
+            __syncwarp();
+            if (lane < copies) {
+                const int panel = lane % (D / 64), i = lane / (D / 64);
+                tma_load_3d(smem_u32(qmem) + panel * (kAttnRows * 128) + i * box * 128, few ? &a.qfew : &a.qmap, 64 * panel,
+                            w.h * a.group, w.rq.q0 + w.t.token0 + i * a.few_tokens, qfull);
             }
             __syncwarp();
             ++seg;
@@ -617,7 +668,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             const bool whole = w.k0 == 0 && w.k1 == w.units;
             const bool valid = row < t.rows;
             if (w.k0 == 0 && !whole) {
-                // the last unit's owner: ranges begin at floor(total c / blocks)
+                // the last unit's owner: ranges begin at floor(total c / blocks); it is the same block of its gang
                 const long long last = w.at + w.units - 1;
                 split0 = make_int4(w.r, w.h, w.qt, t.rows);
                 split_last = (int)(((last + 1) * blocks - 1) / total);
@@ -799,7 +850,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
 // ---------------------------------------------------------------- the join
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocksY = 16;   // blocks of a split's items
+constexpr int kJoinBlocksY = 16;   // most blocks of a split's items
 constexpr int kJoinParts = 8;      // most threads that share an item's partials
 
 // Adds the partials of the query tiles that were split over several blocks, in block order:
@@ -817,12 +868,12 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid
     const int tid = threadIdx.x;
     const int4 s = a.splits[2 * blockIdx.x];
     if (s.x >= 0) {
-        const int last = a.splits[2 * blockIdx.x + 1].x, count = last - (int)blockIdx.x + 1, rows = s.w;
+        const int last = a.splits[2 * blockIdx.x + 1].x, count = last - (int)blockIdx.x / a.gang + 1, rows = s.w;
         const AttnReq rq = attn_req(a, s.x);
         const float c = a.scale_log2;
         const int parts = count >= 8 ? 8 : (count >= 4 ? 4 : 2), per = kJoinThreads / parts;
         const int part = tid / per, items = rows * (D / 8);
-        for (int i0 = blockIdx.y * per; i0 < items; i0 += kJoinBlocksY * per) {
+        for (int i0 = blockIdx.y * per; i0 < items; i0 += gridDim.y * per) {
             const int item = i0 + tid % per, group = item / rows, row = item - group * rows;
             float m = -INFINITY, l = 0.f, o[8];
 #pragma unroll
@@ -830,7 +881,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid
             if (item < items) {
 #pragma unroll 2
                 for (int i = part; i < count; i += parts) {
-                    const int slot = 2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0);
+                    const int slot = 2 * ((int)blockIdx.x + i * a.gang) + (i == 0 ? 1 : 0);
                     const float2 ml = a.ml[slot * kAttnRows + row];
                     const float* src = a.part + ((size_t)slot * D + group * 8) * kAttnRows + row;
                     float v[8];
