@@ -150,6 +150,17 @@ def test_long_split_and_many_tiles(nq):
     check(nq, problem([1000, 17, 0], [400, 200, 333], 8, 2, 128, 16, BF, seed=3))
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim,page,dtype", [(32, 8, 128, 16, FP), (16, 16, 64, 32, BF), (12, 2, 256, 64, BF)])
+def test_many_requests(nq, heads, kv_heads, dim, page, dtype):
+    """More requests than a warp has lanes, each of many key tiles and several to a block."""
+    r = np.random.default_rng(dim)
+    p = problem(r.integers(0, 6000, 70), r.integers(0, 4, 70), heads, kv_heads, dim, page, dtype, seed=dim)
+    first = check(nq, p)
+    for _ in range(20):
+        assert torch.equal(first, nq.attn_paged(p["q"], p["k"], p["v"], p["table"], p["q_start"], p["kv"]))
+    nq.device_error()
+
+
 def test_large_scores_and_rescaling(nq):
     """Scores that grow along the keys: the running maximum moves in every tile."""
     p = problem([1500], [6], 4, 1, 128, 64, BF, seed=9)

@@ -22,16 +22,19 @@
 // result does not depend on timing. Every block finds its range by itself from the lengths on the
 // device: no host copy of the lengths, no plan to keep, no waits between blocks.
 //
-// Roles of a block's 11 warps (one block per SM):
+// Roles of a block's 12 warps (one block per SM):
 //   * warps 0..7 -- softmax: thread = row (TMEM lane) and half of the tile's 128 columns. The two
 //     halves of a row exchange maxima through shared memory. The accumulator is rescaled only
 //     when a row's maximum grows by more than 2^8 in the exponential's argument (p <= 256 stays
 //     exact enough in 16 bits, the sum is fp32); p is rounded to the 16-bit type of the cache
-//     for the second product: its error averages out below the output's own rounding.
-//   * warp 8 -- producer: TMA copies of key and value pages (a 4-D map of the cache: dim, row,
-//     head, block) into a ring of shared-memory slots, 128-byte swizzled. The page ids are the
-//     map's last coordinate: an id outside the cache reads as zeros instead of faulting, and no
-//     offset is formed in 32 bits.
+//     for the second product: its error averages out below the output's own rounding. (Alternate
+//     tiles for the two groups of four warps, each with an accumulator of its own, were slower: 267
+//     us against 253 for 64 one-token requests of 128 columns.)
+//   * warps 8 and 11 -- producers of K and of V: TMA copies of pages (a 4-D map of the cache: dim,
+//     row, head, block) into a ring of shared-memory slots, 128-byte swizzled, in the order the MMA
+//     warp consumes them: K 0, K 1, V 0, K 2, V 1, ... The page ids are the map's last coordinate:
+//     an id outside the cache reads as zeros instead of faulting, and no offset is formed in 32 bits.
+//     Two warps, because a page of 16 keys makes copies of 2 KB, whose issue was the limit.
 //   * warp 9 -- MMA issuer: S = Q K^T (both from shared memory), O += P V (P from TMEM, V from
 //     shared memory as the N-major operand). S is double buffered: the product of tile j + 1 is
 //     issued before that of P of tile j, so that the tensor cores work during the softmax.
@@ -55,9 +58,9 @@
 namespace nq {
 
 constexpr int kAttnKeys = 128;                    // keys of a tile
-constexpr int kAttnThreads = 11 * 32;
+constexpr int kAttnThreads = 12 * 32;
 constexpr int kAttnSoftmaxWarps = 8;
-constexpr int kAttnProducer = 8, kAttnMma = 9, kAttnLoader = 10;
+constexpr int kAttnProducerK = 8, kAttnMma = 9, kAttnLoader = 10, kAttnProducerV = 11;
 constexpr int kAttnMaxRequests = 8192;            // the scan's 8 bytes a request fit the tile buffers
 constexpr int kAttnSCol = 256;                    // TMEM column of the first S buffer
 constexpr int kAttnCtrlBytes = 3072;
@@ -375,13 +378,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     uint8_t* const qmem = attn_smem;
     uint8_t* const ring = attn_smem + Geo::kQBytes;
     uint8_t* const ctrl = ring + kSlots * Geo::kSlotBytes;
-    float* const red = reinterpret_cast<float*>(ctrl);                      // [2 tiles][2 halves][128]
+    float* const red = reinterpret_cast<float*>(ctrl);                      // [2][2 groups][128]
     uint64_t* const bars = reinterpret_cast<uint64_t*>(ctrl + 2048);
     // bars: full[8], empty[8], s_full[2], p_ready[2], pv_done[2], o_free, q_full, q_free, done
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 64, sfull0 = empty0 + 64, pready0 = sfull0 + 16;
     const uint32_t pvdone0 = pready0 + 16, ofree = pvdone0 + 16, qfull = ofree + 8, qfree = qfull + 8, done = qfree + 8;
     volatile int* const flags = reinterpret_cast<volatile int*>(ctrl + 2048 + 256);
-    // flags: [0] abort, [1] slots issued, [2] producer done, [3] TMEM base, [4] query tiles issued (-1: not done)
+    // flags: [0] abort, [3] TMEM base
     long long* const warp_sums = reinterpret_cast<long long*>(ctrl + 2048 + 256 + 64);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -402,9 +405,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         mbar_init(done, 1);
         // the swizzled tiles need a 1024-byte base
         flags[0] = (smem_u32(attn_smem) & 1023u) != 0;
-        flags[1] = 0;
-        flags[2] = 0;
-        flags[4] = -1;
         if (flags[0]) atomicOr(a.dev_err, kDevErrTimeout);
         mbar_fence_init();
     }
@@ -487,80 +487,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = (uint32_t)flags[3];
 
-    if (warp == kAttnProducer) {
-        // ------------------------------------------------------------ producer
-        const int kb = min(1 << a.page_shift, kAttnKeys), vb = min(1 << a.page_shift, kVK);
-        const int kboxes = kAttnKeys / kb, page_mask = (1 << a.page_shift) - 1;
-        const int row_bits = __ffs(kb) - 1, vrow_bits = __ffs(vb) - 1;
-        int seq = 0;
+    if (warp == kAttnProducerK || warp == kAttnProducerV) {
+        // ------------------------------------------------------------ producers
+        const bool is_v = warp == kAttnProducerV;
+        // a box is `rows` keys of a page; a slot holds slot_keys keys x slot_cols columns
+        const int slot_keys = is_v ? kVK : kAttnKeys, slot_cols = is_v ? D : kDK, slots = is_v ? kVS : kKS;
+        const int rows = min(1 << a.page_shift, slot_keys), row_bits = __ffs(rows) - 1;
+        const int page_rows = min(1 << a.page_shift, kAttnKeys), page_bits = __ffs(page_rows) - 1;
+        const int ids_of = kAttnKeys >> page_bits, page_mask = (1 << a.page_shift) - 1, panels = slot_cols / 64;
+        const CUtensorMap* const map = is_v ? &a.vmap : &a.kmap;
+        int base = 0;                      // slots filled by the segments before, by both producers
+        uint32_t filled = 0, parity = 0;   // per slot: whether this warp filled it, and the phase
         bool ok = flags[0] == 0;
-        // ids of the boxes of key tile kt, one a lane (-1, which reads as zeros, past the keys)
+        // block ids of key tile kt, one a lane (-1, which reads as zeros, past the keys)
         auto ids = [&](const AttnWalk& k, int kt) {
-            const int key = kt * kAttnKeys + lane * kb;
-            return lane < kboxes && key < k.t.hi ? __ldg(a.table + k.r * a.table_stride + (key >> a.page_shift)) : -1;
-        };
-        auto claim = [&](uint32_t& bar, uint32_t& dst, int bytes) {
-            const int slot = seq % kSlots;
-            if (seq >= kSlots) ok = mbar_wait(empty0 + 8 * slot, ((seq / kSlots) - 1) & 1, flags, a.dev_err, wait_ns);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) return;
-            bar = full0 + 8 * slot;
-            dst = smem_u32(ring + slot * Geo::kSlotBytes);
-            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)bytes);
-            __syncwarp();
-            ++seq;
-        };
-        auto load_k = [&](const AttnWalk& k, int kt, int id) {
-            const int key0 = kt * kAttnKeys;
-            const int boxes = min(kboxes, (k.t.hi - key0 + kb - 1) >> row_bits);
-            for (int s = 0; s < kKS && ok; ++s) {
-                uint32_t bar = 0, dst = 0;
-                claim(bar, dst, boxes * kb * kDK * 2);
-                if (!ok) break;
-                for (int o0 = 0; o0 < boxes * (kDK / 64); o0 += 32) {
-                    const int o = o0 + lane, box = o / (kDK / 64), panel = o % (kDK / 64);
-                    const int block = __shfl_sync(0xFFFFFFFFu, id, box & 31);
-                    if (o < boxes * (kDK / 64))
-                        tma_load_4d(dst + panel * (kAttnKeys * 128) + box * kb * 128, &a.kmap, s * kDK + panel * 64,
-                                    (key0 + box * kb) & page_mask, k.h, block, bar);
-                }
-            }
-        };
-        auto load_v = [&](const AttnWalk& k, int kt, int id) {
-            for (int s = 0; s < kVS && ok; ++s) {
-                const int key0 = kt * kAttnKeys + s * kVK;
-                const int boxes = max(0, min(kVK / vb, (k.t.hi - key0 + vb - 1) >> vrow_bits));
-                uint32_t bar = 0, dst = 0;
-                claim(bar, dst, boxes * vb * D * 2);
-                if (!ok) break;
-                for (int o0 = 0; o0 < boxes * (D / 64); o0 += 32) {
-                    const int o = o0 + lane, box = o / (D / 64), panel = o % (D / 64);
-                    const int block = __shfl_sync(0xFFFFFFFFu, id, ((s * kVK + box * vb) >> row_bits) & 31);
-                    if (o < boxes * (D / 64))
-                        tma_load_4d(dst + panel * (kVK * 128) + box * vb * 128, &a.vmap, panel * 64,
-                                    (key0 + box * vb) & page_mask, k.h, block, bar);
-                }
-            }
+            const int key = kt * kAttnKeys + lane * page_rows;
+            return lane < ids_of && key < k.t.hi ? __ldg(a.table + k.r * a.table_stride + (key >> a.page_shift)) : -1;
         };
         for (; w.more() && ok; w.next(a)) {
             const int n = w.tiles();
             if (n == 0) continue;
-            int id = ids(w, w.key_tile(0)), next_id = -1;
-            if (n > 1) next_id = ids(w, w.key_tile(1));
-            load_k(w, w.key_tile(0), id);
+            int id = ids(w, w.key_tile(0)), id_next = n > 1 ? ids(w, w.key_tile(1)) : -1;
             for (int j = 0; j < n && ok; ++j) {
-                const int after = j + 2 < n ? ids(w, w.key_tile(j + 2)) : -1;
-                if (j + 1 < n) load_k(w, w.key_tile(j + 1), next_id);
-                if (ok) load_v(w, w.key_tile(j), id);
-                id = next_id;
-                next_id = after;
+                const int id_after = j + 2 < n ? ids(w, w.key_tile(j + 2)) : -1;
+                int seq = base + (is_v ? kKS + j * (kKS + kVS) + (j + 1 < n ? kKS : 0)
+                                       : (j == 0 ? 0 : kKS + (j - 1) * (kKS + kVS)));
+                for (int s = 0; s < slots; ++s, ++seq) {
+                    const int slot = seq % kSlots;
+                    // (a barrier is at most one phase behind: what the fill before this one had to wait
+                    // for comes after the use of this slot two rounds ago)
+                    if (seq >= kSlots) ok = mbar_wait(empty0 + 8 * slot, ((seq / kSlots) - 1) & 1, flags, a.dev_err, wait_ns);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const int key0 = w.key_tile(j) * kAttnKeys + (is_v ? s * kVK : 0);
+                    const int boxes = max(0, min(slot_keys >> row_bits, (w.t.hi - key0 + rows - 1) >> row_bits));
+                    const uint32_t bar = full0 + 8 * slot, dst = smem_u32(ring + slot * Geo::kSlotBytes);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * rows * slot_cols * 2));
+                    __syncwarp();
+                    const int copies = boxes * panels, col0 = is_v ? 0 : s * kDK;
+                    for (int o0 = 0; o0 < copies; o0 += 32) {
+                        const int o = o0 + lane, box = o / panels, panel = o % panels;
+                        const int at = (is_v ? s * kVK : 0) + box * rows;
+                        const int block = __shfl_sync(0xFFFFFFFFu, id, (at >> page_bits) & 31);
+                        if (o < copies)
+                            tma_load_4d(dst + panel * (slot_keys * 128) + box * rows * 128, map, col0 + panel * 64,
+                                        (key0 + box * rows) & page_mask, w.h, block, bar);
+                    }
+                    filled |= 1u << slot;
+                    parity = (parity & ~(1u << slot)) | ((uint32_t)((seq / kSlots) & 1) << slot);
+                }
+                id = id_next;
+                id_next = id_after;
             }
+            base += n * (kKS + kVS);
         }
-        if (lane == 0) {
-            flags[1] = seq;
-            __threadfence_block();
-            flags[2] = 1;
-        }
+        if (!ok)                           // aborted: this warp's last copy into each slot
+            for (int i = 0; i < kSlots; ++i)
+                if ((filled >> i) & 1) mbar_wait_drain(full0 + 8 * i, (parity >> i) & 1, kDrainNs);
     } else if (warp == kAttnMma) {
         // ------------------------------------------------------------ MMA issuer
         constexpr uint32_t kIdescS = attn_idesc(BF16, kAttnKeys, false), kIdescO = attn_idesc(BF16, D, true);
@@ -648,7 +631,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             __syncwarp();
             ++seg;
         }
-        if (lane == 0) flags[4] = seg;
+        if (!ok && seg > 0) mbar_wait_drain(qfull, (seg - 1) & 1, kDrainNs);
     } else {
         // ------------------------------------------------------------ softmax
         // pv_done of a buffer may be waited for in any of its phases or in none: S of tile g is full
@@ -687,33 +670,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             bool ok = true;
             for (int j = 0; j < n; ++j, ++g) {
                 const int buf = g & 1, key0 = w.key_tile(j) * kAttnKeys;
-                const uint32_t s_col = lane_base + kAttnSCol + kAttnKeys * buf + 64 * half;
                 ok = mbar_wait(sfull0 + 8 * buf, (g >> 1) & 1, flags, a.dev_err, wait_ns);
                 tc_fence_after();
                 if (active) {
+                    const uint32_t s_col = lane_base + kAttnSCol + kAttnKeys * buf + 64 * half;
+                    const bool masked = key0 + kAttnKeys - 1 > t.pf || (a.window > 0 && key0 < t.pl - a.window + 1);
                     uint32_t v[64];
-                    tmem_ld32(s_col, v);
-                    tmem_ld32(s_col + 32, v + 32);
-                    tmem_wait_ld();
-                    if (key0 + kAttnKeys - 1 > t.pf || (a.window > 0 && key0 < t.pl - a.window + 1)) {
-                        // the row's keys among the thread's 64, one bit each
-                        const int kk = key0 + 64 * half;
-                        uint64_t see = low_bits(p - kk + 1);
-                        if (a.window > 0) see &= ~low_bits(p - a.window + 1 - kk) | low_bits(a.sinks - kk);
-                        const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+                    // 64 columns of S from `col`, which are the keys from kk on; keys that the row does
+                    // not see as -inf
+                    auto load = [&](uint32_t col, int kk) {
+                        tmem_ld32(col, v);
+                        tmem_ld32(col + 32, v + 32);
+                        tmem_wait_ld();
+                        if (masked) {
+                            uint64_t see = low_bits(p - kk + 1);
+                            if (a.window > 0) see &= ~low_bits(p - a.window + 1 - kk) | low_bits(a.sinks - kk);
+                            const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            v[i] = (s0 & (1u << i)) ? v[i] : 0xFF800000u;
-                            v[32 + i] = (s1 & (1u << i)) ? v[32 + i] : 0xFF800000u;
+                            for (int i = 0; i < 32; ++i) {
+                                v[i] = (s0 & (1u << i)) ? v[i] : 0xFF800000u;
+                                v[32 + i] = (s1 & (1u << i)) ? v[32 + i] : 0xFF800000u;
+                            }
                         }
-                    }
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    };
+                    auto maximum = [&]() {
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 64; i += 8)
+                        for (int i = 0; i < 64; i += 8)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(v[i + e]), __uint_as_float(v[i + 4 + e])));
-                    float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                            for (int e = 0; e < 4; ++e)
+                                m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(v[i + e]), __uint_as_float(v[i + 4 + e])));
+                        return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    };
+                    // p = 2^(c s + off), rounded, to column `col` of P; their sum joins l
+                    auto exponentials = [&](uint32_t col, float off) {
+                        uint32_t pk[32];
+                        const uint64_t cc = pack2(__float_as_uint(c), __float_as_uint(c));
+                        const uint64_t oo = pack2(__float_as_uint(off), __float_as_uint(off));
+                        uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) {
+                            const float2 x2 = unpack2(fma2(pack2(v[i], v[i + 1]), cc, oo));
+                            const float e0 = exp2_fast(x2.x), e1 = exp2_fast(x2.y);
+                            sum[(i / 2) & 3] = add2(sum[(i / 2) & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
+                            pk[i / 2] = pack16<BF16>(e0, e1);
+                        }
+                        const float2 s2 = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                        l += s2.x + s2.y;
+                        tmem_st32(col, pk);
+                    };
+                    load(s_col, key0 + 64 * half);
+                    float mx = maximum();
                     float* const x = red + (g & 1) * 256;
                     x[half * 128 + row] = mx;
                     named_bar_sync(1 + quarter, 64);
@@ -724,42 +731,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                         const float f = grow ? exp2_fast((m - mx) * c) : 1.f;
                         mbar_wait(pvdone0 + 8 * (buf ^ 1), ((g - 1) >> 1) & 1, flags, a.dev_err, wait_ns);
                         tc_fence_after();
+                        const uint32_t o_col = lane_base + half * (D / 2);
 #pragma unroll
                         for (int i = 0; i < D / 2; i += 32) {
                             uint32_t o[32];
-                            const uint32_t col = lane_base + half * (D / 2) + i;
-                            tmem_ld32(col, o);
+                            tmem_ld32(o_col + i, o);
                             tmem_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(col, o);
+                            tmem_st32(o_col + i, o);
                         }
                         l *= f;
                     }
                     if (grow) m = mx;
                     const float off = m == -INFINITY ? 0.f : -m * c;
-                    uint32_t pk[32];
-                    const uint64_t cc = pack2(__float_as_uint(c), __float_as_uint(c));
-                    const uint64_t oo = pack2(__float_as_uint(off), __float_as_uint(off));
-                    uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
-                        const float2 x2 = unpack2(fma2(pack2(v[i], v[i + 1]), cc, oo));
-                        const float e0 = exp2_fast(x2.x), e1 = exp2_fast(x2.y);
-                        sum[(i / 2) & 3] = add2(sum[(i / 2) & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
-                        pk[i / 2] = pack16<BF16>(e0, e1);
-                    }
-                    const float2 s2 = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-                    l += s2.x + s2.y;
-                    tmem_st32(s_col, pk);
+                    exponentials(s_col, off);
                     tmem_wait_st();
                 }
                 // V rows that no row sees: zeros
                 // (seen are the keys below the sinks and lo .. hi - 1)
                 if (key0 + kAttnKeys > t.hi || min(t.lo, key0 + kAttnKeys) > max(key0, a.sinks)) {
                     // the V slots of tile j: after K of the first tile, each tile's V follows the next tile's K
-                    // (the tile before is waited for first: a slot's barrier may be one fill behind otherwise)
-                    if (j > 0) ok = mbar_wait(pvdone0 + 8 * (buf ^ 1), ((g - 1) >> 1) & 1, flags, a.dev_err, wait_ns) && ok;
+                    // (with five slots the tile before is waited for first: a slot's barrier may be one
+                    // fill behind otherwise)
+                    if (j > 0)
+                        ok = mbar_wait(pvdone0 + 8 * (buf ^ 1), ((g - 1) >> 1) & 1, flags, a.dev_err, wait_ns) && ok;
                     const int v0 = seq + kKS + j * (kKS + kVS) + (j + 1 < n ? kKS : 0);
                     for (int s = 0; s < kVS; ++s)
                         ok = mbar_wait(full0 + 8 * ((v0 + s) % kSlots), ((v0 + s) / kSlots) & 1, flags, a.dev_err, wait_ns) && ok;
@@ -789,7 +785,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                 x[half * 128 + row] = l;
                 named_bar_sync(1 + quarter, 64);
                 l += x[(half ^ 1) * 128 + row];
-                named_bar_sync(1 + quarter, 64);   // the next tile's maxima use the same buffer
+                named_bar_sync(1 + quarter, 64);       // the next tile's maxima use the same buffer
                 const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
                 float* const pcol = a.part + ((size_t)slot * D + half * (D / 2)) * kAttnRows + row;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -827,18 +823,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         }
     }
 
-    if (flags[0] && tid == 0) {
-        // Aborted: wait (bounded) for the producer to stop, then for its last copy into each slot.
-        const uint64_t t0 = global_timer_ns();
-        while (!flags[2] && global_timer_ns() - t0 < 2 * kDrainNs) {
-        }
-        const int issued = flags[1];
-        for (int j = issued > kSlots ? issued - kSlots : 0; j < issued; ++j)
-            mbar_wait_drain(full0 + 8 * (j % kSlots), (j / kSlots) & 1, kDrainNs);
-        while (flags[4] < 0 && global_timer_ns() - t0 < 4 * kDrainNs) {
-        }
-        if (flags[4] > 0) mbar_wait_drain(qfull, (flags[4] - 1) & 1, kDrainNs);
-    }
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
