@@ -17,7 +17,9 @@
 // heads that leaves at most 1/16 of the SMs without work), so that the rows of a page, which hold
 // all heads, are read from memory at about the same time. The (query tile, key tile) pairs of the
 // whole call, in the order request, gang of heads, query tile, key tile, are cut into one equal
-// range per gang (stream-K): ragged lengths and few rows need no other rule. A query tile whose keys are spread over several blocks is written as
+// range per gang (stream-K): ragged lengths and few rows need no other rule. A boundary within
+// kAttnSnap units of a query tile's begin or end moves there, where a range is long enough to
+// take it: a split costs about as much as so many units (partials written, joined). A query tile whose keys are spread over several blocks is written as
 // fp32 partials with their maxima and sums; attn_join_kernel adds them in block order, so the
 // result does not depend on timing. Every block finds its range by itself from the lengths on the
 // device: no host copy of the lengths, no plan to keep, no waits between blocks.
@@ -63,11 +65,14 @@ constexpr int kAttnSoftmaxWarps = 8;
 constexpr int kAttnProducerK = 8, kAttnMma = 9, kAttnLoader = 10, kAttnProducerV = 11;
 constexpr int kAttnMaxRequests = 8192;            // the scan's 8 bytes a request fit the tile buffers
 constexpr int kAttnSCol = 256;                    // TMEM column of the first S buffer
+constexpr int kAttnMaxSlots = 8;
 constexpr int kAttnCtrlBytes = 3072;
+constexpr int kAttnSnap = 6;                      // units by which a range may grow or shrink to avoid a split
 constexpr float kAttnLazy = 8.f;                  // log2 of the growth that forces a rescale
 
 // Shared-memory geometry for a head dimension: the K slot holds 128 keys x min(D, 128) columns,
-// the V slot as many bytes: 128 keys x D, or 64 keys x 256.
+// the V slot as many bytes: 128 keys x D, or 64 keys x 256. (Slots of 16 KB, twice as many barrier
+// steps a tile, were slower: 635 us against 600 for a 2048-token chunk of 256 columns.)
 template <int D>
 struct AttnGeo {
     static constexpr int kDK = D < 128 ? D : 128;           // columns of a K slot
@@ -78,7 +83,7 @@ struct AttnGeo {
     static constexpr int kQBytes = kAttnRows * D * 2;
     static constexpr int kSlots = D == 256 ? 5 : (D == 128 ? 6 : 8);
     static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kAttnCtrlBytes;
-    static_assert(kSmem <= kSmemLimit, "shared memory");
+    static_assert(kSmem <= kSmemLimit && kSlots <= kAttnMaxSlots, "shared memory");
     static_assert(kVKeys * D * 2 == kSlotBytes, "one slot size");
     static_assert(kQBytes + kSlots * kSlotBytes >= kAttnMaxRequests * 8, "room for the scan");
 };
@@ -178,24 +183,21 @@ struct AttnWalk {
         k0 = from;
         k1 = (int)min((long long)units, from + left);
     }
-    // Begins the range u0..u1-1, whose first unit is of request r_ (units base..base + all - 1).
-    // Whole warps call this: the lanes look for the first tile together.
-    __device__ __forceinline__ void start(const AttnArgs& a, int r_, const AttnReq& rq_, long long base, long long all,
-                                          long long u0, long long u1) {
-        left = u1 - u0;
-        at = u0;
-        if (left <= 0) return;
+    // Finds unit u: of request r_, whose units are base..base + all - 1. Whole warps call this: the
+    // lanes look for the query tile together. Returns the unit's place in its tile.
+    __device__ __forceinline__ int find(const AttnArgs& a, int r_, const AttnReq& rq_, long long base, long long all,
+                                        long long u) {
         r = r_;
         rq = rq_;
         nqt = attn_tiles(a, rq);
         const long long per = attn_div(all, a.heads / a.gang);
-        const int turn = (int)attn_div(u0 - base, per);
+        const int turn = (int)attn_div(u - base, per);
         h = turn * a.gang + (int)(blockIdx.x % a.gang);
-        long long rem = (u0 - base) - turn * per;
+        long long rem = (u - base) - turn * per;
         const int lane = threadIdx.x & 31;
         for (qt = 0;; qt += 32) {
-            const int u = attn_tile_units(a, rq, qt + lane, nqt);
-            long long x = u;
+            const int n_ = attn_tile_units(a, rq, qt + lane, nqt);
+            long long x = n_;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
                 const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
@@ -204,14 +206,30 @@ struct AttnWalk {
             const unsigned past = __ballot_sync(0xFFFFFFFFu, x > rem);
             if (past || qt + 32 >= nqt) {
                 const int src = past ? __ffs(past) - 1 : 0;
-                rem -= __shfl_sync(0xFFFFFFFFu, x - u, src);
+                rem -= __shfl_sync(0xFFFFFFFFu, x - n_, src);
                 qt += src;
                 break;
             }
             rem -= __shfl_sync(0xFFFFFFFFu, x, 31);
         }
         t = attn_tile(a, rq, qt);
-        cut((int)rem);
+        units = max(1, t.n);
+        return (int)rem;
+    }
+    // Where a boundary `from` units into this tile is: moved to the tile's begin or end if that is near.
+    __device__ __forceinline__ int snapped(int from, int snap) const {
+        return from <= snap ? 0 : (units - from <= snap ? units : from);
+    }
+    // Begins a range of n units at unit u, `from` units into the tile found.
+    __device__ __forceinline__ void begin(const AttnArgs& a, long long u, int from, long long n) {
+        at = u;
+        left = n;
+        k0 = k1 = units;
+        if (left <= 0) return;
+        if (from == units)
+            next(a);                   // the next tile's begin
+        else
+            cut(from);
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
     __device__ __forceinline__ void next(const AttnArgs& a) {
@@ -381,7 +399,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     float* const red = reinterpret_cast<float*>(ctrl);                      // [2][2 groups][128]
     uint64_t* const bars = reinterpret_cast<uint64_t*>(ctrl + 2048);
     // bars: full[8], empty[8], s_full[2], p_ready[2], pv_done[2], o_free, q_full, q_free, done
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 64, sfull0 = empty0 + 64, pready0 = sfull0 + 16;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kAttnMaxSlots, sfull0 = empty0 + 8 * kAttnMaxSlots, pready0 = sfull0 + 16;
     const uint32_t pvdone0 = pready0 + 16, ofree = pvdone0 + 16, qfull = ofree + 8, qfree = qfull + 8, done = qfree + 8;
     volatile int* const flags = reinterpret_cast<volatile int*>(ctrl + 2048 + 256);
     // flags: [0] abort, [3] TMEM base
@@ -414,15 +432,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     // The block's range of units. Up to 32 requests every warp scans by itself, one a lane; more are
     // scanned by the block into the ring buffers (free until the first copies).
     AttnWalk w;
-    long long total = 0, blocks;       // blocks: ranges with work
-    // no range is empty: the join takes every block from a tile's first to its last as a part
-    auto range = [&](long long& u0, long long& u1) {
+    w.left = 0;
+    long long total = 0, blocks = 1;   // blocks: ranges with work
+    int snap = 0;
+    // locate(u): finds unit u in w, and returns its place in its tile
+    auto range = [&](auto locate) {
         const long long gangs = gridDim.x / a.gang, me = blockIdx.x / a.gang;
+        // no range is empty but between whole tiles: the join takes every block from a tile's first to
+        // its last as a part
         blocks = max(1ll, min(gangs, total));
-        u0 = min(attn_div(total * me, blocks), total);
-        u1 = min(attn_div(total * (me + 1), blocks), total);
+        snap = attn_div(total, blocks) > 2 * kAttnSnap ? kAttnSnap : 0;
+        long long u0 = min(attn_div(total * me, blocks), total), u1 = min(attn_div(total * (me + 1), blocks), total);
+        if (u0 >= u1) return;
+        if (u1 < total && snap > 0) {
+            const int from = locate(u1);
+            u1 += w.snapped(from, snap) - from;
+        }
+        const int from = locate(u0), to = w.snapped(from, snap);
+        u0 += to - from;
+        w.begin(a, u0, to, u1 - u0);
     };
-    long long u0, u1;
     if (a.R <= 32) {
         AttnReq rq = {0, 0, 0};
         if (lane < a.R) rq = attn_req(a, lane);
@@ -434,12 +463,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             if (lane >= d) upto += u;
         }
         total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        range(u0, u1);
-        const int r = min(__popc(__ballot_sync(0xFFFFFFFFu, upto <= u0)), a.R - 1);
-        rq.q0 = __shfl_sync(0xFFFFFFFFu, rq.q0, r);
-        rq.n = __shfl_sync(0xFFFFFFFFu, rq.n, r);
-        rq.kv = __shfl_sync(0xFFFFFFFFu, rq.kv, r);
-        w.start(a, r, rq, __shfl_sync(0xFFFFFFFFu, upto - mine, r), __shfl_sync(0xFFFFFFFFu, mine, r), u0, u1);
+        range([&](long long u) {
+            const int r = min(__popc(__ballot_sync(0xFFFFFFFFu, upto <= u)), a.R - 1);
+            AttnReq q;
+            q.q0 = __shfl_sync(0xFFFFFFFFu, rq.q0, r);
+            q.n = __shfl_sync(0xFFFFFFFFu, rq.n, r);
+            q.kv = __shfl_sync(0xFFFFFFFFu, rq.kv, r);
+            return w.find(a, r, q, __shfl_sync(0xFFFFFFFFu, upto - mine, r), __shfl_sync(0xFFFFFFFFu, mine, r), u);
+        });
     } else {
         long long* const upto = reinterpret_cast<long long*>(attn_smem);
         for (int r0 = 0; r0 < a.R; r0 += kAttnThreads) {
@@ -465,21 +496,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             if (r < a.R) upto[r] = before + x;
         }
         __syncthreads();
-        range(u0, u1);
-        if (u0 < u1) {
-            int lo = 0, hi = a.R - 1;  // the first request whose units pass u0
+        range([&](long long u) {
+            int lo = 0, hi = a.R - 1;  // the first request whose units pass u
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (upto[mid] > u0)
+                if (upto[mid] > u)
                     hi = mid;
                 else
                     lo = mid + 1;
             }
             const long long base = lo > 0 ? upto[lo - 1] : 0;
-            w.start(a, lo, attn_req(a, lo), base, upto[lo] - base, u0, u1);
-        } else {
-            w.left = 0;
-        }
+            return w.find(a, lo, attn_req(a, lo), base, upto[lo] - base, u);
+        });
         fence_proxy_async_smem();      // the scan's buffers go to the copy engine
     }
     tc_fence_before();
@@ -651,10 +679,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             const bool whole = w.k0 == 0 && w.k1 == w.units;
             const bool valid = row < t.rows;
             if (w.k0 == 0 && !whole) {
-                // the last unit's owner: ranges begin at floor(total c / blocks); it is the same block of its gang
-                const long long last = w.at + w.units - 1;
+                // the last unit's owner: ranges begin at floor(total c / blocks), and one that begins near
+                // the tile's end at that; it is the same block of its gang
+                const long long end = w.at + w.units;
+                long long c = (end * blocks - 1) / total;
+                const int from = (int)max(0ll, attn_div(total * c, blocks) - w.at);
+                if (w.snapped(from, snap) == w.units) --c;
                 split0 = make_int4(w.r, w.h, w.qt, t.rows);
-                split_last = (int)(((last + 1) * blocks - 1) / total);
+                split_last = (int)c;
             }
             uint16_t* const orow = a.out + (w.rq.q0 + t.token0 + row_token) * a.out_stride +
                                    (long long)(w.h * a.group + row_head) * D + half * (D / 2);
@@ -842,7 +874,7 @@ constexpr int kJoinParts = 8;      // most threads that share an item's partials
 // (x, *) share the items of the tile that block x of the attention kernel opened, neighbouring lanes
 // taking neighbouring rows (partials are stored column by column). Up to 8 threads share an
 // item's partials, each with a running maximum, so that few rows with many partials are read in
-// parallel. Bound by latency: two rounds of loads. The same blocks write zeros to the output rows
+// parallel. Bound by latency: two or three rounds of loads. The same blocks write zeros to the output rows
 // past the last request's.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid_constant__ AttnArgs a) {
@@ -855,7 +887,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid
         const int last = a.splits[2 * blockIdx.x + 1].x, count = last - (int)blockIdx.x / a.gang + 1, rows = s.w;
         const AttnReq rq = attn_req(a, s.x);
         const float c = a.scale_log2;
-        const int parts = count >= 8 ? 8 : (count >= 4 ? 4 : 2), per = kJoinThreads / parts;
+        const int parts = count >= 8 ? 8 : (count >= 4 ? 4 : 1), per = kJoinThreads / parts;
         const int part = tid / per, items = rows * (D / 8);
         for (int i0 = blockIdx.y * per; i0 < items; i0 += gridDim.y * per) {
             const int item = i0 + tid % per, group = item / rows, row = item - group * rows;
@@ -863,7 +895,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = 0.f;
             if (item < items) {
-#pragma unroll 2
+#pragma unroll 3
                 for (int i = part; i < count; i += parts) {
                     const int slot = 2 * ((int)blockIdx.x + i * a.gang) + (i == 0 ? 1 : 0);
                     const float2 ml = a.ml[slot * kAttnRows + row];
