@@ -161,6 +161,23 @@ def test_many_requests(nq, heads, kv_heads, dim, page, dtype):
     nq.device_error()
 
 
+@pytest.mark.parametrize("old,new,heads,kv_heads,page,dtype", [
+    ([0], [700], 24, 4, 64, BF), ([0], [300], 64, 1, 64, FP), ([700], [800], 24, 4, 16, BF),
+    ([100, 0, 5000], [250, 129, 400], 24, 4, 64, BF), ([3000], [2100], 8, 8, 256, BF), ([1], [1100], 16, 2, 32, FP),
+    ([64, 900, 0, 30], [1200, 1, 0, 500], 10, 1, 128, BF), ([20000], [700], 24, 4, 64, BF)])
+def test_prompts_of_256_columns(nq, old, new, heads, kv_heads, page, dtype):
+    """Calls large enough that two blocks share a query tile."""
+    p = problem(old, new, heads, kv_heads, 256, page, dtype, seed=sum(new))
+    first = check(nq, p)
+    assert torch.equal(first, check(nq, p))
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 4), (300, 130), (4096, 0), (4097, 4), (5000, 200)])
+def test_prompts_of_256_columns_with_windows(nq, window, sinks):
+    p = problem([6000, 0], [500, 300], 24, 4, 256, 64, BF, seed=window)
+    check(nq, p, window, sinks)
+
+
 def test_large_scores_and_rescaling(nq):
     """Scores that grow along the keys: the running maximum moves in every tile."""
     p = problem([1500], [6], 4, 1, 128, 64, BF, seed=9)

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "nq.h"
@@ -16,34 +17,77 @@ long long kv_cache_span(const nq_kv_cache* c);
 
 namespace {
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool PAIR>
 cudaError_t attn_launch(const AttnArgs& a, int blocks, cudaStream_t stream, bool pdl) {
-    auto kern = attn_kernel<D, BF16>;
+    auto kern = attn_kernel<D, BF16, PAIR>;
     static thread_local int set_for_device = -1;
     int dev = 0;
     cudaGetDevice(&dev);
     if (set_for_device != dev) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnGeo<D>::kSmem);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnGeo<D, PAIR>::kSmem);
         if (e != cudaSuccess) return e;
         set_for_device = dev;
     }
-    cudaError_t e = step_launch(kern, dim3(blocks), dim3(kAttnThreads), AttnGeo<D>::kSmem, stream, pdl, 1, a);
+    cudaError_t e = step_launch(kern, dim3(blocks), dim3(kAttnThreads), AttnGeo<D, PAIR>::kSmem, stream, pdl && !PAIR,
+                                PAIR ? 2 : 1, a);
     if (e != cudaSuccess) return e;
     // a block takes 32 items of a split with many parts; launched without dependent launch: waiting
     // blocks slowed the kernel before them (one token over 4099 keys: 21.4 us with, 15.5 without)
-    const int rows = (a.tokens < a.tile_tokens ? a.tokens : a.tile_tokens) * a.group;
+    const int rows = (a.tokens < a.block_tokens ? a.tokens : a.block_tokens) * a.group;
     const int y = (rows * (D / 8) + 31) / 32;
     return step_launch(attn_join_kernel<D, BF16>, dim3(blocks, y < kJoinBlocksY ? y : kJoinBlocksY), dim3(kJoinThreads), 0,
                        stream, false, 1, a);
 }
 
 template <bool BF16>
-cudaError_t attn_launch_dim(int dim, const AttnArgs& a, int blocks, cudaStream_t stream, bool pdl) {
+cudaError_t attn_launch_dim(int dim, bool pair, const AttnArgs& a, int blocks, cudaStream_t stream, bool pdl) {
     switch (dim) {
-        case 64: return attn_launch<64, BF16>(a, blocks, stream, pdl);
-        case 128: return attn_launch<128, BF16>(a, blocks, stream, pdl);
-        default: return attn_launch<256, BF16>(a, blocks, stream, pdl);
+        case 64: return attn_launch<64, BF16, false>(a, blocks, stream, pdl);
+        case 128: return attn_launch<128, BF16, false>(a, blocks, stream, pdl);
+        default:
+            return pair ? attn_launch<256, BF16, true>(a, blocks, stream, pdl)
+                        : attn_launch<256, BF16, false>(a, blocks, stream, pdl);
     }
+}
+
+// Pairs of blocks that can be resident at once (queried once).
+int pair_capacity(int sms) {
+    static std::atomic<int> known{-1};
+    int n = known.load();
+    if (n >= 0) return n;
+    auto kern = attn_kernel<256, true, true>;
+    constexpr int smem = AttnGeo<256, true>::kSmem;
+    n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(sms / 2 * 2);
+        cfg.blockDim = dim3(kAttnThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+    }
+    if (n > sms / 2) n = sms / 2;
+    known.store(n);
+    return n;
+}
+
+// Whether a call of 256 columns runs on pairs of blocks: where its requests bring on average rows
+// for two pairs' query tiles or more, all its heads enough to fill the SMs, and no window makes the tiles
+// short (the lengths are on the device; any split of the tokens is right either way). Measured,
+// pairs against single blocks, 24 query and 4 KV heads: 2048 tokens over 16384 keys 534 us
+// against 566 (page 16: 535, 670), 8 x 128 over up to 8000 173 against 204, 4 x 1000 without a cache 129, 132; but
+// 512 over 4096 73, 72, 86 over 16000 69, 63, and 700 in a window of 1024 58, 52.
+bool attn_uses_pairs(int tokens, int R, int group, int q_heads, int window) {
+    return (long long)tokens * group >= 512ll * R && (long long)tokens * q_heads >= 16384 && (window == 0 || window >= 4096);
 }
 
 bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -110,18 +154,23 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     const bool bf16 = dtype == NQ_BF16;
     a.heads = cache->heads;
     a.group = q_heads / cache->heads;
-    a.tile_tokens = kAttnRows / a.group;
+    a.block_tokens = kAttnRows / a.group;
+    const int pairs = cache->dim == 256 && attn_uses_pairs(tokens, R, a.group, q_heads, window) ? pair_capacity(d.sms) : 0;
+    const bool pair = pairs > 0;
+    const int units = pair ? pairs : d.sms;
+    a.tile_tokens = pair ? 2 * a.block_tokens : a.block_tokens;
     a.gang = 1;
-    for (int g = 2; g <= a.heads && g <= d.sms; ++g)
-        if (a.heads % g == 0 && d.sms / g * g >= d.sms - d.sms / 16) a.gang = g;
-    const int blocks = d.sms / a.gang * a.gang;
+    for (int g = 2; g <= a.heads && g <= units; ++g)
+        if (a.heads % g == 0 && units / g * g >= units - units / 16) a.gang = g;
+    a.stride = pair ? 2 * a.gang : a.gang;
+    const int blocks = units / a.gang * a.stride;
     a.few_tokens = 1;
     while (a.few_tokens * a.group % 8 != 0) a.few_tokens *= 2;
-    if (a.few_tokens > a.tile_tokens) a.few_tokens = a.tile_tokens;
-    if (!encode_q_map(&a.qmap, q, q_stride, cache->dim, q_heads, tokens, a.group, a.tile_tokens, bf16) ||
+    if (a.few_tokens > a.block_tokens) a.few_tokens = a.block_tokens;
+    if (!encode_q_map(&a.qmap, q, q_stride, cache->dim, q_heads, tokens, a.group, a.block_tokens, bf16) ||
         !encode_q_map(&a.qfew, q, q_stride, cache->dim, q_heads, tokens, a.group, a.few_tokens, bf16) ||
-        !encode_kv_map(&a.kmap, cache->K, cache, bf16, kAttnKeys) ||
-        !encode_kv_map(&a.vmap, cache->V, cache, bf16, cache->dim == 256 ? 64 : kAttnKeys))
+        !encode_kv_map(&a.kmap, cache->K, cache, bf16, pair ? 64 : kAttnKeys) ||
+        !encode_kv_map(&a.vmap, cache->V, cache, bf16, cache->dim == 256 && !pair ? 64 : kAttnKeys))
         return NQ_ERR_CUDA;
     a.out = static_cast<uint16_t*>(out);
     a.out_stride = out_stride;
@@ -142,8 +191,8 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     a.ml = reinterpret_cast<float2*>(ws + kAttnErrBytes + (size_t)d.sms * kAttnSplitBytes);
     a.part = reinterpret_cast<float*>(a.ml + (size_t)d.sms * 2 * kAttnRows);
     a.wait_ns = d.wait_ns;
-    const cudaError_t e = bf16 ? attn_launch_dim<true>(cache->dim, a, blocks, s, d.pdl)
-                               : attn_launch_dim<false>(cache->dim, a, blocks, s, d.pdl);
+    const cudaError_t e = bf16 ? attn_launch_dim<true>(cache->dim, pair, a, blocks, s, d.pdl)
+                               : attn_launch_dim<false>(cache->dim, pair, a, blocks, s, d.pdl);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 

@@ -24,6 +24,12 @@
 // result does not depend on timing. Every block finds its range by itself from the lengths on the
 // device: no host copy of the lengths, no plan to keep, no waits between blocks.
 //
+// Pairs. For prompts of 256 columns (attn_uses_pairs) two blocks of a cluster take a query tile of 256
+// rows: each its 128 rows of Q, S, P and O, half of the keys of a K tile, half of the columns of a
+// V tile, and the even block issues the products for both (cta_group::2). That halves the copies
+// and the reads of K and V from shared memory, which alone take a block longer than its products
+// (320 KB a key tile at 128 bytes a cycle: 2560 cycles, against 2048).
+//
 // Roles of a block's 12 warps (one block per SM):
 //   * warps 0..7 -- softmax: thread = row (TMEM lane) and half of the tile's 128 columns. The two
 //     halves of a row exchange maxima through shared memory. The accumulator is rescaled only
@@ -73,18 +79,20 @@ constexpr float kAttnLazy = 8.f;                  // log2 of the growth that for
 // Shared-memory geometry for a head dimension: the K slot holds 128 keys x min(D, 128) columns,
 // the V slot as many bytes: 128 keys x D, or 64 keys x 256. (Slots of 16 KB, twice as many barrier
 // steps a tile, were slower: 635 us against 600 for a 2048-token chunk of 256 columns.)
-template <int D>
+template <int D, bool PAIR = false>
 struct AttnGeo {
-    static constexpr int kDK = D < 128 ? D : 128;           // columns of a K slot
+    static constexpr int kDK = PAIR || D < 128 ? D : 128;    // columns of a K slot
+    static constexpr int kKKeys = PAIR ? 64 : 128;           // keys of a K slot
     static constexpr int kKSlots = D / kDK;                  // K slots of a key tile
-    static constexpr int kVKeys = D == 256 ? 64 : 128;       // keys of a V slot
+    static constexpr int kDV = PAIR ? D / 2 : D;             // columns of a V slot
+    static constexpr int kVKeys = D == 256 && !PAIR ? 64 : 128;  // keys of a V slot
     static constexpr int kVSlots = kAttnKeys / kVKeys;
-    static constexpr int kSlotBytes = kAttnKeys * kDK * 2;
+    static constexpr int kSlotBytes = kKKeys * kDK * 2;
     static constexpr int kQBytes = kAttnRows * D * 2;
     static constexpr int kSlots = D == 256 ? 5 : (D == 128 ? 6 : 8);
     static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kAttnCtrlBytes;
     static_assert(kSmem <= kSmemLimit && kSlots <= kAttnMaxSlots, "shared memory");
-    static_assert(kVKeys * D * 2 == kSlotBytes, "one slot size");
+    static_assert(kVKeys * kDV * 2 == kSlotBytes, "one slot size");
     static_assert(kQBytes + kSlots * kSlotBytes >= kAttnMaxRequests * 8, "room for the scan");
 };
 
@@ -98,15 +106,17 @@ struct AttnArgs {
     const int* q_start;
     const int* kv_lens;
     int R, tokens, heads, group;       // heads: KV heads; group: query heads per KV head
-    int gang;                          // blocks that take the heads of a range together
-    int tile_tokens;                   // tokens of a query tile: 128 / group
+    int gang;                          // blocks (pairs) that take the heads of a range together
+    int tile_tokens;                   // tokens of a query tile: a block's, or two blocks' of a pair
+    int block_tokens;                  // tokens of a block: 128 / group
+    int stride;                        // blocks from a split's part to the next: gang, times two for pairs
     int few_tokens;                    // tokens of a small box: the fewest whose rows are a multiple of 8
     int page_shift, max_keys;
     int window, sinks;                 // window 0: none, and then no sinks
     float scale_log2;                  // scale x log2(e)
     float* part;                       // [2 blocks][D][128 rows] partial accumulators
     float2* ml;                        // [2 blocks][128] (maximum, sum)
-    int4* splits;                      // [blocks][2] split records
+    int4* splits;                      // [blocks][2]: request, head, first token, rows; parts
     int* dev_err;
     unsigned long long wait_ns;
 };
@@ -172,6 +182,7 @@ struct AttnWalk {
     long long left, at;                // units left, global index of the next one
     AttnReq rq;
     AttnTile t;
+    int me;                            // the block, or the pair of blocks
     int r, h, qt, nqt;
     int k0, k1, units;                 // the segment: units k0..k1 of the tile's `units`
     __device__ __forceinline__ void enter(const AttnArgs& a) {
@@ -192,7 +203,7 @@ struct AttnWalk {
         nqt = attn_tiles(a, rq);
         const long long per = attn_div(all, a.heads / a.gang);
         const int turn = (int)attn_div(u - base, per);
-        h = turn * a.gang + (int)(blockIdx.x % a.gang);
+        h = turn * a.gang + me % a.gang;
         long long rem = (u - base) - turn * per;
         const int lane = threadIdx.x & 31;
         for (qt = 0;; qt += 32) {
@@ -240,7 +251,7 @@ struct AttnWalk {
             qt = 0;
             h += a.gang;
             if (h >= a.heads) {
-                h = (int)(blockIdx.x % a.gang);
+                h = me % a.gang;
                 do {
                     ++r;
                     enter(a);
@@ -309,6 +320,47 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t addr, uint32_t pane
     return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
+
+// The same over a pair of blocks (cta_group::2): issued by the even block of the cluster for both,
+// each holding its rows of A and D and half of B's N. A commit arrives on the barrier at this
+// address in both blocks.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tc_mma_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate, bool issue) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"((uint32_t)issue)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_pair_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate, bool issue) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"((uint32_t)issue)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, bool issue) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+            bar),
+        "r"((uint32_t)issue), "h"((uint16_t)3)
+        : "memory");
+}
+
+// Arrival on a barrier of another block of the cluster, and the fence for what it has to publish.
+__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 #define NQ_R4(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3])
 #define NQ_O4(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3])
@@ -380,30 +432,35 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
 }
 
 // Instruction descriptor: D fp32, A and B of one 16-bit type, A K-major, B K-major or (b_mn)
-// N-major, M = 128, N = n.
-constexpr uint32_t attn_idesc(bool bf16, int n, bool b_mn) {
+// N-major, M = m, N = n.
+constexpr uint32_t attn_idesc(bool bf16, int m, int n, bool b_mn) {
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kAttnRows >> 4) << 24);
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // ---------------------------------------------------------------- the kernel
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool PAIR>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
-    using Geo = AttnGeo<D>;
+    using Geo = AttnGeo<D, PAIR>;
+    constexpr int kBlocks = PAIR ? 2 : 1;      // blocks of a query tile
     constexpr int kSlots = Geo::kSlots, kKS = Geo::kKSlots, kVS = Geo::kVSlots, kDK = Geo::kDK, kVK = Geo::kVKeys;
+    constexpr int kKK = Geo::kKKeys, kDV = Geo::kDV;
+    const int rank = PAIR ? (int)cluster_rank() : 0;
     extern __shared__ __align__(1024) uint8_t attn_smem[];
     uint8_t* const qmem = attn_smem;
     uint8_t* const ring = attn_smem + Geo::kQBytes;
     uint8_t* const ctrl = ring + kSlots * Geo::kSlotBytes;
     float* const red = reinterpret_cast<float*>(ctrl);                      // [2][2 groups][128]
     uint64_t* const bars = reinterpret_cast<uint64_t*>(ctrl + 2048);
-    // bars: full[8], empty[8], s_full[2], p_ready[2], pv_done[2], o_free, q_full, q_free, done
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kAttnMaxSlots, sfull0 = empty0 + 8 * kAttnMaxSlots, pready0 = sfull0 + 16;
-    const uint32_t pvdone0 = pready0 + 16, ofree = pvdone0 + 16, qfull = ofree + 8, qfree = qfull + 8, done = qfree + 8;
-    volatile int* const flags = reinterpret_cast<volatile int*>(ctrl + 2048 + 256);
+    // bars: full[8], empty[8], s_full[2], p_ready[2], pv_done[2], o_free, q_full, q_free, done, and of the
+    // leading block of a pair: the other's q_full and full[8], passed on
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kAttnMaxSlots, sfull0 = empty0 + 8 * kAttnMaxSlots;
+    const uint32_t pready0 = sfull0 + 16, pvdone0 = pready0 + 16, ofree = pvdone0 + 16, qfull = ofree + 8, qfree = qfull + 8;
+    const uint32_t done = qfree + 8, qfull_other = done + 8, full_other0 = qfull_other + 8;
+    volatile int* const flags = reinterpret_cast<volatile int*>(ctrl + 2048 + 320);
     // flags: [0] abort, [3] TMEM base
-    long long* const warp_sums = reinterpret_cast<long long*>(ctrl + 2048 + 256 + 64);
+    long long* const warp_sums = reinterpret_cast<long long*>(ctrl + 2048 + 384);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t wait_ns = a.wait_ns;
@@ -411,14 +468,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(full0 + 8 * i, 1);
             mbar_init(empty0 + 8 * i, 1);
+            mbar_init(full_other0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sfull0 + 8 * i, 1);
-            mbar_init(pready0 + 8 * i, kAttnSoftmaxWarps);
+            mbar_init(pready0 + 8 * i, kBlocks * kAttnSoftmaxWarps);
             mbar_init(pvdone0 + 8 * i, 1);
         }
-        mbar_init(ofree, kAttnSoftmaxWarps);
+        mbar_init(ofree, kBlocks * kAttnSoftmaxWarps);
         mbar_init(qfull, 1);
+        mbar_init(qfull_other, 1);
         mbar_init(qfree, 1);
         mbar_init(done, 1);
         // the swizzled tiles need a 1024-byte base
@@ -426,18 +485,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         if (flags[0]) atomicOr(a.dev_err, kDevErrTimeout);
         mbar_fence_init();
     }
-    if (warp == 0) tmem_alloc(smem_u32(const_cast<int*>(flags) + 3), 512);
+    if (warp == 0) {
+        if constexpr (PAIR)
+            tmem_alloc_pair(smem_u32(const_cast<int*>(flags) + 3), 512);
+        else
+            tmem_alloc(smem_u32(const_cast<int*>(flags) + 3), 512);
+    }
     grid_dependency_wait();
 
     // The block's range of units. Up to 32 requests every warp scans by itself, one a lane; more are
     // scanned by the block into the ring buffers (free until the first copies).
     AttnWalk w;
+    w.me = blockIdx.x / kBlocks;
     w.left = 0;
     long long total = 0, blocks = 1;   // blocks: ranges with work
     int snap = 0;
     // locate(u): finds unit u in w, and returns its place in its tile
     auto range = [&](auto locate) {
-        const long long gangs = gridDim.x / a.gang, me = blockIdx.x / a.gang;
+        const long long gangs = gridDim.x / kBlocks / a.gang, me = w.me / a.gang;
         // no range is empty but between whole tiles: the join takes every block from a tile's first to
         // its last as a part
         blocks = max(1ll, min(gangs, total));
@@ -514,12 +579,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)flags[3];
+    // One arrival of the warp on a barrier of the leading block. The second block's is released at block
+    // scope, which is cheap (at cluster scope it cost a tile 1100 cycles): TMEM is ordered by tcgen05's
+    // own fences, and what else it has written it fences itself.
+    const uint32_t to_leader = PAIR ? cluster_map(full0, 0) - full0 : 0;
+    auto arrive_leader = [&](uint32_t bar) {
+        if (PAIR && rank == 1) {
+            if (lane == 0) mbar_arrive_remote_cta(bar + to_leader);
+        } else {
+            mbar_arrive_if(bar, lane == 0);
+        }
+    };
+    if constexpr (PAIR) cluster_sync_all();    // both blocks' barriers are initialised
 
     if (warp == kAttnProducerK || warp == kAttnProducerV) {
         // ------------------------------------------------------------ producers
         const bool is_v = warp == kAttnProducerV;
         // a box is `rows` keys of a page; a slot holds slot_keys keys x slot_cols columns
-        const int slot_keys = is_v ? kVK : kAttnKeys, slot_cols = is_v ? D : kDK, slots = is_v ? kVS : kKS;
+        const int slot_keys = is_v ? kVK : kKK, slot_cols = is_v ? kDV : kDK, slots = is_v ? kVS : kKS;
         const int rows = min(1 << a.page_shift, slot_keys), row_bits = __ffs(rows) - 1;
         const int page_rows = min(1 << a.page_shift, kAttnKeys), page_bits = __ffs(page_rows) - 1;
         const int ids_of = kAttnKeys >> page_bits, page_mask = (1 << a.page_shift) - 1, panels = slot_cols / 64;
@@ -547,15 +624,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     if (seq >= kSlots) ok = mbar_wait(empty0 + 8 * slot, ((seq / kSlots) - 1) & 1, flags, a.dev_err, wait_ns);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    const int key0 = w.key_tile(j) * kAttnKeys + (is_v ? s * kVK : 0);
+                    // a pair's blocks load half of the keys of K, half of the columns of V
+                    const int off = is_v ? s * kVK : rank * kKK, key0 = w.key_tile(j) * kAttnKeys + off;
                     const int boxes = max(0, min(slot_keys >> row_bits, (w.t.hi - key0 + rows - 1) >> row_bits));
                     const uint32_t bar = full0 + 8 * slot, dst = smem_u32(ring + slot * Geo::kSlotBytes);
                     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * rows * slot_cols * 2));
                     __syncwarp();
-                    const int copies = boxes * panels, col0 = is_v ? 0 : s * kDK;
+                    const int copies = boxes * panels, col0 = is_v ? rank * kDV : s * kDK;
                     for (int o0 = 0; o0 < copies; o0 += 32) {
                         const int o = o0 + lane, box = o / panels, panel = o % panels;
-                        const int at = (is_v ? s * kVK : 0) + box * rows;
+                        const int at = off + box * rows;
                         const int block = __shfl_sync(0xFFFFFFFFu, id, (at >> page_bits) & 31);
                         if (o < copies)
                             tma_load_4d(dst + panel * (slot_keys * 128) + box * rows * 128, map, col0 + panel * 64,
@@ -572,9 +650,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         if (!ok)                           // aborted: this warp's last copy into each slot
             for (int i = 0; i < kSlots; ++i)
                 if ((filled >> i) & 1) mbar_wait_drain(full0 + 8 * i, (parity >> i) & 1, kDrainNs);
+    } else if (PAIR && rank == 1 && warp == kAttnMma) {
+        // ------------------------------------------------------------ the second block's copies, passed on
+        int seq = 0, seg = 0;
+        bool ok = flags[0] == 0;
+        for (; w.more() && ok; w.next(a)) {
+            const int n = w.tiles();
+            if (n == 0) continue;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(qfull, seg & 1, flags, a.dev_err, wait_ns));
+            if (ok) arrive_leader(qfull_other);
+            for (int i = 0; i < n * (kKS + kVS) && ok; ++i, ++seq) {
+                const int slot = seq % kSlots;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full0 + 8 * slot, (seq / kSlots) & 1, flags, a.dev_err, wait_ns));
+                if (ok) arrive_leader(full_other0 + 8 * slot);
+            }
+            ++seg;
+        }
     } else if (warp == kAttnMma) {
         // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t kIdescS = attn_idesc(BF16, kAttnKeys, false), kIdescO = attn_idesc(BF16, D, true);
+        constexpr uint32_t kIdescS = attn_idesc(BF16, kBlocks * kAttnRows, kAttnKeys, false);
+        constexpr uint32_t kIdescO = attn_idesc(BF16, kBlocks * kAttnRows, D, true);
+        auto commit = [&](uint32_t bar, bool issue) {
+            if constexpr (PAIR)
+                tc_commit_pair(bar, issue);
+            else
+                tc_commit(bar, issue);
+        };
+        // a slot is full, in both blocks of a pair
+        auto wait_full = [&](int slot, uint32_t parity) {
+            bool there = mbar_wait(full0 + 8 * slot, parity, flags, a.dev_err, wait_ns);
+            if (PAIR) there = there && mbar_wait_cluster(full_other0 + 8 * slot, parity, flags, a.dev_err, wait_ns);
+            return there;
+        };
+        // a barrier on which the softmax warps (of both blocks) arrive
+        auto wait_warps = [&](uint32_t bar, uint32_t parity) {
+            if constexpr (PAIR)
+                return mbar_wait_cluster(bar, parity, flags, a.dev_err, wait_ns);
+            else
+                return mbar_wait(bar, parity, flags, a.dev_err, wait_ns);
+        };
         const bool leader = elect_one();
         const uint32_t qbase = smem_u32(qmem), ring0 = smem_u32(ring);
         int seq = 0, g = 0, seg = 0;
@@ -583,40 +697,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             const uint32_t s_col = tmem + kAttnSCol + kAttnKeys * (gt & 1);
             for (int s = 0; s < kKS; ++s) {
                 const int slot = seq % kSlots;
-                ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(full0 + 8 * slot, (seq / kSlots) & 1, flags, a.dev_err, wait_ns));
+                ok = __all_sync(0xFFFFFFFFu, ok && wait_full(slot, (seq / kSlots) & 1));
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t kbase = ring0 + slot * Geo::kSlotBytes;
 #pragma unroll
                 for (int i = 0; i < kDK / 16; ++i) {
                     const uint64_t ad = smem_desc_sw128(qbase + (s * (kDK / 64) + i / 4) * (kAttnRows * 128) + 32 * (i % 4));
-                    const uint64_t bd = smem_desc_sw128(kbase + (i / 4) * (kAttnKeys * 128) + 32 * (i % 4));
-                    tc_mma_ss(s_col, ad, bd, kIdescS, (s > 0 || i > 0) ? 1u : 0u, leader);
+                    const uint64_t bd = smem_desc_sw128(kbase + (i / 4) * (kKK * 128) + 32 * (i % 4));
+                    if constexpr (PAIR)
+                        tc_mma_pair_ss(s_col, ad, bd, kIdescS, i > 0 ? 1u : 0u, leader);
+                    else
+                        tc_mma_ss(s_col, ad, bd, kIdescS, (s > 0 || i > 0) ? 1u : 0u, leader);
                 }
-                tc_commit(empty0 + 8 * slot, leader);
+                commit(empty0 + 8 * slot, leader);
                 ++seq;
             }
-            tc_commit(sfull0 + 8 * (gt & 1), leader);
+            commit(sfull0 + 8 * (gt & 1), leader);
         };
         for (; w.more() && ok; w.next(a)) {
             const int n = w.tiles();
             if (n == 0) continue;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(qfull, seg & 1, flags, a.dev_err, wait_ns));
+            ok = mbar_wait(qfull, seg & 1, flags, a.dev_err, wait_ns);
+            if (PAIR) ok = ok && mbar_wait_cluster(qfull_other, seg & 1, flags, a.dev_err, wait_ns);
+            ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             score(g);
             for (int j = 0; j < n && ok; ++j, ++g) {
                 if (j + 1 < n) score(g + 1);
                 if (!ok) break;
-                if (j == n - 1) tc_commit(qfree, leader);
+                if (j == n - 1) commit(qfree, leader);
                 const int buf = g & 1;
-                ok = mbar_wait(pready0 + 8 * buf, (g >> 1) & 1, flags, a.dev_err, wait_ns);
-                if (ok && j == 0 && seg > 0) ok = mbar_wait(ofree, (seg - 1) & 1, flags, a.dev_err, wait_ns);
+                ok = wait_warps(pready0 + 8 * buf, (g >> 1) & 1);
+                if (ok && j == 0 && seg > 0) ok = wait_warps(ofree, (seg - 1) & 1);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const uint32_t p_col = tmem + kAttnSCol + kAttnKeys * buf;
                 for (int s = 0; s < kVS; ++s) {
                     const int slot = seq % kSlots;
-                    ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(full0 + 8 * slot, (seq / kSlots) & 1, flags, a.dev_err, wait_ns));
+                    ok = __all_sync(0xFFFFFFFFu, ok && wait_full(slot, (seq / kSlots) & 1));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t vbase = ring0 + slot * Geo::kSlotBytes;
@@ -624,18 +743,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     for (int i = 0; i < kVK / 16; ++i) {
                         const int key = s * kVK + 16 * i;    // its half of P starts at column 64 * (key / 64)
                         const uint32_t ac = p_col + 64 * (key / 64) + (key % 64) / 2;
-                        tc_mma(tmem, ac, smem_desc_mn128(vbase + i * 2048, kVK * 128), kIdescO,
-                               (j > 0 || s > 0 || i > 0) ? 1u : 0u, leader);
+                        const uint64_t bd = smem_desc_mn128(vbase + i * 2048, kVK * 128);
+                        const uint32_t add = (j > 0 || s > 0 || i > 0) ? 1u : 0u;
+                        if constexpr (PAIR)
+                            tc_mma_pair(tmem, ac, bd, kIdescO, add, leader);
+                        else
+                            tc_mma(tmem, ac, bd, kIdescO, add, leader);
                     }
-                    tc_commit(empty0 + 8 * slot, leader);
+                    commit(empty0 + 8 * slot, leader);
                     ++seq;
                 }
-                if (ok) tc_commit(pvdone0 + 8 * buf, leader);
+                if (ok) commit(pvdone0 + 8 * buf, leader);
             }
             ++seg;
         }
         // every MMA has completed before TMEM can be freed
-        tc_commit(done, leader);
+        commit(done, leader);
         mbar_wait_drain(done, 0, kDrainNs);
     } else if (warp == kAttnLoader) {
         // ------------------------------------------------------------ query tiles
@@ -646,15 +769,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             if (seg > 0) ok = mbar_wait(qfree, (seg - 1) & 1, flags, a.dev_err, wait_ns);
             if (!ok) break;
             // few tokens: as many small boxes as they fill
-            const int box = a.few_tokens * a.group, n = (w.t.rows + box - 1) / box;
+            const int rows_here = min(max(w.t.rows - rank * a.block_tokens * a.group, 1), a.block_tokens * a.group);
+            const int box = a.few_tokens * a.group, n = (rows_here + box - 1) / box;
             const bool few = n * box <= kAttnRows && n <= 4;
-            const int rows = few ? n * box : a.tile_tokens * a.group, copies = (few ? n : 1) * (D / 64);
+            const int rows = few ? n * box : a.block_tokens * a.group, copies = (few ? n : 1) * (D / 64);
             if (lane == 0) mbar_arrive_expect_tx(qfull, (uint32_t)(rows * D * 2));
             __syncwarp();
             if (lane < copies) {
                 const int panel = lane % (D / 64), i = lane / (D / 64);
                 tma_load_3d(smem_u32(qmem) + panel * (kAttnRows * 128) + i * box * 128, few ? &a.qfew : &a.qmap, 64 * panel,
-                            w.h * a.group, w.rq.q0 + w.t.token0 + i * a.few_tokens, qfull);
+                            w.h * a.group, w.rq.q0 + w.t.token0 + rank * a.block_tokens + i * a.few_tokens, qfull);
             }
             __syncwarp();
             ++seg;
@@ -672,12 +796,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const int row_token = row / a.group, row_head = row - row_token * a.group;
         int g = 0, seq = 0;
         int4 split0 = make_int4(-1, 0, 0, 0);
-        int split_last = 0;
+        int split_count = 0;
         for (; w.more(); w.next(a)) {
             const AttnTile& t = w.t;
             const int n = w.tiles();
             const bool whole = w.k0 == 0 && w.k1 == w.units;
-            const bool valid = row < t.rows;
+            // this block's part of the tile
+            const int token0 = t.token0 + rank * a.block_tokens;
+            const int rows = min(max(t.rows - rank * a.block_tokens * a.group, 0), a.block_tokens * a.group);
+            const int pf = t.pf + rank * a.block_tokens, pl = min(pf + a.block_tokens - 1, t.pl);
+            const bool valid = row < rows;
             if (w.k0 == 0 && !whole) {
                 // the last unit's owner: ranges begin at floor(total c / blocks), and one that begins near
                 // the tile's end at that; it is the same block of its gang
@@ -685,10 +813,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                 long long c = (end * blocks - 1) / total;
                 const int from = (int)max(0ll, attn_div(total * c, blocks) - w.at);
                 if (w.snapped(from, snap) == w.units) --c;
-                split0 = make_int4(w.r, w.h, w.qt, t.rows);
-                split_last = (int)c;
+                split0 = make_int4(w.r, w.h, token0, rows);
+                split_count = (int)c - w.me / a.gang + 1;
             }
-            uint16_t* const orow = a.out + (w.rq.q0 + t.token0 + row_token) * a.out_stride +
+            uint16_t* const orow = a.out + (w.rq.q0 + token0 + row_token) * a.out_stride +
                                    (long long)(w.h * a.group + row_head) * D + half * (D / 2);
             if (n == 0) {                  // no key is seen
                 if (valid)
@@ -696,8 +824,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     for (int i = 0; i < D / 2; i += 8) *reinterpret_cast<uint4*>(orow + i) = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            const bool active = 32 * quarter < t.rows;
-            const int p = t.pf + row_token;
+            const bool active = 32 * quarter < rows;
+            const int p = pf + row_token;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = 0; j < n; ++j, ++g) {
@@ -706,7 +834,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                 tc_fence_after();
                 if (active) {
                     const uint32_t s_col = lane_base + kAttnSCol + kAttnKeys * buf + 64 * half;
-                    const bool masked = key0 + kAttnKeys - 1 > t.pf || (a.window > 0 && key0 < t.pl - a.window + 1);
+                    const bool masked = key0 + kAttnKeys - 1 > pf || (a.window > 0 && key0 < pl - a.window + 1);
                     uint32_t v[64];
                     // 64 columns of S from `col`, which are the keys from kk on; keys that the row does
                     // not see as -inf
@@ -795,18 +923,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                         // keys b0..b1-1 of the tile lie between the sinks and the window, e0.. past the last key
                         const int b0 = max(0, a.sinks - key0), b1 = min(kAttnKeys, t.lo - key0);
                         const int e0 = max(0, min(kAttnKeys, t.hi - key0)), nb = max(0, b1 - b0);
-                        for (int i = tid; i < (nb + kAttnKeys - e0) * (D / 8); i += kAttnSoftmaxWarps * 32) {
-                            const int at = i / (D / 8), ch = i % (D / 8), key = at < nb ? b0 + at : e0 + at - nb;
+                        for (int i = tid; i < (nb + kAttnKeys - e0) * (kDV / 8); i += kAttnSoftmaxWarps * 32) {
+                            const int at = i / (kDV / 8), ch = i % (kDV / 8), key = at < nb ? b0 + at : e0 + at - nb;
                             uint8_t* const slot = ring + ((v0 + key / kVK) % kSlots) * Geo::kSlotBytes;
                             *reinterpret_cast<uint4*>(slot + (ch / 8) * (kVK * 128) + (key % kVK) * 128 + (ch % 8) * 16) =
                                 make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
+                        if (PAIR) fence_acq_rel_cluster();
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                mbar_arrive_if(pready0 + 8 * buf, lane == 0);
+                arrive_leader(pready0 + 8 * buf);
             }
             seq += n * (kKS + kVS);
             // the tile's rows: finished, or a partial with its maximum and sum
@@ -847,19 +976,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             }
             tc_fence_before();
             __syncwarp();
-            mbar_arrive_if(ofree, lane == 0);
+            arrive_leader(ofree);
         }
         if (tid == 0) {
             a.splits[2 * blockIdx.x] = split0;
-            a.splits[2 * blockIdx.x + 1] = make_int4(split_last, 0, 0, 0);
+            a.splits[2 * blockIdx.x + 1] = make_int4(split_count, 0, 0, 0);
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();    // nothing arrives on, or multiplies in, a block that has left
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        if constexpr (PAIR)
+            tmem_dealloc_pair(tmem, 512);
+        else
+            tmem_dealloc(tmem, 512);
     }
 }
 
@@ -884,7 +1017,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid
     const int tid = threadIdx.x;
     const int4 s = a.splits[2 * blockIdx.x];
     if (s.x >= 0) {
-        const int last = a.splits[2 * blockIdx.x + 1].x, count = last - (int)blockIdx.x / a.gang + 1, rows = s.w;
+        const int count = a.splits[2 * blockIdx.x + 1].x, rows = s.w;
         const AttnReq rq = attn_req(a, s.x);
         const float c = a.scale_log2;
         const int parts = count >= 8 ? 8 : (count >= 4 ? 4 : 1), per = kJoinThreads / parts;
@@ -897,7 +1030,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid
             if (item < items) {
 #pragma unroll 3
                 for (int i = part; i < count; i += parts) {
-                    const int slot = 2 * ((int)blockIdx.x + i * a.gang) + (i == 0 ? 1 : 0);
+                    const int slot = 2 * ((int)blockIdx.x + i * a.stride) + (i == 0 ? 1 : 0);
                     const float2 ml = a.ml[slot * kAttnRows + row];
                     const float* src = a.part + ((size_t)slot * D + group * 8) * kAttnRows + row;
                     float v[8];
@@ -937,7 +1070,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid
                 u.y = pack16<BF16>(o[2] * inv, o[3] * inv);
                 u.z = pack16<BF16>(o[4] * inv, o[5] * inv);
                 u.w = pack16<BF16>(o[6] * inv, o[7] * inv);
-                *reinterpret_cast<uint4*>(a.out + (rq.q0 + s.z * a.tile_tokens + token) * a.out_stride +
+                *reinterpret_cast<uint4*>(a.out + (rq.q0 + s.z + token) * a.out_stride +
                                           (long long)head * D + group * 8) = u;
             }
             __syncthreads();
