@@ -894,7 +894,7 @@ const char* nq_status_string(nq_status s) {
     }
 }
 
-int nq_version(void) { return (2 << 16) | 0; }
+int nq_version(void) { return (2 << 16) | 1; }
 
 size_t nq_packed_bytes_q4(int K, int N) { return check_shape(K, N) == NQ_OK ? packed_bytes(4, K, N) : 0; }
 size_t nq_packed_bytes_q5(int K, int N) { return check_shape(K, N) == NQ_OK ? packed_bytes(5, K, N) : 0; }
