@@ -381,6 +381,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
         NQ_R4(v, 0), NQ_R4(v, 4), NQ_R4(v, 8), NQ_R4(v, 12), NQ_R4(v, 16), NQ_R4(v, 20), NQ_R4(v, 24), NQ_R4(v, 28)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        NQ_R4(v, 0), NQ_R4(v, 4), NQ_R4(v, 8), NQ_R4(v, 12)
+        : "memory");
+}
 #undef NQ_R4
 #undef NQ_O4
 
@@ -835,52 +841,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                 if (active) {
                     const uint32_t s_col = lane_base + kAttnSCol + kAttnKeys * buf + 64 * half;
                     const bool masked = key0 + kAttnKeys - 1 > pf || (a.window > 0 && key0 < pl - a.window + 1);
+                    // the thread's 64 columns of S, which are the keys from kk on; keys that the row does not
+                    // see as -inf
                     uint32_t v[64];
-                    // 64 columns of S from `col`, which are the keys from kk on; keys that the row does
-                    // not see as -inf
-                    auto load = [&](uint32_t col, int kk) {
-                        tmem_ld32(col, v);
-                        tmem_ld32(col + 32, v + 32);
-                        tmem_wait_ld();
-                        if (masked) {
-                            uint64_t see = low_bits(p - kk + 1);
-                            if (a.window > 0) see &= ~low_bits(p - a.window + 1 - kk) | low_bits(a.sinks - kk);
-                            const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+                    const int kk = key0 + 64 * half;
+                    tmem_ld32(s_col, v);
+                    tmem_ld32(s_col + 32, v + 32);
+                    tmem_wait_ld();
+                    if (masked) {
+                        uint64_t see = low_bits(p - kk + 1);
+                        if (a.window > 0) see &= ~low_bits(p - a.window + 1 - kk) | low_bits(a.sinks - kk);
+                        const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                v[i] = (s0 & (1u << i)) ? v[i] : 0xFF800000u;
-                                v[32 + i] = (s1 & (1u << i)) ? v[32 + i] : 0xFF800000u;
-                            }
+                        for (int i = 0; i < 32; ++i) {
+                            v[i] = (see0 & (1u << i)) ? v[i] : 0xFF800000u;
+                            v[32 + i] = (see1 & (1u << i)) ? v[32 + i] : 0xFF800000u;
                         }
-                    };
-                    auto maximum = [&]() {
-                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < 64; i += 8)
+                    for (int i = 0; i < 64; i += 8)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(v[i + e]), __uint_as_float(v[i + 4 + e])));
-                        return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    };
-                    // p = 2^(c s + off), rounded, to column `col` of P; their sum joins l
-                    auto exponentials = [&](uint32_t col, float off) {
-                        uint32_t pk[32];
-                        const uint64_t cc = pack2(__float_as_uint(c), __float_as_uint(c));
-                        const uint64_t oo = pack2(__float_as_uint(off), __float_as_uint(off));
-                        uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-                        for (int i = 0; i < 64; i += 2) {
-                            const float2 x2 = unpack2(fma2(pack2(v[i], v[i + 1]), cc, oo));
-                            const float e0 = exp2_fast(x2.x), e1 = exp2_fast(x2.y);
-                            sum[(i / 2) & 3] = add2(sum[(i / 2) & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
-                            pk[i / 2] = pack16<BF16>(e0, e1);
-                        }
-                        const float2 s2 = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-                        l += s2.x + s2.y;
-                        tmem_st32(col, pk);
-                    };
-                    load(s_col, key0 + 64 * half);
-                    float mx = maximum();
+                        for (int e = 0; e < 4; ++e)
+                            m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(v[i + e]), __uint_as_float(v[i + 4 + e])));
+                    float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     float* const x = red + (g & 1) * 256;
                     x[half * 128 + row] = mx;
                     named_bar_sync(1 + quarter, 64);
@@ -905,7 +889,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     }
                     if (grow) m = mx;
                     const float off = m == -INFINITY ? 0.f : -m * c;
-                    exponentials(s_col, off);
+                    // p = 2^(c s + off), rounded, over S; their sum joins l. In two parts, so that the first is
+                    // stored while the second is computed.
+                    const uint64_t cc = pack2(__float_as_uint(c), __float_as_uint(c));
+                    const uint64_t oo = pack2(__float_as_uint(off), __float_as_uint(off));
+                    uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 x2 = unpack2(fma2(pack2(v[32 * q + i], v[32 * q + i + 1]), cc, oo));
+                            const float e0 = exp2_fast(x2.x), e1 = exp2_fast(x2.y);
+                            sum[(i / 2) & 3] = add2(sum[(i / 2) & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
+                            pk[i / 2] = pack16<BF16>(e0, e1);
+                        }
+                        tmem_st16(s_col + 16 * q, pk);
+                    }
+                    const float2 s2 = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                    l += s2.x + s2.y;
                     tmem_wait_st();
                 }
                 // V rows that no row sees: zeros
