@@ -1,5 +1,6 @@
 /*
- * nq.h -- C ABI of the GB300 (sm_103a) groupwise int4/int5 small-batch projection library.
+ * nq.h -- C ABI of the GB300 (sm_103a) groupwise int4/int5 small-batch projection library, and of
+ * the serving step around the projections (paged KV cache, attention, sampling).
  *
  * The operation (what the pages tune for single-GPU decode and speculative verify rounds):
  *
@@ -530,7 +531,7 @@ nq_status nq_reserve(int T_max, int K_max, int N_max);
 
 /*
  * nq_device_error: synchronise the current device, then report and clear the device-side
- * error flags of its workspace and of nq_gemm_q4_noalloc's fixed scratch: NQ_OK, or
+ * error flags of its workspaces (nq_attn_paged's among them) and of nq_gemm_q4_noalloc's fixed scratch: NQ_OK, or
  * NQ_ERR_TIMEOUT if a bounded wait inside a kernel ran out since the last check (that
  * call's outputs are then undefined). Clears the split-K tickets as well, so later calls
  * start clean.
@@ -538,8 +539,8 @@ nq_status nq_reserve(int T_max, int K_max, int N_max);
 nq_status nq_device_error(void);
 
 /*
- * nq_wait_limit: the bound, in nanoseconds, of every device-side wait of later projection
- * calls (a pipeline stage, an activation slab, a cluster peer). ns > 0 sets it; ns <= 0 only
+ * nq_wait_limit: the bound, in nanoseconds, of every device-side wait of later projection and
+ * attention calls (a pipeline stage, an activation slab, a cluster peer). ns > 0 sets it; ns <= 0 only
  * queries. Returns the previous bound. Default 2 s, or the environment variable NQ_WAIT_NS
  * read at the first call. A wait that runs out aborts its thread block (its outputs are
  * undefined, nq_device_error reports NQ_ERR_TIMEOUT) after the block has waited, on a
