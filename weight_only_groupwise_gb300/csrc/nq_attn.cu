@@ -18,7 +18,7 @@ long long kv_cache_span(const nq_kv_cache* c);
 namespace {
 
 template <int D, bool BF16, bool PAIR>
-cudaError_t attn_launch(const AttnArgs& a, int blocks, cudaStream_t stream, bool pdl) {
+cudaError_t attn_launch(const AttnArgs& a, int blocks, bool splits, cudaStream_t stream, bool pdl) {
     auto kern = attn_kernel<D, BF16, PAIR>;
     static thread_local int set_for_device = -1;
     int dev = 0;
@@ -30,7 +30,7 @@ cudaError_t attn_launch(const AttnArgs& a, int blocks, cudaStream_t stream, bool
     }
     cudaError_t e = step_launch(kern, dim3(blocks), dim3(kAttnThreads), AttnGeo<D, PAIR>::kSmem, stream, pdl && !PAIR,
                                 PAIR ? 2 : 1, a);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || !splits) return e;
     // a block takes 32 items of a split with many parts; launched without dependent launch: waiting
     // blocks slowed the kernel before them (one token over 4099 keys: 21.4 us with, 15.5 without)
     const int rows = (a.tokens < a.block_tokens ? a.tokens : a.block_tokens) * a.group;
@@ -40,13 +40,13 @@ cudaError_t attn_launch(const AttnArgs& a, int blocks, cudaStream_t stream, bool
 }
 
 template <bool BF16>
-cudaError_t attn_launch_dim(int dim, bool pair, const AttnArgs& a, int blocks, cudaStream_t stream, bool pdl) {
+cudaError_t attn_launch_dim(int dim, bool pair, const AttnArgs& a, int blocks, bool splits, cudaStream_t stream, bool pdl) {
     switch (dim) {
-        case 64: return attn_launch<64, BF16, false>(a, blocks, stream, pdl);
-        case 128: return attn_launch<128, BF16, false>(a, blocks, stream, pdl);
+        case 64: return attn_launch<64, BF16, false>(a, blocks, splits, stream, pdl);
+        case 128: return attn_launch<128, BF16, false>(a, blocks, splits, stream, pdl);
         default:
-            return pair ? attn_launch<256, BF16, true>(a, blocks, stream, pdl)
-                        : attn_launch<256, BF16, false>(a, blocks, stream, pdl);
+            return pair ? attn_launch<256, BF16, true>(a, blocks, splits, stream, pdl)
+                        : attn_launch<256, BF16, false>(a, blocks, splits, stream, pdl);
     }
 }
 
@@ -191,8 +191,14 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     a.ml = reinterpret_cast<float2*>(ws + kAttnErrBytes + (size_t)d.sms * kAttnSplitBytes);
     a.part = reinterpret_cast<float*>(a.ml + (size_t)d.sms * 2 * kAttnRows);
     a.wait_ns = d.wait_ns;
-    const cudaError_t e = bf16 ? attn_launch_dim<true>(cache->dim, pair, a, blocks, s, d.pdl)
-                               : attn_launch_dim<false>(cache->dim, pair, a, blocks, s, d.pdl);
+    // whether any query tile can be long enough to be split: the keys a token can see, and the window's
+    // drift over a tile's tokens
+    long long keys = a.max_keys;
+    if (window > 0 && keys > (long long)window + a.tile_tokens + 2 * kAttnKeys + sinks)
+        keys = (long long)window + a.tile_tokens + 2 * kAttnKeys + sinks;
+    const bool splits = (keys + kAttnKeys - 1) / kAttnKeys > kAttnWhole;
+    const cudaError_t e = bf16 ? attn_launch_dim<true>(cache->dim, pair, a, blocks, splits, s, d.pdl)
+                               : attn_launch_dim<false>(cache->dim, pair, a, blocks, splits, s, d.pdl);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 

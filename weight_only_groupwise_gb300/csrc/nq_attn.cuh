@@ -19,7 +19,8 @@
 // whole call, in the order request, gang of heads, query tile, key tile, are cut into one equal
 // range per gang (stream-K): ragged lengths and few rows need no other rule. A boundary within
 // kAttnSnap units of a query tile's begin or end moves there, where a range is long enough to
-// take it: a split costs about as much as so many units (partials written, joined). A query tile whose keys are spread over several blocks is written as
+// take it, and one inside a tile of up to kAttnWhole units always: a split costs about as much as so
+// many units (partials written, joined). Where no tile can be longer the join is not launched. A query tile whose keys are spread over several blocks is written as
 // fp32 partials with their maxima and sums; attn_join_kernel adds them in block order, so the
 // result does not depend on timing. Every block finds its range by itself from the lengths on the
 // device: no host copy of the lengths, no plan to keep, no waits between blocks.
@@ -74,6 +75,7 @@ constexpr int kAttnSCol = 256;                    // TMEM column of the first S 
 constexpr int kAttnMaxSlots = 8;
 constexpr int kAttnCtrlBytes = 3072;
 constexpr int kAttnSnap = 6;                      // units by which a range may grow or shrink to avoid a split
+constexpr int kAttnWhole = 4;                     // a query tile of up to so many units is never split
 constexpr float kAttnLazy = 8.f;                  // log2 of the growth that forces a rescale
 
 // Shared-memory geometry for a head dimension: the K slot holds 128 keys x min(D, 128) columns,
@@ -127,13 +129,15 @@ struct AttnReq {
     int q0, n, kv;                     // first token, new tokens, keys
 };
 
-__device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, int r) {
+__device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, int b, int e, int kv) {
     AttnReq q;
-    const int b = a.q_start[r], e = a.q_start[r + 1];
     q.q0 = min(max(b, 0), a.tokens);
     q.n = min(max(e, q.q0), a.tokens) - q.q0;
-    q.kv = min(max(a.kv_lens[r], 0), a.max_keys);
+    q.kv = min(max(kv, 0), a.max_keys);
     return q;
+}
+__device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, int r) {
+    return attn_req(a, a.q_start[r], a.q_start[r + 1], a.kv_lens[r]);
 }
 
 // x / y for non-negative x and positive y, in 32 bits where they fit.
@@ -185,9 +189,20 @@ struct AttnWalk {
     int me;                            // the block, or the pair of blocks
     int r, h, qt, nqt;
     int k0, k1, units;                 // the segment: units k0..k1 of the tile's `units`
+    int next_b, next_e, next_kv;       // request r + 1 as it lies in memory, fetched ahead
+    __device__ __forceinline__ void fetch(const AttnArgs& a) {
+        if (r + 1 < a.R) {
+            next_b = __ldg(a.q_start + r + 1);
+            next_e = __ldg(a.q_start + r + 2);
+            next_kv = __ldg(a.kv_lens + r + 1);
+        }
+    }
+    // The next request.
     __device__ __forceinline__ void enter(const AttnArgs& a) {
-        rq = attn_req(a, r);
+        ++r;
+        rq = attn_req(a, next_b, next_e, next_kv);
         nqt = attn_tiles(a, rq);
+        fetch(a);
     }
     __device__ __forceinline__ void cut(int from) {
         units = max(1, t.n);
@@ -206,7 +221,7 @@ struct AttnWalk {
         h = turn * a.gang + me % a.gang;
         long long rem = (u - base) - turn * per;
         const int lane = threadIdx.x & 31;
-        for (qt = 0;; qt += 32) {
+        for (qt = 0; nqt > 1; qt += 32) {
             const int n_ = attn_tile_units(a, rq, qt + lane, nqt);
             long long x = n_;
 #pragma unroll
@@ -229,6 +244,7 @@ struct AttnWalk {
     }
     // Where a boundary `from` units into this tile is: moved to the tile's begin or end if that is near.
     __device__ __forceinline__ int snapped(int from, int snap) const {
+        if (units <= kAttnWhole) return 2 * from < units ? 0 : units;
         return from <= snap ? 0 : (units - from <= snap ? units : from);
     }
     // Begins a range of n units at unit u, `from` units into the tile found.
@@ -237,6 +253,7 @@ struct AttnWalk {
         left = n;
         k0 = k1 = units;
         if (left <= 0) return;
+        fetch(a);
         if (from == units)
             next(a);                   // the next tile's begin
         else
@@ -253,7 +270,6 @@ struct AttnWalk {
             if (h >= a.heads) {
                 h = me % a.gang;
                 do {
-                    ++r;
                     enter(a);
                 } while (nqt == 0 && r < a.R - 1);
             }
@@ -515,7 +531,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         snap = attn_div(total, blocks) > 2 * kAttnSnap ? kAttnSnap : 0;
         long long u0 = min(attn_div(total * me, blocks), total), u1 = min(attn_div(total * (me + 1), blocks), total);
         if (u0 >= u1) return;
-        if (u1 < total && snap > 0) {
+        if (u1 < total) {
             const int from = locate(u1);
             u1 += w.snapped(from, snap) - from;
         }
@@ -802,6 +818,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const int row_token = row / a.group, row_head = row - row_token * a.group;
         int g = 0, seq = 0;
         int4 split0 = make_int4(-1, 0, 0, 0);
+        const int end = min(max(__ldg(a.q_start + a.R), 0), a.tokens);   // output rows from here on are zeros
         int split_count = 0;
         for (; w.more(); w.next(a)) {
             const AttnTile& t = w.t;
@@ -815,8 +832,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             if (w.k0 == 0 && !whole) {
                 // the last unit's owner: ranges begin at floor(total c / blocks), and one that begins near
                 // the tile's end at that; it is the same block of its gang
-                const long long end = w.at + w.units;
-                long long c = (end * blocks - 1) / total;
+                const long long stop = w.at + w.units;
+                long long c = (stop * blocks - 1) / total;
                 const int from = (int)max(0ll, attn_div(total * c, blocks) - w.at);
                 if (w.snapped(from, snap) == w.units) --c;
                 split0 = make_int4(w.r, w.h, token0, rows);
@@ -980,6 +997,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             __syncwarp();
             arrive_leader(ofree);
         }
+        for (int i = end + blockIdx.x; i < a.tokens; i += gridDim.x)
+            for (int e = tid; e < a.heads * a.group * (D / 8); e += kAttnSoftmaxWarps * 32)
+                reinterpret_cast<uint4*>(a.out + i * a.out_stride)[e] = make_uint4(0, 0, 0, 0);
         if (tid == 0) {
             a.splits[2 * blockIdx.x] = split0;
             a.splits[2 * blockIdx.x + 1] = make_int4(split_count, 0, 0, 0);
@@ -1009,8 +1029,7 @@ constexpr int kJoinParts = 8;      // most threads that share an item's partials
 // (x, *) share the items of the tile that block x of the attention kernel opened, neighbouring lanes
 // taking neighbouring rows (partials are stored column by column). Up to 8 threads share an
 // item's partials, each with a running maximum, so that few rows with many partials are read in
-// parallel. Bound by latency: two or three rounds of loads. The same blocks write zeros to the output rows
-// past the last request's.
+// parallel. Bound by latency: two or three rounds of loads.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid_constant__ AttnArgs a) {
     __shared__ float acc[kJoinThreads][11];    // 8 columns, maximum, sum (odd stride: no bank conflicts)
@@ -1078,10 +1097,6 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_join_kernel(const __grid
             __syncthreads();
         }
     }
-    const int end = min(max(a.q_start[a.R], 0), a.tokens), chunks = a.heads * a.group * (D / 8);
-    for (int t = end + blockIdx.x + gridDim.x * blockIdx.y; t < a.tokens; t += gridDim.x * gridDim.y)
-        for (int i = tid; i < chunks; i += kJoinThreads)
-            reinterpret_cast<uint4*>(a.out + t * a.out_stride)[i] = make_uint4(0, 0, 0, 0);
 }
 
 }  // namespace nq
