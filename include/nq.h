@@ -474,14 +474,14 @@ nq_status nq_kv_append(const void* k, long long k_stride, const void* v, long lo
  *   tokens <= 2^23; 1 <= G <= 128; max_blocks * page <= 2^30
  * Scores, softmax statistics and sums are fp32; the probabilities are rounded to the 16-bit type
  * for their product with V, O once at the end. Table entries of pages that no new token sees are
- * not used (a window's old pages may have been given back) apart from those that share a tile of
- * 128 keys with seen ones, which may be any number; an entry outside the cache reads as rows of
- * zeros. Cache rows that no new token sees may hold anything, NaN included. A NaN or infinity in
+ * not used (a window's old pages may have been given back, page by page); an entry outside the
+ * cache reads as rows of zeros. Cache rows that no new token sees may hold anything, NaN included. A NaN or infinity in
  * a V row that one of a tile's tokens sees reaches the other tokens of that tile (up to 128 / G
  * consecutive ones), as 0 * NaN does in a plain product.
  * q_start is clamped to 0..tokens and taken as non-decreasing, kv_lens to 0..max_blocks * page.
- * One launch over all SMs and one that joins query tiles whose keys were spread over several;
- * deterministic for a given device. Uses a library workspace of about 40 MB, allocated on the
+ * One launch over all SMs and one that joins query tiles whose keys were spread over several (left
+ * out where max_blocks or the window bounds every tile to a few hundred keys); deterministic for a
+ * given device. Uses a library workspace of about 40 MB, allocated on the
  * first call (or by nq_attn_reserve, before stream capture) and shared like the projections'
  * workspace: order the calls of one device on one stream.
  */

@@ -143,6 +143,26 @@ def test_window_pages_given_back(nq):
     check(nq, p, window=100, sinks=3)
 
 
+@pytest.mark.parametrize("dim,page", [(256, 64), (128, 16), (128, 256), (64, 128)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (37, 5), (128, 16), (130, 70), (256, 128), (300, 200)])
+def test_rows_between_sinks_and_window_hold_nan(nq, dim, page, window, sinks):
+    """Rows that no new token sees, in pages with seen ones and of their own; the latter's entries name a NaN page."""
+    old, new = [700, 513, 250, 37, 1000, 384], [1, 2, 1, 3, 8, 1]
+    p = problem(old, new, 8, 2, dim, page, BF, seed=window + page)
+    pad = int(next(i for i in range(p["k"].shape[0]) if not (p["table"] == i).any()))      # a spare page: all NaN
+    assert p["v"][pad].isnan().all()
+    for r, (have, n) in enumerate(zip(old, new)):
+        lo = have - window + 1          # the first new token's first key
+        for key in range(sinks, max(sinks, lo)):
+            at = (int(p["table"][r, key // page]), key % page)
+            p["k"][at] = math.nan
+            p["v"][at] = math.nan
+        for b in range(-(-(have + n) // page)):
+            if b * page >= sinks and (b + 1) * page <= lo:
+                p["table"][r, b] = pad
+    check(nq, p, window, sinks)
+
+
 def test_long_split_and_many_tiles(nq):
     """One request over every block of the grid, and prompts of several query tiles."""
     check(nq, problem([40000], [1], 6, 1, 256, 64, BF, seed=1))

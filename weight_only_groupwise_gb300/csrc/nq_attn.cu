@@ -174,6 +174,7 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
         return NQ_ERR_CUDA;
     a.out = static_cast<uint16_t*>(out);
     a.out_stride = out_stride;
+    a.wide = reinterpret_cast<uintptr_t>(out) % 32 == 0 && out_stride % 16 == 0;
     a.table = block_table;
     a.table_stride = table_stride;
     a.q_start = q_start;

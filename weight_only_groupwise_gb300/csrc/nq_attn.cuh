@@ -20,10 +20,11 @@
 // range per gang (stream-K): ragged lengths and few rows need no other rule. A boundary within
 // kAttnSnap units of a query tile's begin or end moves there, where a range is long enough to
 // take it, and one inside a tile of up to kAttnWhole units always: a split costs about as much as so
-// many units (partials written, joined). Where no tile can be longer the join is not launched. A query tile whose keys are spread over several blocks is written as
-// fp32 partials with their maxima and sums; attn_join_kernel adds them in block order, so the
-// result does not depend on timing. Every block finds its range by itself from the lengths on the
-// device: no host copy of the lengths, no plan to keep, no waits between blocks.
+// many units (partials written, joined). Where no tile can be longer the join is not launched. A
+// query tile whose keys are spread over several blocks is written as fp32 partials with their
+// maxima and sums; attn_join_kernel adds them in block order, so the result does not depend on
+// timing. Every block finds its range by itself from the lengths on the device: no host copy of the
+// lengths, no plan to keep, no waits between blocks.
 //
 // Pairs. For prompts of 256 columns (attn_uses_pairs) two blocks of a cluster take a query tile of 256
 // rows: each its 128 rows of Q, S, P and O, half of the keys of a K tile, half of the columns of a
@@ -53,7 +54,9 @@
 // TMEM: O in columns 0..dim-1, the S buffers (P over them) in columns 256.. and 384...
 //
 // Rows of V that no row of the tile sees (past the last key, before a window) may hold anything,
-// NaN included, and 0 x NaN would reach the sum: the softmax warps zero them in shared memory.
+// NaN included, and 0 x NaN would reach the sum. Whole pages of them are never read: their id becomes
+// -1, which loads as zeros. The others' rows the softmax warps zero in shared memory (all of them
+// zeroed there: 46.5 -> 48.4 us for 3 windowed requests, 219 -> 234 for 4096 tokens from scratch).
 #pragma once
 
 #include <cuda.h>
@@ -103,6 +106,7 @@ struct AttnArgs {
     CUtensorMap qfew;                  // the same with boxes of few_tokens
     uint16_t* out;
     long long out_stride;              // between tokens, elements
+    bool wide;                         // whether out's rows are aligned to 32 bytes
     const int* table;
     long long table_stride;
     const int* q_start;
@@ -435,6 +439,19 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// 32 bytes to global memory: one store where they are aligned (a row of the output is a lane's, so every
+// 16-byte store of a warp touches 32 lines), else two.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&u)[8], bool aligned) {
+    if (aligned)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                     "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                     : "memory");
+    else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    }
+}
+
 // Bits 0..n-1 of 64, for any n.
 __device__ __forceinline__ uint64_t low_bits(int n) {
     return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
@@ -626,10 +643,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         int base = 0;                      // slots filled by the segments before, by both producers
         uint32_t filled = 0, parity = 0;   // per slot: whether this warp filled it, and the phase
         bool ok = flags[0] == 0;
-        // block ids of key tile kt, one a lane (-1, which reads as zeros, past the keys)
+        // block ids of key tile kt, one a lane: -1, which reads as zeros, where no row sees any of the keys
         auto ids = [&](const AttnWalk& k, int kt) {
             const int key = kt * kAttnKeys + lane * page_rows;
-            return lane < ids_of && key < k.t.hi ? __ldg(a.table + k.r * a.table_stride + (key >> a.page_shift)) : -1;
+            const bool seen = key < k.t.hi && (key < a.sinks || key + page_rows > k.t.lo);
+            return lane < ids_of && seen ? __ldg(a.table + k.r * a.table_stride + (key >> a.page_shift)) : -1;
         };
         for (; w.more() && ok; w.next(a)) {
             const int n = w.tiles();
@@ -648,7 +666,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     if (!ok) break;
                     // a pair's blocks load half of the keys of K, half of the columns of V
                     const int off = is_v ? s * kVK : rank * kKK, key0 = w.key_tile(j) * kAttnKeys + off;
-                    const int boxes = max(0, min(slot_keys >> row_bits, (w.t.hi - key0 + rows - 1) >> row_bits));
+                    // V is filled whole, with zeros past the keys: 0 x what a slot held before may be NaN
+                    int boxes = slot_keys >> row_bits;
+                    if (!is_v) boxes = max(0, min(boxes, (w.t.hi - key0 + rows - 1) >> row_bits));
                     const uint32_t bar = full0 + 8 * slot, dst = smem_u32(ring + slot * Geo::kSlotBytes);
                     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * rows * slot_cols * 2));
                     __syncwarp();
@@ -867,7 +887,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     tmem_wait_ld();
                     if (masked) {
                         uint64_t see = low_bits(p - kk + 1);
-                        if (a.window > 0) see &= ~low_bits(p - a.window + 1 - kk) | low_bits(a.sinks - kk);
+                        if (a.window > 0)
+                        see &= ~low_bits(p - a.window + 1 - kk) | low_bits(a.sinks - kk);
                         const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
@@ -927,8 +948,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     l += s2.x + s2.y;
                     tmem_wait_st();
                 }
-                // V rows that no row sees: zeros
-                // (seen are the keys below the sinks and lo .. hi - 1)
                 if (key0 + kAttnKeys > t.hi || min(t.lo, key0 + kAttnKeys) > max(key0, a.sinks)) {
                     // the V slots of tile j: after K of the first tile, each tile's V follows the next tile's K
                     // (with five slots the tile before is waited for first: a slot's barrier may be one
@@ -939,15 +958,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     for (int s = 0; s < kVS; ++s)
                         ok = mbar_wait(full0 + 8 * ((v0 + s) % kSlots), ((v0 + s) / kSlots) & 1, flags, a.dev_err, wait_ns) && ok;
                     if (ok) {
-                        // keys b0..b1-1 of the tile lie between the sinks and the window, e0.. past the last key
-                        const int b0 = max(0, a.sinks - key0), b1 = min(kAttnKeys, t.lo - key0);
-                        const int e0 = max(0, min(kAttnKeys, t.hi - key0)), nb = max(0, b1 - b0);
-                        for (int i = tid; i < (nb + kAttnKeys - e0) * (kDV / 8); i += kAttnSoftmaxWarps * 32) {
-                            const int at = i / (kDV / 8), ch = i % (kDV / 8), key = at < nb ? b0 + at : e0 + at - nb;
-                            uint8_t* const slot = ring + ((v0 + key / kVK) % kSlots) * Geo::kSlotBytes;
-                            *reinterpret_cast<uint4*>(slot + (ch / 8) * (kVK * 128) + (key % kVK) * 128 + (ch % 8) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
+                        // a thread's 16-byte chunk of the rows, every kStep-th row
+                        constexpr int kChunks = kDV / 8, kStep = kAttnSoftmaxWarps * 32 / kChunks;
+                        const int ch = tid % kChunks;
+                        auto zero = [&](int from, int to) {
+                            from -= key0;
+                            to = min(to - key0, kAttnKeys);
+                            for (int key = from + tid / kChunks; key < to; key += kStep) {
+                                uint8_t* const slot = ring + ((v0 + key / kVK) % kSlots) * Geo::kSlotBytes;
+                                *reinterpret_cast<uint4*>(slot + (ch / 8) * (kVK * 128) + (key % kVK) * 128 + (ch % 8) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                        };
+                        // Keys that no row sees in pages with others that some row does (V's producer leaves out
+                        // whole pages): from the last key on, up to the window, from the sinks on
+                        const int page = min(1 << a.page_shift, kAttnKeys);
+                        const int tail = t.hi & (page - 1) ? t.hi & -kAttnKeys : -1;
+                        const int head = (t.lo & (page - 1)) && t.lo > a.sinks ? t.lo & -kAttnKeys : -1;
+                        const int first = (a.sinks & (page - 1)) && a.sinks < t.lo ? a.sinks & -kAttnKeys : -1;
+                        if (key0 == tail) zero(t.hi, (t.hi + page - 1) & -page);
+                        if (key0 == head) zero(max(t.lo & -page, a.sinks), t.lo);
+                        if (key0 == first) zero(a.sinks, min((a.sinks + page - 1) & -page, t.lo));
                         fence_proxy_async_smem();
                         if (PAIR) fence_acq_rel_cluster();
                     }
@@ -977,13 +1008,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     if (valid && ok) {
                         if (whole) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint4 u;
-                                u.x = pack16<BF16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                                u.y = pack16<BF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                                u.z = pack16<BF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                                u.w = pack16<BF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                                *reinterpret_cast<uint4*>(orow + i + e) = u;
+                            for (int e = 0; e < 32; e += 16) {
+                                uint32_t u[8];
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    u[q] = pack16<BF16>(__uint_as_float(o[e + 2 * q]) * inv, __uint_as_float(o[e + 2 * q + 1]) * inv);
+                                store32(orow + i + e, u, a.wide);
                             }
                         } else {
 #pragma unroll
