@@ -125,6 +125,31 @@ def test_few_levels_with_many_ties(nq):
         check(nq, x.to(dtype), e, settings(12, 1.0, k, 0.7, 0.0))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [4097, 20000, 60000])
+def test_scores_that_grow_with_the_rank(nq, V, dtype):
+    """The worst noise for a choice by trial: every set's best token is its last in the row's order."""
+    x, _ = rows(10, V, dtype, V + 3)
+    order = torch.argsort(x.double(), dim=1, descending=True, stable=True)
+    place = torch.empty_like(order).scatter_(1, order, torch.arange(V, device="cuda").expand(10, V).contiguous())
+    score = place.double() * (20 / V)
+    t = 1.25
+    e = torch.exp((x.double() - x.double().amax(1, keepdim=True)).clamp(min=-60) / t - score).float()
+    k = [0, 0, 0, 300, 3000, 5000, V - 5, 700, 3000, V - 1]
+    p = [0.5, 0.97, 0.999, 1.0, 1.0, 1.0, 1.0, 0.9, 0.5, 0.99]
+    got = nq.sample(x, e, **settings(10, t, k, p, 0.0)).cpu().numpy()
+    d = ((x.double().gather(1, order) - x.double().amax(1, keepdim=True)) / t).cpu().numpy()
+    place = place.cpu().numpy()
+    for i in range(10):
+        n = int((d[i] > -math.inf).sum())
+        n = min(n, k[i]) if k[i] else n
+        w = np.exp(d[i, :n])
+        before, total = np.cumsum(w) - w, w.sum()
+        # the last kept token, whatever an error of 1e-6 makes of the share
+        least, most = (int((before < np.float32(p[i]) * total * f).sum()) if p[i] < 1 else n for f in (1 - 1e-6, 1 + 1e-6))
+        assert least - 1 <= place[i, got[i]] <= most - 1, (i, least, most, place[i, got[i]])
+
+
 def test_equal_scores_take_the_lowest_index(nq):
     x = torch.zeros((2, 5000), device="cuda")
     e = torch.ones((2, 5000), device="cuda")

@@ -7,21 +7,26 @@
 //
 // A row is a thread-block cluster, a slice of the row a block, kept in shared memory when it fits
 // (one read of the logits from memory). Three ways through a row:
-//   * no top-k and no top-p: the cluster's maximum, then one pass that takes the argmax. The score
-//     is first estimated with the fast logarithm; only tokens that could beat the thread's best
-//     are scored exactly.
+//   * no top-k and no top-p: the cluster's maximum, then one pass that takes the argmax (the race).
+//     The score is first estimated with the fast logarithm; only tokens that could beat the
+//     thread's best are scored exactly.
 //   * a cut that few tokens pass (the common case): kept tokens are a prefix of the row's order
 //     (logit descending, index ascending). Every block sorts its threads' maxima; the k-th of
 //     them bounds the block's k-th token from below, so the tokens from there up, little more than k,
 //     hold its first k. They are handed to one block, which sorts them and settles the row: one
 //     barrier of the cluster. top-p alone tries the same with k = 64 if those can hold the share.
-//   * a cut among many tokens: a histogram of counts and weights over the cluster, by the distance
-//     to the maximum, finds the cut's bin; its tokens are sorted by one block, which gives the cut
-//     as (logit, index). A bin of more tokens than that block can sort (far tails, many equal
-//     logits) is cut again by the bits of the logits' ordered integers, at most three times. Then
-//     the pass of the first way over the tokens inside the cut.
-// Weights are summed as 2^-30 fixed point in integers (two 16-bit halves in the histograms), or
-// by each thread in a fixed order: no sum depends on the order of atomics.
+//   * a cut among many tokens: the race over all tokens, then one pass that sums what lies before
+//     its winner. If that is less than k tokens, or than the share p, the winner is kept, and so
+//     is the winner of the kept ones. Else all kept tokens lie before it, and the race is run
+//     again among those. A winner lies at a random place of the mass, so it is kept with the
+//     probability of the kept mass, 1 + ln(1 / kept mass) races on average; the same pass halves the
+//     interval that holds the cut, so that 65 races are the most whatever the noise.
+//   * both such a top-k and a top-p: the share is one of top-k's mass, so top-k's cut is needed itself: a
+//     histogram of the cluster's tokens by the distance to the maximum finds the cut's bin, whose
+//     tokens one block sorts. A bin of more tokens than that block can sort (far tails, many equal
+//     logits) is cut again by the bits of the logits' ordered integers, at most three times.
+// Weights are summed as 2^-30 fixed point in integers, or by each thread in a fixed order: no sum
+// depends on the order of atomics.
 //
 // Bound by the latency of these few steps for few rows, by instructions per token for many (the
 // logits' bytes alone would take a fraction of it).
@@ -52,7 +57,7 @@ constexpr int kSaPer = kSaBins / kSaThreads;   // bins of a thread
 constexpr int kSaList = 4 * kSaThreads;        // tokens the settling block can sort
 constexpr int kSaTryP = 48;                    // tokens a block hands over for top-p alone
 constexpr int kSaMaxCluster = 8;
-constexpr int kSaMaxSlice = 65535;             // 16-bit halves of the weights sum below 2^32
+constexpr int kSaMaxSlice = 65535;
 constexpr int kSaMaxVocab = kSaMaxSlice / 16 * 16 * kSaMaxCluster;
 constexpr int kSaSliceBytes = 160 * 1024;      // most shared memory for a slice
 constexpr float kSaRange = 32.f;               // distance to the maximum covered by the bins
@@ -99,11 +104,9 @@ __device__ __forceinline__ u64 share_of(float p, u64 w) {
     return t > 0 ? t : 1;
 }
 
-struct Found {             // the bin of a cut: counts and weights of the tokens before it and in it
-    int bin, before, count, total;
-    u64 before_w, total_w;
-    int by_count;          // the cut was looked for by count (else by weight)
-    int none;              // no cut
+struct Found {             // the bin of a cut by count: the tokens before it and in it
+    int bin, before, count;
+    int none;              // fewer tokens than that
 };
 
 struct Share {             // what a block hands to the settling one besides its first tokens
@@ -114,12 +117,8 @@ struct Share {             // what a block hands to the settling one besides its
     int fail;              // its first tokens do not fit
 };
 
-struct Cut {               // kept: tokens whose (key, index) rank is at least this; their weight
-    u64 rank, mass;
-};
-
 struct SaShared {
-    unsigned hist[3][kSaBins];                 // count, low and high halves of the weights
+    unsigned hist[kSaBins];
     u64 list[kSaList];
     u64 part[2][kSaMaxCluster];                // cluster exchange, alternating
     u64 part_w[2][kSaMaxCluster];
@@ -127,7 +126,8 @@ struct SaShared {
     u64 warp_w[kSaWarps];
     Share share[kSaMaxCluster];
     Found found;
-    Cut cut;
+    u64 cut;
+    u64 kept, target;                          // of the trials: the least rank known to be kept, the share
     uint32_t bound;
     int listed, verdict;
 };
@@ -156,6 +156,22 @@ __device__ __forceinline__ void unpack_chunk(const uint4& u, float (&x)[8], __ha
     }
 }
 
+__device__ __forceinline__ void load4(const uint8_t* p, float (&x)[4], float) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    x[0] = u.x;
+    x[1] = u.y;
+    x[2] = u.z;
+    x[3] = u.w;
+}
+template <typename T>
+__device__ __forceinline__ void load4(const uint8_t* p, float (&x)[4], T) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    float v[8];
+    unpack_chunk(make_uint4(u.x, u.y, 0, 0), v, T());
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = v[e];
+}
+
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -177,6 +193,9 @@ struct Row {
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = i0 + e >= begin && i0 + e < end ? base[i0 + e] : T(-INFINITY);
         return *reinterpret_cast<const uint4*>(x);
+    }
+    __device__ __forceinline__ float value(int i) const {
+        return as_float(smem ? reinterpret_cast<const T*>(smem)[i - first(0)] : base[i]);
     }
     __device__ __forceinline__ void load(int c, float (&x)[E]) const {
         unpack_chunk(smem ? reinterpret_cast<const uint4*>(smem)[c] : from_global(c), x, T());
@@ -358,33 +377,17 @@ __device__ __forceinline__ int settle(SaShared& s, int n, float m, uint32_t boun
     return settled ? index_of(best) : -1;
 }
 
-// The cut among the n tokens of its bin (in s.list), which follow `before` tokens of weight
-// before_w: the k-th token, or the last whose weight before it is below the target.
+// The at-th (from 0) of the n tokens in s.list, in the row's order.
 template <int N>
-__device__ __forceinline__ Cut cut_in_bin(SaShared& s, int n, uint32_t top, float m, int k, int before, u64 before_w,
-                                          u64 target, const Weigher& weight) {
+__device__ __forceinline__ u64 nth(SaShared& s, int n, int at) {
     const int tid = threadIdx.x;
-    u64 v[N], wt[N], x = 0, y = 0, unused, sum;
+    u64 v[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] = tid * N + j < n ? s.list[tid * N + j] : 0;
     block_sort<N>(v, s.list);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const uint32_t key = (uint32_t)(v[j] >> 32);
-        wt[j] = 0;
-        if (tid * N + j < n) wt[j] = weight(key == top ? 0.f : m - key_value(key));
-        y += wt[j];
-    }
-    const u64 own = y;
-    block_scan(x, y, unused, sum, s);
-    y += before_w - own;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int at = tid * N + j;
-        const bool here = k > 0 ? before + at + 1 == k : y < target && (y + wt[j] >= target || at == n - 1);
-        y += wt[j];
-        if (at < n && here) s.cut = {v[j], y};
-    }
+    for (int j = 0; j < N; ++j)
+        if (tid * N + j == at) s.cut = v[j];
     __syncthreads();
     return s.cut;
 }
@@ -439,6 +442,17 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
     const Weigher weight(temp);
     const Settings set = {p, floor_d, k, by_k, by_p};
 
+    // The noise of the slice on its way to L2, for rows that need all of it.
+    auto prefetch = [&]() {
+        const uintptr_t a0 = (reinterpret_cast<uintptr_t>(noise + row.begin) + 15) & ~(uintptr_t)15;
+        const uintptr_t a1 = reinterpret_cast<uintptr_t>(noise + row.end) & ~(uintptr_t)15;
+        if (tid == 0 && a1 > a0)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a0), "r"((uint32_t)(a1 - a0)) : "memory");
+    };
+    const int cap = kSaList / C;
+    const bool try_few = !greedy && (by_k ? k <= cap : by_p);
+    if (!greedy && !try_few && !(least > 0.f)) prefetch();
+
     // The slice goes to shared memory (all copies in flight at once); every thread's maximum.
     if (a.resident) {
         for (int c = tid; c < row.chunks; c += kSaThreads) {
@@ -460,20 +474,19 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
     }
 
     // ---------------------------------------------------------------- a cut that few tokens pass
-    const int cap = kSaList / C;
-    float top_here;
-    if (!greedy && (by_k ? k <= cap : by_p)) {
+    u64 row_top = 0;
+    if (try_few) {
         // at least `want` of the block's tokens are not below the want-th of its threads' maxima
         const int want = by_k ? k : kSaTryP;
         uint32_t key[1] = {order_key(high)};
-        block_sort<1>(key, reinterpret_cast<uint32_t*>(&s.hist[0][0]));
+        block_sort<1>(key, reinterpret_cast<uint32_t*>(&s.hist[0]));
         if (tid == 0) {
             s.warp[0] = key[0];
             s.listed = 0;
         }
         if (tid == want - 1) s.bound = key[0];
         __syncthreads();
-        top_here = key_value((uint32_t)s.warp[0]);
+        const float top_here = key_value((uint32_t)s.warp[0]);
         const bool all = want > kSaThreads || s.bound <= kSaNone;
         const uint32_t low = all ? kSaNone + 1 : s.bound;
         const float low_value = key_value(low);
@@ -509,6 +522,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
             __syncthreads();
         else
             block_scan(x, y, all_w, all_lw, s);
+        if (!by_k && (float)all_lw < p * (float)all_w && !(least > 0.f)) prefetch();      // not likely to do
         if (tid < C) {
             Share h;
             h.weight = (float)all_w;
@@ -570,12 +584,11 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
             cl.sync();
             if (s.verdict) return;
         }
+        row_top = order_key(m);
     } else {
-        top_here = key_value((uint32_t)block_max(order_key(high), s));
+        row_top = cluster_max(order_key(high));
     }
-
-    // ---------------------------------------------------------------- the row's maximum
-    const uint32_t top = (uint32_t)cluster_max(order_key(top_here));
+    const uint32_t top = (uint32_t)row_top;
     if (top <= kSaNone) {                          // nothing to choose from
         if (rank == 0 && tid == 0) a.tokens[r] = -1;
         return;
@@ -598,103 +611,65 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
     const bool inf_row = m == INFINITY;
     auto below = [&](float x) { return inf_row ? (x == INFINITY ? 0.f : INFINITY) : m - x; };
 
-    // ---------------------------------------------------------------- a cut among many tokens
-    auto add = [&](unsigned bin, float d) {
-        atomicAdd(&s.hist[0][bin], 1u);
-        if (by_p) {
-            const unsigned w = weight(d);
-            if (w & 0xFFFFu) atomicAdd(&s.hist[1][bin], w & 0xFFFFu);
-            if (w >> 16) atomicAdd(&s.hist[2][bin], w >> 16);
-        }
-    };
+    // Tokens that may be kept: those above `from`, i.e. of larger values than from_value or of equal ones and
+    // lower indices than from_index.
+    u64 from = ((u64)kSaNone << 32) | 0xFFFFFFFFu;
+    float from_value = -INFINITY;
+    uint32_t from_index = 0;
+    auto value_of = [](u64 v) { return key_value((uint32_t)(v >> 32)); };
+    auto place_of = [](u64 v) { return 0xFFFFFFFFu - (uint32_t)v; };
+
+    // ---------------------------------------------------------------- top-k's cut among many tokens
     auto clear = [&]() {
         __syncthreads();
         if (tid == 0) s.listed = 0;
-        for (int i = tid; i < 3 * kSaBins; i += kSaThreads) (&s.hist[0][0])[i] = 0;
+        for (int i = tid; i < kSaBins; i += kSaThreads) s.hist[i] = 0;
         __syncthreads();
     };
-    // The bin where the count (with `base` tokens before the bins) reaches kk, or where the weight
-    // (with base_w before) reaches the share p of `mass` (0: of the total found here). kk <= 0: by
-    // weight. A count that is not reached turns into the search by weight.
-    auto find = [&](int kk, int base, u64 base_w, u64 mass) {
+    // The bin of the k-th token, `base` tokens lying before the bins.
+    auto find = [&](int base) {
         if (tid == 0) s.found.none = 1;
         cl.sync();
         const int sec = kSaBins / C, per = sec > kSaThreads ? sec / kSaThreads : 1;
         const int b0 = rank * sec + tid * per;
         const bool mine = tid * per < sec;
         unsigned cnt[kSaPer];
-        u64 wt[kSaPer];
-        u64 x = 0, y = 0, tx, ty;
+        u64 x = 0, unused = 0, tx, ty;
 #pragma unroll
         for (int i = 0; i < kSaPer; ++i) {
             cnt[i] = 0;
-            wt[i] = 0;
             if (mine && i < per) {
-                for (int c = 0; c < C; ++c) {
-                    const unsigned* h = C > 1 ? cl.map_shared_rank(&s.hist[0][0], c) : &s.hist[0][0];
-                    cnt[i] += h[b0 + i];
-                    wt[i] += ((u64)h[2 * kSaBins + b0 + i] << 16) + h[kSaBins + b0 + i];
-                }
+#pragma unroll
+                for (int c = 0; c < kSaMaxCluster; ++c)
+                    if (c < C) cnt[i] += cl.map_shared_rank(&s.hist[0], c)[b0 + i];
                 x += cnt[i];
-                y += wt[i];
             }
         }
-        const u64 ox = x, oy = y;
-        block_scan(x, y, tx, ty, s);
-        x -= ox;
-        y -= oy;
-        u64 total = tx, total_w = ty;
+        const u64 own = x;
+        block_scan(x, unused, tx, ty, s);
+        x -= own;
         if (C > 1) {
-            exchange(tx, ty);
-            total = total_w = 0;
-            for (int i = 0; i < C; ++i) {
-                if (i < rank) {
-                    x += s.part[turn][i];
-                    y += s.part_w[turn][i];
-                }
-                total += s.part[turn][i];
-                total_w += s.part_w[turn][i];
-            }
+            exchange(tx, 0);
+            for (int i = 0; i < rank; ++i) x += s.part[turn][i];
         }
         x += base;
-        y += base_w;
-        const bool by_count = kk > 0 && (u64)kk <= base + total;
-        const u64 target = by_p ? share_of(p, mass ? mass : base_w + total_w) : ~0ull;
-        if (by_count || by_p) {
 #pragma unroll
-            for (int i = 0; i < kSaPer; ++i) {
-                if (mine && i < per && cnt[i] > 0 &&
-                    (by_count ? x < (u64)kk && x + cnt[i] >= (u64)kk
-                              : y < target && y + wt[i] >= target)) {
-                    const Found f = {b0 + i, (int)x, (int)cnt[i], (int)(base + total), y, base_w + total_w, by_count, 0};
-                    for (int c = 0; c < C; ++c) *cl.map_shared_rank(&s.found, c) = f;
-                }
-                x += cnt[i];
-                y += wt[i];
+        for (int i = 0; i < kSaPer; ++i) {
+            if (mine && i < per && x < (u64)k && x + cnt[i] >= (u64)k) {
+                const Found f = {b0 + i, (int)x, (int)cnt[i], 0};
+                for (int c = 0; c < C; ++c) *cl.map_shared_rank(&s.found, c) = f;
             }
+            x += cnt[i];
         }
         cl.sync();
         return s.found;
     };
-
-    u64 cut = ranked(kSaNone + 1, 0x7FFFFFFF);     // kept: ranks from here up
-    if (by_k || by_p) {
+    if (by_k && by_p) {
         const float scale = (kSaBins / kSaRange) / fmaxf(temp, kSaLeastT);
         // the last bin takes everything past the range
         auto bin_of = [&](float d) { return (int)fminf(d * scale, (float)(kSaBins - 1)); };
-        auto histogram = [&]() {
-            clear();
-            for (int c = tid; c < row.chunks; c += kSaThreads) {
-                float x[E];
-                row.load(c, x);
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (x[e] > -INFINITY) add(bin_of(below(x[e])), below(x[e]));
-            }
-        };
-        histogram();
-        // The cut of the bin f, if its tokens can be sorted: all blocks hand them to the first.
-        auto sort_bin = [&](const Found& f, u64 mass) {
+        // The cut in the bin f, if its tokens can be sorted: all blocks hand them to the first.
+        auto sort_bin = [&](const Found& f) {
             u64* const list = cl.map_shared_rank(&s.list[0], 0);
             int* const listed = cl.map_shared_rank(&s.listed, 0);
             for (int c = tid; c < row.chunks; c += kSaThreads) {
@@ -711,49 +686,15 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
             }
             cl.sync();
             if (rank == 0) {
-                const u64 target = by_p ? share_of(p, mass) : ~0ull;
-                const int kk = f.by_count ? k : 0;
-                const Cut found = f.count <= kSaThreads
-                                      ? cut_in_bin<1>(s, f.count, top, m, kk, f.before, f.before_w, target, weight)
-                                      : cut_in_bin<4>(s, f.count, top, m, kk, f.before, f.before_w,
-                                                                         target, weight);
+                const int at = k - 1 - f.before;
+                const u64 found = f.count <= kSaThreads ? nth<1>(s, f.count, at) : nth<4>(s, f.count, at);
                 if (tid > 0 && tid < C) *cl.map_shared_rank(&s.cut, tid) = found;
-                if (tid == 0) s.listed = 0;
             }
             cl.sync();
             return s.cut;
         };
-        // From the interval [lo, hi] of keys (tokens above: base, base_w) to one key.
-        struct KeyCut {
-            uint32_t key;
-            int before;
-            u64 before_w;
-        };
-        auto refine = [&](uint32_t lo, uint32_t hi, int kk, int base, u64 base_w, u64 mass) {
-            while (lo < hi) {
-                const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
-                clear();
-                for (int c = tid; c < row.chunks; c += kSaThreads) {
-                    float x[E];
-                    row.load(c, x);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const uint32_t key = order_key(x[e]);
-                        if (key >= lo && key <= hi) add((hi - key) >> shift, below(x[e]));
-                    }
-                }
-                const Found g = find(kk, base, base_w, mass);
-                if (g.none) break;             // cannot be: the interval holds the cut
-                base = g.before;
-                base_w = g.before_w;
-                hi -= (uint32_t)g.bin << shift;
-                const uint32_t least_key = hi - ((1u << shift) - 1);
-                lo = least_key > lo && least_key <= hi ? least_key : lo;
-            }
-            return KeyCut{hi, base, base_w};
-        };
-        // The cut of the bin f by its keys' bits: one key, and the `ties` first tokens at it.
-        auto refine_bin = [&](const Found& f, u64 mass) {
+        // The same by the bits of the bin's keys: down to one key, and the first tokens at it.
+        auto refine_bin = [&](const Found& f) {
             u64 most = 0, fewest = 0;
             for (int c = tid; c < row.chunks; c += kSaThreads) {
                 float x[E];
@@ -766,20 +707,30 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
                         fewest = max(fewest, (u64)(0xFFFFFFFFu - key));
                     }
             }
-            most = cluster_max(most);
-            fewest = cluster_max(fewest);
-            const KeyCut g = refine(0xFFFFFFFFu - (uint32_t)fewest, (uint32_t)most, f.by_count ? k : 0, f.before, f.before_w, mass);
-            const u64 w = weight(g.key == top ? 0.f : below(key_value(g.key)));
-            u64 ties;
-            if (f.by_count) {
-                ties = (u64)(k - g.before);
-            } else {
-                // tokens at the key whose mass before is below the share
-                const u64 target = share_of(p, mass);
-                ties = w > 0 && g.before_w < target ? (target - g.before_w + w - 1) / w : 0;
+            uint32_t hi = (uint32_t)cluster_max(most), lo = 0xFFFFFFFFu - (uint32_t)cluster_max(fewest);
+            int before = f.before;
+            while (lo < hi) {
+                const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
+                clear();
+                for (int c = tid; c < row.chunks; c += kSaThreads) {
+                    float x[E];
+                    row.load(c, x);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const uint32_t key = order_key(x[e]);
+                        if (key >= lo && key <= hi) atomicAdd(&s.hist[(hi - key) >> shift], 1u);
+                    }
+                }
+                const Found g = find(before);
+                if (g.none) break;             // cannot be: the interval holds the cut
+                before = g.before;
+                hi -= (uint32_t)g.bin << shift;
+                const uint32_t least_key = hi - ((1u << shift) - 1);
+                lo = least_key > lo && least_key <= hi ? least_key : lo;
             }
-            // the index of the last of them
-            const float at = key_value(g.key);
+            // the index of the last of the tokens at the key that are kept
+            const u64 ties = (u64)(k - before);
+            const float at = key_value(hi);
             u64 x = 0, y = 0, tx, ty, seen = 0, last = 0;
             for (int c = tid; c < row.chunks; c += kSaThreads) {
                 float v[E];
@@ -814,25 +765,26 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
                     if (v[e] == at && x++ < ties) last = (u64)(row.first(c) + e) + 1;
             }
             last = cluster_max(last);
-            return Cut{ranked(g.key, (int)last - 1), g.before_w + ties * w};
+            return ranked(hi, (int)last - 1);
         };
-        auto cut_of = [&](const Found& f, u64 mass) { return f.count <= kSaList ? sort_bin(f, mass) : refine_bin(f, mass); };
-        const Found f = find(by_k ? k : 0, 0, 0, 0);
+        clear();
+        for (int c = tid; c < row.chunks; c += kSaThreads) {
+            float x[E];
+            row.load(c, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (x[e] > -INFINITY) atomicAdd(&s.hist[bin_of(below(x[e]))], 1u);
+        }
+        const Found f = find(0);
         if (!f.none) {
-            const Cut g = cut_of(f, f.total_w);
-            cut = g.rank;
-            if (f.by_count && by_p) {
-                // the share of the mass that top-k kept: the same histogram, unless the refinement took it
-                if (f.count > kSaList) histogram();
-                const Found fp = find(0, 0, 0, g.mass);
-                if (!fp.none) cut = max(cut, cut_of(fp, g.mass).rank);
-            }
+            const u64 last = f.count <= kSaList ? sort_bin(f) : refine_bin(f);
+            from = last - 1;               // at the last kept token's value, one index further
+            from_value = value_of(last);
+            from_index = place_of(last) + 1;
         }
     }
 
     // ---------------------------------------------------------------- the race over the row
-    const float cut_value = key_value((uint32_t)(cut >> 32));
-    const int cut_index = index_of(cut);
     // First by an estimate of the score (fast logarithm, product with 1 / T), each thread its best
     // two; then exactly, where a thread's best is within the estimate's error of the block's.
     const float floor_e = -floor_d * temp;
@@ -847,7 +799,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
         unsigned kept = 0, edge = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {              // false for NaN and -inf
-            const bool in = v[e] > cut_value || (v[e] == cut_value && i0 + e <= cut_index);
+            const bool in = v[e] > from_value || (v[e] == from_value && (uint32_t)(i0 + e) < from_index);
             const float d = below(v[e]);
             kept |= in && !(d > floor_hi) ? 1u << e : 0u;
             edge |= d > floor_lo ? 1u << e : 0u;
@@ -876,56 +828,146 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
         const float sc = fmaf(-0.6931472f, __log2f(z), -below(v) * step);
         return sc == sc ? sc : -INFINITY;
     };
-    float first = -INFINITY, second = -INFINITY;
-    int first_i = -1;
-    float v[E], z[E];
-    unsigned kept = fetch(tid, v, z);
-    for (int c = tid; c < row.chunks; c += kSaThreads) {
-        float vn[E], zn[E];
-        const unsigned kept_next = fetch(c + kSaThreads, vn, zn);
-        const int i0 = row.first(c);
+    auto race = [&]() {
+        float first = -INFINITY, second = -INFINITY;
+        int first_i = -1;
+        float v[E], z[E];
+        // all tokens: four loads of noise in flight, nothing to choose
+        const bool all = from_value == -INFINITY && !(least > 0.f) && aligned && row.smem && !inf_row;
+        if (all) {
+            const int groups = (row.lead + row.end - row.begin + 3) / 4;
+            for (int g = tid; g < groups; g += 4 * kSaThreads) {
+                float4 u[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float sc = estimate(v[e], z[e]);
-            const bool in = (kept >> e) & 1, over = in && (sc > first || first_i < 0);
-            second = over ? first : (in ? fmaxf(second, sc) : second);
-            first = over ? sc : first;
-            first_i = over ? i0 + e : first_i;
-        }
-        kept = kept_next;
+                for (int j = 0; j < 4; ++j) {
+                    const int i0 = row.first(0) + 4 * (g + j * kSaThreads);
+                    if (i0 >= row.begin && i0 + 4 <= row.end) {
+                        u[j] = __ldg(reinterpret_cast<const float4*>(noise + i0));
+                    } else {
+                        float w[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            v[e] = vn[e];
-            z[e] = zn[e];
-        }
-    }
-    // the estimate is off by less than `off` (unusual temperatures: not relied on)
-    const float lead = key_value((uint32_t)block_max(first_i < 0 ? 0 : order_key(first), s));
-    auto may_win = [&](float sc) {
-        if (!scaled.usual || lead == -INFINITY) return true;
-        return sc > -INFINITY && !(sc + (2e-3f + 4e-6f * fabsf(sc)) < lead);
-    };
-    u64 best = 0;
-    auto exact = [&](float l, float noise_i, int i) {
-        float sc = scaled(below(l)) - logf(noise_i);
-        if (sc != sc) sc = -INFINITY;
-        best = max(best, ranked(order_key(sc), i));
-    };
-    if (first_i >= 0 && may_win(first)) {
-        if (may_win(second)) {                     // more than one of the thread's tokens
-            for (int c = tid; c < row.chunks; c += kSaThreads) {
-                kept = fetch(c, v, z);
+                        for (int e = 0; e < 4; ++e) w[e] = i0 + e >= row.begin && i0 + e < row.end ? __ldg(noise + i0 + e) : 1.f;
+                        u[j] = make_float4(w[0], w[1], w[2], w[3]);
+                    }
+                }
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if ((kept >> e) & 1 && may_win(estimate(v[e], z[e]))) exact(v[e], z[e], row.first(c) + e);
+                for (int j = 0; j < 4; ++j) {
+                    const int at = 4 * (g + j * kSaThreads);
+                    if (at >= 4 * groups) break;
+                    float x[4];
+                    load4(row.smem + at * sizeof(T), x, T());
+                    const float w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {          // NaN is never over
+                        const float sc = fmaf(-0.6931472f, __log2f(w[e]), (x[e] - m) * step);
+                        const bool over = sc > first;
+                        second = over ? first : fmaxf(second, sc);
+                        first = over ? sc : first;
+                        first_i = over ? row.first(0) + at + e : first_i;
+                    }
+                }
             }
-        } else {
-            float l = as_float(row.base[first_i]);
-            exact(l, noise[first_i], first_i);
         }
+        unsigned kept = all ? 0u : fetch(tid, v, z);
+        for (int c = tid; c < row.chunks && !all; c += kSaThreads) {
+            float vn[E], zn[E];
+            const unsigned kept_next = fetch(c + kSaThreads, vn, zn);
+            const int i0 = row.first(c);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float sc = estimate(v[e], z[e]);
+                const bool in = (kept >> e) & 1, over = in && (sc > first || first_i < 0);
+                second = over ? first : (in ? fmaxf(second, sc) : second);
+                first = over ? sc : first;
+                first_i = over ? i0 + e : first_i;
+            }
+            kept = kept_next;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                v[e] = vn[e];
+                z[e] = zn[e];
+            }
+        }
+        // the estimate is off by less than `off` (unusual temperatures: not relied on)
+        const float lead = key_value((uint32_t)block_max(first_i < 0 && !all ? 0 : order_key(first), s));
+        auto may_win = [&](float sc) {
+            if (!scaled.usual || lead == -INFINITY) return true;
+            return sc > -INFINITY && !(sc + (2e-3f + 4e-6f * fabsf(sc)) < lead);
+        };
+        u64 best = 0;
+        auto exact = [&](float l, float noise_i, int i) {
+            float sc = scaled(below(l)) - logf(noise_i);
+            if (sc != sc) sc = -INFINITY;
+            best = max(best, ranked(order_key(sc), i));
+        };
+        if (lead == -INFINITY || (first_i >= 0 && may_win(first))) {
+            if (lead == -INFINITY || may_win(second)) {        // more than one of the thread's tokens
+                for (int c = tid; c < row.chunks; c += kSaThreads) {
+                    kept = fetch(c, v, z);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if ((kept >> e) & 1 && may_win(estimate(v[e], z[e]))) exact(v[e], z[e], row.first(c) + e);
+                }
+            } else {
+                exact(row.value(first_i), noise[first_i], first_i);
+            }
+        }
+        return index_of(cluster_max(best));
+    };
+
+    // ---------------------------------------------------------------- the winner, if it is kept
+    // Ranks from s.kept up are kept, ranks up to `from` are not. What lies before a token is counted or, for
+    // top-p, weighed; the share is one of the weight of the first round's set.
+    if (tid == 0) {
+        s.kept = ((u64)top << 32) | 0xFFFFFFFFu;
+        s.target = by_p ? 0 : (u64)k;
     }
-    const u64 winner = cluster_max(best);
-    if (rank == 0 && tid == 0) a.tokens[r] = index_of(winner);
+    int winner;
+    for (int round = 0;; ++round) {
+        winner = race();
+        if (!by_k && !by_p) break;
+        const float won = as_float(row.base[winner]);
+        const u64 won_at = ranked(order_key(won), winner);
+        const u64 hi = s.kept;
+        u64 target = s.target;
+        if (won_at >= hi) break;
+        u64 mid = won_at + (hi - won_at) / 2;
+        if ((mid >> 32) == 0x7FFFFFFFu) mid = 0x7FFFFFFEFFFFFFFFull;       // as a value that key equals 0
+        const float than = round == 0 ? from_value : value_of(mid);
+        const uint32_t than_index = round == 0 ? from_index : place_of(mid);
+        u64 x = 0, y = 0, before_mid, before;      // the first round: the whole set in place of before_mid
+        for (int c = tid; c < row.chunks; c += kSaThreads) {
+            float v[E];
+            row.load(c, v);
+            const uint32_t i0 = (uint32_t)row.first(c);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const unsigned w = by_p ? weight(below(v[e])) : 1u;
+                x += v[e] > than || (v[e] == than && i0 + e < than_index) ? w : 0u;
+                y += v[e] > won || (v[e] == won && i0 + e < (uint32_t)winner) ? w : 0u;
+            }
+        }
+        block_scan(x, y, before_mid, before, s);
+        if (C > 1) {
+            exchange(before_mid, before);
+            before_mid = before = 0;
+            for (int i = 0; i < C; ++i) {
+                before_mid += s.part[turn][i];
+                before += s.part_w[turn][i];
+            }
+        }
+        if (round == 0 && by_p) target = share_of(p, before_mid);
+        if (before < target) break;
+        from = won_at;
+        if (round > 0 && before_mid >= target) from = max(from, mid);
+        if (tid == 0) {                            // read again after the race's barriers
+            if (round > 0 && before_mid < target) s.kept = mid;
+            s.target = target;
+        }
+        from_value = value_of(from);
+        from_index = place_of(from);
+    }
+    if (rank == 0 && tid == 0) a.tokens[r] = winner;
 }
 
 template <typename T>
