@@ -21,15 +21,20 @@
 //     again among those. A winner lies at a random place of the mass, so it is kept with the
 //     probability of the kept mass, 1 + ln(1 / kept mass) races on average; the same pass halves the
 //     interval that holds the cut, so that 65 races are the most whatever the noise.
-//   * both such a top-k and a top-p: the share is one of top-k's mass, so top-k's cut is needed itself: a
-//     histogram of the cluster's tokens by the distance to the maximum finds the cut's bin, whose
-//     tokens one block sorts. A bin of more tokens than that block can sort (far tails, many equal
-//     logits) is cut again by the bits of the logits' ordered integers, at most three times.
+//   * both such a top-k and a top-p: the share is one of top-k's mass. A histogram of the cluster's
+//     tokens by the distance to the maximum finds the bin of top-k's cut, which bounds that mass
+//     to a few tokens' weights: enough to judge nearly every winner. Else the bin's tokens are sorted by
+//     one block; a bin of more tokens than that block can sort (far tails, many equal logits) is
+//     cut again by the bits of the logits' ordered integers, at most three times.
+// The race lists the tokens that may be kept in shared memory, so that all threads share them
+// (64 rows with min-p 31 -> 20 us); a race over all tokens needs no list.
 // Weights are summed as 2^-30 fixed point in integers, or by each thread in a fixed order: no sum
 // depends on the order of atomics.
 //
-// Bound by the latency of these few steps for few rows, by instructions per token for many (the
-// logits' bytes alone would take a fraction of it).
+// Bound by the latency of these few steps for few rows, by instructions per token and barriers
+// for many (the logits' bytes alone would take a fraction of it). Measured: one row of 152064 bf16,
+// top-k 50 and top-p 0.9, 10.2 us; 64 of them 17; 64 with mixed settings 47; 256 of 128257 fp32 124. With
+// histograms of the mass in place of the trials the mixed ones took 79 and 157.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -55,11 +60,13 @@ constexpr int kSaWarps = kSaThreads / 32;
 constexpr int kSaBins = 2048;
 constexpr int kSaPer = kSaBins / kSaThreads;   // bins of a thread
 constexpr int kSaList = 4 * kSaThreads;        // tokens the settling block can sort
+constexpr int kSaTokens = kSaBins + 2 * kSaList;   // kept tokens a block lists before it scores them
 constexpr int kSaTryP = 48;                    // tokens a block hands over for top-p alone
 constexpr int kSaMaxCluster = 8;
 constexpr int kSaMaxSlice = 65535;
 constexpr int kSaMaxVocab = kSaMaxSlice / 16 * 16 * kSaMaxCluster;
 constexpr int kSaSliceBytes = 160 * 1024;      // most shared memory for a slice
+constexpr int kSaTwoBytes = 86 * 1024;          // up to here two blocks fit an SM
 constexpr float kSaRange = 32.f;               // distance to the maximum covered by the bins
 constexpr float kSaLeastT = 0.75f;             // in units of max(T, this)
 constexpr float kSaOne = 1073741824.f;         // 2^30: the weight of the maximum
@@ -109,6 +116,18 @@ struct Found {             // the bin of a cut by count: the tokens before it an
     int none;              // fewer tokens than that
 };
 
+// Tokens of a higher rank than (at, index): from `next` up, or `at` itself below the index.
+struct Above {
+    float at, next;
+    int index;
+    __device__ __forceinline__ explicit Above(u64 rank)
+        : at(key_value((uint32_t)(rank >> 32))), next(key_value((uint32_t)(rank >> 32) + 1)),
+          index((int)min(0xFFFFFFFFu - (uint32_t)rank, 0x7FFFFFFFu)) {}
+    // for a chunk of n tokens from i0: values from here up, and whether the index falls inside
+    __device__ __forceinline__ float least(int i0, int n) const { return i0 + n <= index ? at : next; }
+    __device__ __forceinline__ bool inside(int i0, int n) const { return i0 < index && i0 + n > index; }
+};
+
 struct Share {             // what a block hands to the settling one besides its first tokens
     float weight, listed_weight;   // sums of its tokens' weights and of the handed ones, for its own maximum
     float top;             // its maximum
@@ -118,8 +137,13 @@ struct Share {             // what a block hands to the settling one besides its
 };
 
 struct SaShared {
-    unsigned hist[kSaBins];
-    u64 list[kSaList];
+    union {
+        struct {
+            unsigned hist[kSaBins];
+            u64 list[kSaList];
+        };
+        int kept_tokens[kSaTokens];
+    };
     u64 part[2][kSaMaxCluster];                // cluster exchange, alternating
     u64 part_w[2][kSaMaxCluster];
     u64 warp[kSaWarps];
@@ -127,7 +151,7 @@ struct SaShared {
     Share share[kSaMaxCluster];
     Found found;
     u64 cut;
-    u64 kept, target;                          // of the trials: the least rank known to be kept, the share
+    u64 kept, target, target_hi;               // of the trials: the least rank known to be kept; bounds of the share
     uint32_t bound;
     int listed, verdict;
 };
@@ -392,8 +416,8 @@ __device__ __forceinline__ u64 nth(SaShared& s, int n, int at) {
     return s.cut;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs a) {
+template <typename T, int PerSm>
+__global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t sa_slice[];
     __shared__ SaShared s;
     cg::cluster_group cl = cg::this_cluster();
@@ -611,18 +635,9 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
     const bool inf_row = m == INFINITY;
     auto below = [&](float x) { return inf_row ? (x == INFINITY ? 0.f : INFINITY) : m - x; };
 
-    // Tokens that may be kept: those above `from`, i.e. of larger values than from_value or of equal ones and
-    // lower indices than from_index.
-    u64 from = ((u64)kSaNone << 32) | 0xFFFFFFFFu;
-    float from_value = -INFINITY;
-    uint32_t from_index = 0;
-    auto value_of = [](u64 v) { return key_value((uint32_t)(v >> 32)); };
-    auto place_of = [](u64 v) { return 0xFFFFFFFFu - (uint32_t)v; };
-
     // ---------------------------------------------------------------- top-k's cut among many tokens
     auto clear = [&]() {
         __syncthreads();
-        if (tid == 0) s.listed = 0;
         for (int i = tid; i < kSaBins; i += kSaThreads) s.hist[i] = 0;
         __syncthreads();
     };
@@ -664,109 +679,113 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
         cl.sync();
         return s.found;
     };
-    if (by_k && by_p) {
-        const float scale = (kSaBins / kSaRange) / fmaxf(temp, kSaLeastT);
-        // the last bin takes everything past the range
-        auto bin_of = [&](float d) { return (int)fminf(d * scale, (float)(kSaBins - 1)); };
-        // The cut in the bin f, if its tokens can be sorted: all blocks hand them to the first.
-        auto sort_bin = [&](const Found& f) {
-            u64* const list = cl.map_shared_rank(&s.list[0], 0);
-            int* const listed = cl.map_shared_rank(&s.listed, 0);
-            for (int c = tid; c < row.chunks; c += kSaThreads) {
-                float x[E];
-                row.load(c, x);
-                unsigned hit = 0;
+    const float scale = (kSaBins / kSaRange) / fmaxf(temp, kSaLeastT);
+    // the last bin takes everything past the range
+    auto place = [&](float d) { return fminf(d * scale, (float)(kSaBins - 1)); };
+    auto bin_of = [&](float d) { return (int)place(d); };
+    // The cut in the bin f, if its tokens can be sorted: all blocks hand them to the first.
+    auto sort_bin = [&](const Found& f) {
+        u64* const list = cl.map_shared_rank(&s.list[0], 0);
+        int* const listed = cl.map_shared_rank(&s.listed, 0);
+        if (tid == 0) s.listed = 0;
+        cl.sync();
+        for (int c = tid; c < row.chunks; c += kSaThreads) {
+            float x[E];
+            row.load(c, x);
+            unsigned hit = 0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) hit |= x[e] > -INFINITY && bin_of(below(x[e])) == f.bin ? 1u << e : 0u;
-                if (hit) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if ((hit >> e) & 1) list[atomicAdd(listed, 1)] = ranked(order_key(x[e]), row.first(c) + e);
-                }
-            }
-            cl.sync();
-            if (rank == 0) {
-                const int at = k - 1 - f.before;
-                const u64 found = f.count <= kSaThreads ? nth<1>(s, f.count, at) : nth<4>(s, f.count, at);
-                if (tid > 0 && tid < C) *cl.map_shared_rank(&s.cut, tid) = found;
-            }
-            cl.sync();
-            return s.cut;
-        };
-        // The same by the bits of the bin's keys: down to one key, and the first tokens at it.
-        auto refine_bin = [&](const Found& f) {
-            u64 most = 0, fewest = 0;
-            for (int c = tid; c < row.chunks; c += kSaThreads) {
-                float x[E];
-                row.load(c, x);
+            for (int e = 0; e < E; ++e) hit |= x[e] > -INFINITY && bin_of(below(x[e])) == f.bin ? 1u << e : 0u;
+            if (hit) {
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (x[e] > -INFINITY && bin_of(below(x[e])) == f.bin) {
-                        const uint32_t key = order_key(x[e]);
-                        most = max(most, (u64)key);
-                        fewest = max(fewest, (u64)(0xFFFFFFFFu - key));
-                    }
+                    if ((hit >> e) & 1) list[atomicAdd(listed, 1)] = ranked(order_key(x[e]), row.first(c) + e);
             }
-            uint32_t hi = (uint32_t)cluster_max(most), lo = 0xFFFFFFFFu - (uint32_t)cluster_max(fewest);
-            int before = f.before;
-            while (lo < hi) {
-                const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
-                clear();
-                for (int c = tid; c < row.chunks; c += kSaThreads) {
-                    float x[E];
-                    row.load(c, x);
+        }
+        cl.sync();
+        if (rank == 0) {
+            const int at = k - 1 - f.before;
+            const u64 found = f.count <= kSaThreads ? nth<1>(s, f.count, at) : nth<4>(s, f.count, at);
+            if (tid > 0 && tid < C) *cl.map_shared_rank(&s.cut, tid) = found;
+        }
+        cl.sync();
+        return s.cut;
+    };
+    // The same by the bits of the bin's keys: down to one key, and the first tokens at it.
+    auto refine_bin = [&](const Found& f) {
+        u64 most = 0, fewest = 0;
+        for (int c = tid; c < row.chunks; c += kSaThreads) {
+            float x[E];
+            row.load(c, x);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const uint32_t key = order_key(x[e]);
-                        if (key >= lo && key <= hi) atomicAdd(&s.hist[(hi - key) >> shift], 1u);
-                    }
+            for (int e = 0; e < E; ++e)
+                if (x[e] > -INFINITY && bin_of(below(x[e])) == f.bin) {
+                    const uint32_t key = order_key(x[e]);
+                    most = max(most, (u64)key);
+                    fewest = max(fewest, (u64)(0xFFFFFFFFu - key));
                 }
-                const Found g = find(before);
-                if (g.none) break;             // cannot be: the interval holds the cut
-                before = g.before;
-                hi -= (uint32_t)g.bin << shift;
-                const uint32_t least_key = hi - ((1u << shift) - 1);
-                lo = least_key > lo && least_key <= hi ? least_key : lo;
-            }
-            // the index of the last of the tokens at the key that are kept
-            const u64 ties = (u64)(k - before);
-            const float at = key_value(hi);
-            u64 x = 0, y = 0, tx, ty, seen = 0, last = 0;
+        }
+        uint32_t hi = (uint32_t)cluster_max(most), lo = 0xFFFFFFFFu - (uint32_t)cluster_max(fewest);
+        int before = f.before;
+        while (lo < hi) {
+            const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
+            clear();
             for (int c = tid; c < row.chunks; c += kSaThreads) {
-                float v[E];
+                float x[E];
+                row.load(c, x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const uint32_t key = order_key(x[e]);
+                    if (key >= lo && key <= hi) atomicAdd(&s.hist[(hi - key) >> shift], 1u);
+                }
+            }
+            const Found g = find(before);
+            if (g.none) break;             // cannot be: the interval holds the cut
+            before = g.before;
+            hi -= (uint32_t)g.bin << shift;
+            const uint32_t least_key = hi - ((1u << shift) - 1);
+            lo = least_key > lo && least_key <= hi ? least_key : lo;
+        }
+        // the index of the last of the tokens at the key that are kept
+        const u64 ties = (u64)(k - before);
+        const float at = key_value(hi);
+        u64 x = 0, y = 0, tx, ty, seen = 0, last = 0;
+        for (int c = tid; c < row.chunks; c += kSaThreads) {
+            float v[E];
+            row.load(c, v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x += v[e] == at ? 1 : 0;
+        }
+        block_scan(x, y, tx, ty, s);
+        if (C > 1) {
+            exchange(tx, 0);
+            for (int i = 0; i < rank; ++i) seen += s.part[turn][i];
+        }
+        for (int c0 = 0; c0 < row.chunks; c0 += kSaThreads) {
+            const int c = c0 + tid;
+            float v[E];
+            u64 own = 0;
+            if (c < row.chunks) {
                 row.load(c, v);
+            } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e) x += v[e] == at ? 1 : 0;
+                for (int e = 0; e < E; ++e) v[e] = -INFINITY;
             }
+#pragma unroll
+            for (int e = 0; e < E; ++e) own += v[e] == at ? 1 : 0;
+            x = own;
+            y = 0;
             block_scan(x, y, tx, ty, s);
-            if (C > 1) {
-                exchange(tx, 0);
-                for (int i = 0; i < rank; ++i) seen += s.part[turn][i];
-            }
-            for (int c0 = 0; c0 < row.chunks; c0 += kSaThreads) {
-                const int c = c0 + tid;
-                float v[E];
-                u64 own = 0;
-                if (c < row.chunks) {
-                    row.load(c, v);
-                } else {
+            x += seen - own;                   // tokens at the cut before this chunk
+            seen += tx;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[e] = -INFINITY;
-                }
-#pragma unroll
-                for (int e = 0; e < E; ++e) own += v[e] == at ? 1 : 0;
-                x = own;
-                y = 0;
-                block_scan(x, y, tx, ty, s);
-                x += seen - own;                   // tokens at the cut before this chunk
-                seen += tx;
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (v[e] == at && x++ < ties) last = (u64)(row.first(c) + e) + 1;
-            }
-            last = cluster_max(last);
-            return ranked(hi, (int)last - 1);
-        };
+            for (int e = 0; e < E; ++e)
+                if (v[e] == at && x++ < ties) last = (u64)(row.first(c) + e) + 1;
+        }
+        last = cluster_max(last);
+        return ranked(hi, (int)last - 1);
+    };
+    Found f = {0, 0, 0, 1};
+    if (by_k && by_p) {
         clear();
         for (int c = tid; c < row.chunks; c += kSaThreads) {
             float x[E];
@@ -775,66 +794,56 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
             for (int e = 0; e < E; ++e)
                 if (x[e] > -INFINITY) atomicAdd(&s.hist[bin_of(below(x[e]))], 1u);
         }
-        const Found f = find(0);
-        if (!f.none) {
-            const u64 last = f.count <= kSaList ? sort_bin(f) : refine_bin(f);
-            from = last - 1;               // at the last kept token's value, one index further
-            from_value = value_of(last);
-            from_index = place_of(last) + 1;
-        }
+        f = find(0);
     }
 
     // ---------------------------------------------------------------- the race over the row
     // First by an estimate of the score (fast logarithm, product with 1 / T), each thread its best
     // two; then exactly, where a thread's best is within the estimate's error of the block's.
+    u64 from = ((u64)kSaNone << 32) | 0xFFFFFFFFu;     // only tokens of higher ranks may be kept
     const float floor_e = -floor_d * temp;
     const float floor_lo = least > 0.f ? floor_e * 0.99999f : INFINITY, floor_hi = least > 0.f ? floor_e * 1.00001f : INFINITY;
-    const bool aligned = (reinterpret_cast<uintptr_t>(noise + row.first(0)) & 15u) == 0;
     const float step = fminf(scaled.inv, 1e30f);
-    // the kept tokens of a chunk and their noise
-    auto fetch = [&](int c, float (&v)[E], float (&z)[E]) {
-        if (c >= row.chunks) return 0u;
-        row.load(c, v);
-        const int i0 = row.first(c);
-        unsigned kept = 0, edge = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {              // false for NaN and -inf
-            const bool in = v[e] > from_value || (v[e] == from_value && (uint32_t)(i0 + e) < from_index);
-            const float d = below(v[e]);
-            kept |= in && !(d > floor_hi) ? 1u << e : 0u;
-            edge |= d > floor_lo ? 1u << e : 0u;
-        }
-        if (kept & edge) {                         // as near to min-p's distance as rounding reaches
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if ((edge >> e) & 1 && !(scaled(below(v[e])) >= floor_d)) kept &= ~(1u << e);
-        }
-        if (aligned && kept == (1u << E) - 1) {
-#pragma unroll
-            for (int e = 0; e < E; e += 4) {
-                const float4 u = __ldg(reinterpret_cast<const float4*>(noise + i0 + e));
-                z[e] = u.x;
-                z[e + 1] = u.y;
-                z[e + 2] = u.z;
-                z[e + 3] = u.w;
-            }
-        } else if (kept) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) z[e] = (kept >> e) & 1 ? __ldg(noise + i0 + e) : 1.f;
-        }
-        return kept;
-    };
     auto estimate = [&](float v, float z) {
         const float sc = fmaf(-0.6931472f, __log2f(z), -below(v) * step);
         return sc == sc ? sc : -INFINITY;
     };
+    // the tokens of a chunk that may be kept, as bits; false for NaN and -inf
+    auto kept_of = [&](int c, const Above& set, float (&v)[E]) {
+        row.load(c, v);
+        const int i0 = row.first(c);
+        const float low = set.least(i0, E);
+        unsigned kept = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) kept |= v[e] >= low ? 1u << e : 0u;
+        if (set.inside(i0, E)) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) kept |= v[e] == set.at && i0 + e < set.index ? 1u << e : 0u;
+        }
+        if (kept && least > 0.f) {
+            unsigned edge = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float d = below(v[e]);
+                kept &= d > floor_hi ? ~(1u << e) : ~0u;
+                edge |= d > floor_lo ? 1u << e : 0u;
+            }
+            if (kept & edge) {                         // as near to min-p's distance as rounding reaches
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if ((edge >> e) & 1 && !(scaled(below(v[e])) >= floor_d)) kept &= ~(1u << e);
+            }
+        }
+        return kept;
+    };
     auto race = [&]() {
+        const Above set(from);
         float first = -INFINITY, second = -INFINITY;
         int first_i = -1;
-        float v[E], z[E];
-        // all tokens: four loads of noise in flight, nothing to choose
-        const bool all = from_value == -INFINITY && !(least > 0.f) && aligned && row.smem && !inf_row;
+        const bool all = set.at == -INFINITY && !(least > 0.f) && row.smem && !inf_row &&
+                         (reinterpret_cast<uintptr_t>(noise + row.first(0)) & 15u) == 0;
         if (all) {
+            // every token: four loads of noise in flight, nothing to choose
             const int groups = (row.lead + row.end - row.begin + 3) / 4;
             for (int g = tid; g < groups; g += 4 * kSaThreads) {
                 float4 u[4];
@@ -867,28 +876,57 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
                     }
                 }
             }
-        }
-        unsigned kept = all ? 0u : fetch(tid, v, z);
-        for (int c = tid; c < row.chunks && !all; c += kSaThreads) {
-            float vn[E], zn[E];
-            const unsigned kept_next = fetch(c + kSaThreads, vn, zn);
-            const int i0 = row.first(c);
+        } else {
+            // the kept tokens are listed, so that all threads share them, and scored when the list is full
+            __syncthreads();
+            if (tid == 0) s.listed = 0;
+            __syncthreads();
+            const int lane = tid & 31;
+            for (int c0 = 0; c0 < row.chunks; c0 += kSaThreads) {
+                float v[E];
+                const unsigned kept = c0 + tid < row.chunks ? kept_of(c0 + tid, set, v) : 0u;
+                int at = 0;
+                if (__any_sync(0xFFFFFFFFu, kept)) {
+                    int upto = __popc(kept);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float sc = estimate(v[e], z[e]);
-                const bool in = (kept >> e) & 1, over = in && (sc > first || first_i < 0);
-                second = over ? first : (in ? fmaxf(second, sc) : second);
-                first = over ? sc : first;
-                first_i = over ? i0 + e : first_i;
-            }
-            kept = kept_next;
+                    for (int d = 1; d < 32; d *= 2) {
+                        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+                        if (lane >= d) upto += o;
+                    }
+                    if (lane == 31) at = atomicAdd(&s.listed, upto);
+                    at = __shfl_sync(0xFFFFFFFFu, at, 31) + upto - __popc(kept);
+                    for (unsigned k2 = kept; k2; k2 &= k2 - 1) s.kept_tokens[at++] = row.first(c0 + tid) + __ffs(k2) - 1;
+                }
+                // the last of the warp's places is its last lane's
+                const bool last = c0 + kSaThreads >= row.chunks;
+                if (!__syncthreads_or(at > kSaTokens - kSaThreads * E) && !last) continue;
+                const int n = s.listed;
+                for (int i = tid; i < n; i += 4 * kSaThreads) {
+                    int t[4];
+                    float z[4];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                v[e] = vn[e];
-                z[e] = zn[e];
+                    for (int j = 0; j < 4; ++j)
+                        if (i + j * kSaThreads < n) {
+                            t[j] = s.kept_tokens[i + j * kSaThreads];
+                            z[j] = __ldg(noise + t[j]);
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (i + j * kSaThreads < n) {
+                            const float sc = estimate(row.value(t[j]), z[j]);
+                            const bool over = sc > first || first_i < 0;
+                            second = over ? first : fmaxf(second, sc);
+                            first = over ? sc : first;
+                            first_i = over ? t[j] : first_i;
+                        }
+                }
+                if (last) break;
+                __syncthreads();
+                if (tid == 0) s.listed = 0;
+                __syncthreads();
             }
         }
-        // the estimate is off by less than `off` (unusual temperatures: not relied on)
+        // the estimate is off by less than this (unusual temperatures: not relied on)
         const float lead = key_value((uint32_t)block_max(first_i < 0 && !all ? 0 : order_key(first), s));
         auto may_win = [&](float sc) {
             if (!scaled.usual || lead == -INFINITY) return true;
@@ -900,79 +938,134 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleArgs 
             if (sc != sc) sc = -INFINITY;
             best = max(best, ranked(order_key(sc), i));
         };
-        if (lead == -INFINITY || (first_i >= 0 && may_win(first))) {
-            if (lead == -INFINITY || may_win(second)) {        // more than one of the thread's tokens
-                for (int c = tid; c < row.chunks; c += kSaThreads) {
-                    kept = fetch(c, v, z);
+        const bool any = lead == -INFINITY || (first_i >= 0 && may_win(first));
+        if (__syncthreads_or(any && (lead == -INFINITY || may_win(second)))) {
+            for (int c = tid; c < row.chunks; c += kSaThreads) {   // two of one thread's tokens, or nothing to go by
+                float v[E];
+                const unsigned kept = kept_of(c, set, v);
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if ((kept >> e) & 1 && may_win(estimate(v[e], z[e]))) exact(v[e], z[e], row.first(c) + e);
-                }
-            } else {
-                exact(row.value(first_i), noise[first_i], first_i);
+                for (int e = 0; e < E; ++e)
+                    if ((kept >> e) & 1) {
+                        const float z = __ldg(noise + row.first(c) + e);
+                        if (may_win(estimate(v[e], z))) exact(v[e], z, row.first(c) + e);
+                    }
             }
+        } else if (any) {
+            exact(row.value(first_i), __ldg(noise + first_i), first_i);
         }
         return index_of(cluster_max(best));
     };
 
     // ---------------------------------------------------------------- the winner, if it is kept
-    // Ranks from s.kept up are kept, ranks up to `from` are not. What lies before a token is counted or, for
-    // top-p, weighed; the share is one of the weight of the first round's set.
+    // Sums over the cluster of two sets' tokens: their number or, for top-p, their weight.
+    auto weigh = [&](float l) { return by_p ? weight(below(l)) : 1u; };
+    auto sums = [&](const Above& a0, const Above& a1, bool bins, bool whole, u64& s0, u64& s1) {
+        u64 x = 0, y = 0;
+        const float edge = key_value(order_key(-(float)f.bin) + 1);        // the least number above -f.bin
+        for (int c = tid; c < row.chunks; c += kSaThreads) {
+            float v[E];
+            row.load(c, v);
+            const int i0 = row.first(c);
+            const float l0 = bins ? edge : a0.least(i0, E), l1 = a1.least(i0, E);
+            if (!whole) {                              // few chunks have tokens of either
+                float most = v[0];
+#pragma unroll
+                for (int e = 1; e < E; ++e) most = fmaxf(most, v[e]);
+                if (!(most >= fminf(l0, l1))) continue;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const unsigned w = weigh(v[e]);
+                x += (bins ? -(below(v[e]) * scale) : v[e]) >= l0 ? w : 0u;
+                y += v[e] >= l1 ? w : 0u;
+            }
+        }
+        // equal values below the index in the chunk that the index falls in
+        auto rest = [&](const Above& a) {
+            const int c = (a.index - row.first(0)) / E, i0 = row.first(c);
+            u64 n = 0;
+            if (a.index > row.first(0) && c < row.chunks && c % kSaThreads == tid)
+                for (int i = i0; i < a.index; ++i) n += i >= row.begin && row.value(i) == a.at ? 1 : 0;
+            return n * weigh(a.at);
+        };
+        if (!bins) x += rest(a0);
+        y += rest(a1);
+        block_scan(x, y, s0, s1, s);
+        if (C > 1) {
+            exchange(s0, s1);
+            s0 = s1 = 0;
+            for (int i = 0; i < C; ++i) {
+                s0 += s.part[turn][i];
+                s1 += s.part_w[turn][i];
+            }
+        }
+    };
+    // Ranks from s.kept up are kept, ranks up to `from` are not. With both cuts top-k's is known at
+    // first by its bin only (`loose`), which bounds the weight of its tokens from both sides; a token
+    // between the bounds, one in thousands, makes all blocks look for the cut itself.
+    bool loose = !f.none;
     if (tid == 0) {
         s.kept = ((u64)top << 32) | 0xFFFFFFFFu;
-        s.target = by_p ? 0 : (u64)k;
+        s.target = s.target_hi = by_p ? 0 : (u64)k;
     }
     int winner;
     for (int round = 0;; ++round) {
         winner = race();
         if (!by_k && !by_p) break;
-        const float won = as_float(row.base[winner]);
-        const u64 won_at = ranked(order_key(won), winner);
-        const u64 hi = s.kept;
-        u64 target = s.target;
-        if (won_at >= hi) break;
-        u64 mid = won_at + (hi - won_at) / 2;
+        const u64 won = ranked(order_key(as_float(row.base[winner])), winner), hi = s.kept;
+        u64 target = s.target, target_hi = s.target_hi;
+        if (won >= hi) break;
+        u64 mid = won + (hi - won) / 2, before_mid, before;
         if ((mid >> 32) == 0x7FFFFFFFu) mid = 0x7FFFFFFEFFFFFFFFull;       // as a value that key equals 0
-        const float than = round == 0 ? from_value : value_of(mid);
-        const uint32_t than_index = round == 0 ? from_index : place_of(mid);
-        u64 x = 0, y = 0, before_mid, before;      // the first round: the whole set in place of before_mid
-        for (int c = tid; c < row.chunks; c += kSaThreads) {
-            float v[E];
-            row.load(c, v);
-            const uint32_t i0 = (uint32_t)row.first(c);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const unsigned w = by_p ? weight(below(v[e])) : 1u;
-                x += v[e] > than || (v[e] == than && i0 + e < than_index) ? w : 0u;
-                y += v[e] > won || (v[e] == won && i0 + e < (uint32_t)winner) ? w : 0u;
+        // the first round has no use for mid: top-p's set, or the part of it in the bins before top-k's
+        sums(Above(round == 0 ? from : mid), Above(won), round == 0 && loose, round == 0, before_mid, before);
+        if (round == 0 && by_p) {
+            u64 most = 0, fewest = 0;
+            if (loose) {
+                const u64 w0 = f.bin > 0 ? weight(f.bin / scale * 0.999999f) : (u64)kSaOne;
+                const u64 w1 = weight((f.bin + 1) / scale * 1.000001f);
+                most = (u64)(k - f.before) * (w0 + (w0 >> 13) + 1);
+                fewest = f.bin < kSaBins - 1 && w1 > 0 ? (u64)(k - f.before) * (w1 - (w1 >> 13) - 1) : 0;
             }
+            target = share_of(p, before_mid + fewest);
+            target_hi = share_of(p, before_mid + most);
         }
-        block_scan(x, y, before_mid, before, s);
-        if (C > 1) {
-            exchange(before_mid, before);
-            before_mid = before = 0;
-            for (int i = 0; i < C; ++i) {
-                before_mid += s.part[turn][i];
-                before += s.part_w[turn][i];
-            }
+        // 1: kept, 0: not kept, -1: not known
+        auto judge = [&](u64 rank, u64 sum) {
+            if (!loose) return sum < target ? 1 : 0;
+            const float at = place(below(key_value((uint32_t)(rank >> 32))));
+            if (sum >= target_hi || at >= (float)(f.bin + 1)) return 0;
+            return sum < target && at < (float)f.bin ? 1 : -1;
+        };
+        const int is_kept = judge(won, before), mid_kept = round > 0 ? judge(mid, before_mid) : 0;
+        if (is_kept == 1) break;
+        from = won;
+        // past the far edge of top-k's bin nothing is kept
+        if (loose && f.bin < kSaBins - 1)
+            from = max(from, (u64)order_key(m - (f.bin + 1) / scale * 1.00001f - 1e-6f * fabsf(m)) << 32);
+        if (is_kept < 0 || mid_kept < 0) {
+            const u64 last = f.count <= kSaList ? sort_bin(f) : refine_bin(f);
+            u64 mass, unused;
+            sums(Above(last - 1), Above(last - 1), false, true, mass, unused);
+            target = target_hi = share_of(p, mass);
+            loose = false;
+            if (won >= last && before < target) break;
+            from = max(from, last - 1);
+        } else if (round > 0 && mid_kept == 0) {
+            from = max(from, mid);
         }
-        if (round == 0 && by_p) target = share_of(p, before_mid);
-        if (before < target) break;
-        from = won_at;
-        if (round > 0 && before_mid >= target) from = max(from, mid);
-        if (tid == 0) {                            // read again after the race's barriers
-            if (round > 0 && before_mid < target) s.kept = mid;
+        if (tid == 0) {                                // read again after the race's barriers
+            if (round > 0 && mid_kept == 1) s.kept = mid;
             s.target = target;
+            s.target_hi = target_hi;
         }
-        from_value = value_of(from);
-        from_index = place_of(from);
     }
     if (rank == 0 && tid == 0) a.tokens[r] = winner;
 }
 
-template <typename T>
-nq_status sample_launch(SampleArgs a, int B, const StepDevice& d, cudaStream_t stream) {
-    auto kern = sample_kernel<T>;
+template <typename T, int PerSm>
+nq_status sample_launch(const SampleArgs& a, int B, int C, size_t bytes, const StepDevice& d, cudaStream_t stream) {
+    auto kern = sample_kernel<T, PerSm>;
     static thread_local int set_for_device = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -981,19 +1074,26 @@ nq_status sample_launch(SampleArgs a, int B, const StepDevice& d, cudaStream_t s
             return NQ_ERR_CUDA;
         set_for_device = dev;
     }
+    return step_launch(kern, dim3((unsigned)(B * C)), dim3(kSaThreads), a.resident ? bytes : 0, stream, d.pdl, C, a) ==
+                   cudaSuccess
+               ? NQ_OK
+               : NQ_ERR_CUDA;
+}
+
+template <typename T>
+nq_status sample_rows(SampleArgs a, int B, const StepDevice& d, cudaStream_t stream) {
     // Eight blocks a row while every block of the call can be resident at once (two an SM); past
     // that fewer and larger slices, up to 40000 tokens (fp32: what fits shared memory), which saves
-    // cluster barriers. Measured, mixed settings: 64 rows of 152064 bf16 74 us at 8 and 4, 94 at 2;
-    // 256 rows of 128257 fp32 199 at 8, 163 at 4, 168 at 2; top-k 50 on 256 rows of 32001 61 at 8, 16 at 1.
+    // cluster barriers. Measured, mixed settings: 64 rows of 152064 bf16 51 us at 8, 47 at 4; 256
+    // rows of 128257 fp32 157 at 8, 124 at 4, 267 at 2; top-k 50 on 256 rows of 32001 25 at 2, 16 at 1.
     int C = kSaMaxCluster;
     while (C > 1 && (long long)B * C > 2 * d.sms && a.V / (C / 2) <= 40000) C /= 2;
     a.slice = ((a.V + C - 1) / C + 15) / 16 * 16;
     const size_t bytes = ((size_t)a.slice * sizeof(T) + 15) / 16 * 16 + 16;
     a.resident = bytes <= (size_t)kSaSliceBytes;
-    return step_launch(kern, dim3((unsigned)(B * C)), dim3(kSaThreads), a.resident ? bytes : 0, stream, d.pdl, C, a) ==
-                   cudaSuccess
-               ? NQ_OK
-               : NQ_ERR_CUDA;
+    // Slices of which only one fits an SM leave a thread 128 registers (256 rows of 128257 fp32 137 -> 124 us).
+    if (a.resident && bytes > (size_t)kSaTwoBytes) return sample_launch<T, 1>(a, B, C, bytes, d, stream);
+    return sample_launch<T, 2>(a, B, C, bytes, d, stream);
 }
 
 bool meet(const void* a, long long na, const void* b, long long nb) {
@@ -1029,7 +1129,7 @@ extern "C" nq_status nq_sample(const void* logits, int dtype, long long stride, 
     if (st != NQ_OK) return st;
     SampleArgs a = {logits, stride, noise, noise_stride, temperature, top_k, top_p, min_p, tokens, V, 0, 0};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == NQ_BF16) return sample_launch<__nv_bfloat16>(a, B, d, s);
-    if (dtype == NQ_FP16) return sample_launch<__half>(a, B, d, s);
-    return sample_launch<float>(a, B, d, s);
+    if (dtype == NQ_BF16) return sample_rows<__nv_bfloat16>(a, B, d, s);
+    if (dtype == NQ_FP16) return sample_rows<__half>(a, B, d, s);
+    return sample_rows<float>(a, B, d, s);
 }
