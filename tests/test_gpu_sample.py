@@ -102,6 +102,16 @@ def test_cuts_few_and_many(nq, dtype, t, k, p, m):
     check(nq, x, e, settings(6, t, k, p, m))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_shorter_than_their_blocks(nq, dtype):
+    """Every length up to a few chunks, at every alignment: blocks without tokens take no part."""
+    for V in range(1, 140, 3):
+        wide, e = rows(8, V + 8, dtype, V, hot=0)
+        for off in (0, 3):
+            x = wide[:, off:off + V]
+            check(nq, x, e[:, off:off + V], settings(8, [1.0, 0.3, 2.0, 100.0] * 2, [0, V, 0, V - 1] * 2, [1.0] * 4 + [0.9] * 4, 0.0))
+
+
 def test_equal_logits_are_cut_by_index(nq):
     """All logits equal: top-k and top-p cut inside one tie, whose weights are exactly 1."""
     V = 20000

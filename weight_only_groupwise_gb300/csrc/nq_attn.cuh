@@ -887,8 +887,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                     tmem_wait_ld();
                     if (masked) {
                         uint64_t see = low_bits(p - kk + 1);
-                        if (a.window > 0)
-                        see &= ~low_bits(p - a.window + 1 - kk) | low_bits(a.sinks - kk);
+                        if (a.window > 0) see &= ~low_bits(p - a.window + 1 - kk) | low_bits(a.sinks - kk);
                         const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {

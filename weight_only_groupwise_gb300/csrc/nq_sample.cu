@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleA
                          (reinterpret_cast<uintptr_t>(noise + row.first(0)) & 15u) == 0;
         if (all) {
             // every token: four loads of noise in flight, nothing to choose
-            const int groups = (row.lead + row.end - row.begin + 3) / 4;
+            const int groups = row.chunks > 0 ? (row.lead + row.end - row.begin + 3) / 4 : 0;
             for (int g = tid; g < groups; g += 4 * kSaThreads) {
                 float4 u[4];
 #pragma unroll
