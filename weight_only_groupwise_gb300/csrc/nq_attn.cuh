@@ -949,9 +949,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                 }
                 if (key0 + kAttnKeys > t.hi || min(t.lo, key0 + kAttnKeys) > max(key0, a.sinks)) {
                     // the V slots of tile j: after K of the first tile, each tile's V follows the next tile's K
-                    // (with five slots the tile before is waited for first: a slot's barrier may be one
-                    // fill behind otherwise)
-                    if (j > 0)
+                    // (S of the tile is there, so the slots up to its K have been filled; where a slot's fill before
+                    // this one comes later, the tile before is waited for, or the barrier may be one fill behind)
+                    if (kKS + 2 * kVS > kSlots && j > 0)
                         ok = mbar_wait(pvdone0 + 8 * (buf ^ 1), ((g - 1) >> 1) & 1, flags, a.dev_err, wait_ns) && ok;
                     const int v0 = seq + kKS + j * (kKS + kVS) + (j + 1 < n ? kKS : 0);
                     for (int s = 0; s < kVS; ++s)
