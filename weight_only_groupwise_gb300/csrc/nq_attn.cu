@@ -163,7 +163,9 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     for (int g = 2; g <= a.heads && g <= units; ++g)
         if (a.heads % g == 0 && units / g * g >= units - units / 16) a.gang = g;
     a.stride = pair ? 2 * a.gang : a.gang;
-    const int blocks = units / a.gang * a.stride;
+    a.gangs = units / a.gang;
+    a.turns = a.heads / a.gang;
+    const int blocks = a.gangs * a.stride;
     a.few_tokens = 1;
     while (a.few_tokens * a.group % 8 != 0) a.few_tokens *= 2;
     if (a.few_tokens > a.block_tokens) a.few_tokens = a.block_tokens;

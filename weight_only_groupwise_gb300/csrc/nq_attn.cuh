@@ -113,6 +113,7 @@ struct AttnArgs {
     const int* kv_lens;
     int R, tokens, heads, group;       // heads: KV heads; group: query heads per KV head
     int gang;                          // blocks (pairs) that take the heads of a range together
+    int gangs, turns;                  // gangs of the launch; times that a gang goes through the heads
     int tile_tokens;                   // tokens of a query tile: a block's, or two blocks' of a pair
     int block_tokens;                  // tokens of a block: 128 / group
     int stride;                        // blocks from a split's part to the next: gang, times two for pairs
@@ -158,7 +159,7 @@ struct AttnTile {
 };
 
 __device__ __forceinline__ int attn_tiles(const AttnArgs& a, const AttnReq& q) {
-    return (q.n + a.tile_tokens - 1) / a.tile_tokens;
+    return q.n <= a.tile_tokens ? min(q.n, 1) : (q.n + a.tile_tokens - 1) / a.tile_tokens;
 }
 
 __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, const AttnReq& q, int qt) {
@@ -220,8 +221,8 @@ struct AttnWalk {
         r = r_;
         rq = rq_;
         nqt = attn_tiles(a, rq);
-        const long long per = attn_div(all, a.heads / a.gang);
-        const int turn = (int)attn_div(u - base, per);
+        const long long per = a.turns == 1 ? all : attn_div(all, a.turns);
+        const int turn = a.turns == 1 ? 0 : (int)attn_div(u - base, per);
         h = turn * a.gang + me % a.gang;
         long long rem = (u - base) - turn * per;
         const int lane = threadIdx.x & 31;
@@ -288,28 +289,32 @@ struct AttnWalk {
     }
 };
 
-// Units of a request per KV head: all query tiles' key tiles, the warp's lanes sharing long ones.
-__device__ __forceinline__ long long attn_units(const AttnArgs& a, const AttnReq& q, bool live) {
+// Units of a request per KV head: all query tiles' key tiles. Of long requests (the bits of `big`) the
+// warp's lanes share the tiles, and the warps of a block take every `warps`-th, into `sums`.
+__device__ __forceinline__ long long attn_units(const AttnArgs& a, const AttnReq& q, bool live, unsigned& big) {
     const int nqt = live ? attn_tiles(a, q) : 0;
     long long w = 0;
     if (nqt <= 2)
         for (int i = 0; i < nqt; ++i) w += max(1, attn_tile(a, q, i).n);
-    unsigned big = __ballot_sync(0xFFFFFFFFu, nqt > 2);
-    while (big) {
+    big = __ballot_sync(0xFFFFFFFFu, nqt > 2);
+    return w;
+}
+__device__ __forceinline__ void attn_units_long(const AttnArgs& a, const AttnReq& q, unsigned big, int warp, int warps,
+                                                long long* sums) {
+    for (int i = 0; big; ++i, big &= big - 1) {
+        if (i % warps != warp) continue;
         const int src = __ffs(big) - 1;
-        big &= big - 1;
         AttnReq s;
         s.q0 = 0;
         s.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
         s.kv = __shfl_sync(0xFFFFFFFFu, q.kv, src);
         const int m = attn_tiles(a, s);
         long long v = 0;
-        for (int i = threadIdx.x & 31; i < m; i += 32) v += max(1, attn_tile(a, s, i).n);
+        for (int k = threadIdx.x & 31; k < m; k += 32) v += max(1, attn_tile(a, s, k).n);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-        if ((int)(threadIdx.x & 31) == src) w = v;
+        if ((threadIdx.x & 31) == 0) sums[src] = v;
     }
-    return w;
 }
 
 // ---------------------------------------------------------------- instructions
@@ -540,26 +545,59 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     long long total = 0, blocks = 1;   // blocks: ranges with work
     int snap = 0;
     // locate(u): finds unit u in w, and returns its place in its tile
+    struct Plan {
+        AttnWalk walk;
+        int from[2], to[2];
+    };
+    Plan* const plan = reinterpret_cast<Plan*>(ctrl + 2048 + 640);
+    static_assert(2048 + 640 + sizeof(Plan) <= kAttnCtrlBytes, "room for the plan");
     auto range = [&](auto locate) {
-        const long long gangs = gridDim.x / kBlocks / a.gang, me = w.me / a.gang;
+        const long long me = w.me / a.gang;
         // no range is empty but between whole tiles: the join takes every block from a tile's first to
         // its last as a part
-        blocks = max(1ll, min(gangs, total));
-        snap = attn_div(total, blocks) > 2 * kAttnSnap ? kAttnSnap : 0;
-        long long u0 = min(attn_div(total * me, blocks), total), u1 = min(attn_div(total * (me + 1), blocks), total);
-        if (u0 >= u1) return;
-        if (u1 < total) {
-            const int from = locate(u1);
-            u1 += w.snapped(from, snap) - from;
+        blocks = max(1ll, min((long long)a.gangs, total));
+        snap = total > 2 * kAttnSnap * blocks ? kAttnSnap : 0;
+        const long long e0 = total * me, e1 = e0 + total;
+        long long u0, u1;
+        if (e1 >> 32 == 0) {           // both quotients at once
+            u0 = (uint32_t)e0 / (uint32_t)blocks;
+            u1 = (uint32_t)e1 / (uint32_t)blocks;
+        } else {
+            u0 = e0 / blocks;
+            u1 = e1 / blocks;
         }
-        const int from = locate(u0), to = w.snapped(from, snap);
-        u0 += to - from;
-        w.begin(a, u0, to, u1 - u0);
+        u0 = min(u0, total);
+        u1 = min(u1, total);
+        if (u0 >= u1) return;
+        // half of the warps look for the begin, half for the end (each search is a chain of some 0.9 us)
+        const bool last = warp >= kAttnThreads / 64;
+        int from = 0, to = 0;
+        if (!last || u1 < total) {
+            from = locate(last ? u1 : u0);
+            to = w.snapped(from, snap);
+        }
+        if (lane == 0 && (warp == 0 || warp == kAttnThreads / 64)) {
+            if (!last) plan->walk = w;
+            plan->from[last] = from;
+            plan->to[last] = to;
+        }
+        __syncthreads();
+        w = plan->walk;
+        u0 += plan->to[0] - plan->from[0];
+        u1 += plan->to[1] - plan->from[1];
+        w.begin(a, u0, plan->to[0], u1 - u0);
     };
     if (a.R <= 32) {
         AttnReq rq = {0, 0, 0};
         if (lane < a.R) rq = attn_req(a, lane);
-        const long long mine = attn_units(a, rq, lane < a.R) * (a.heads / a.gang);
+        unsigned big;                  // the same in every warp
+        long long mine = attn_units(a, rq, lane < a.R, big);
+        if (big) {
+            attn_units_long(a, rq, big, warp, kAttnThreads / 32, warp_sums);
+            __syncthreads();
+            if ((big >> lane) & 1) mine = warp_sums[lane];
+        }
+        mine *= a.turns;
         long long upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -581,7 +619,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             const int r = r0 + tid;
             AttnReq rq = {0, 0, 0};
             if (r < a.R) rq = attn_req(a, r);
-            long long x = attn_units(a, rq, r < a.R) * (a.heads / a.gang);
+            unsigned big;
+            long long x = attn_units(a, rq, r < a.R, big);
+            if (big) {
+                attn_units_long(a, rq, big, 0, 1, upto + r0 + 32 * warp);
+                __syncwarp();
+                if ((big >> lane) & 1) x = upto[r];
+            }
+            x *= a.turns;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
                 const long long u = __shfl_up_sync(0xFFFFFFFFu, x, d);
@@ -838,7 +883,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const int row_token = row / a.group, row_head = row - row_token * a.group;
         int g = 0, seq = 0;
         int4 split0 = make_int4(-1, 0, 0, 0);
-        const int end = min(max(__ldg(a.q_start + a.R), 0), a.tokens);   // output rows from here on are zeros
         int split_count = 0;
         for (; w.more(); w.next(a)) {
             const AttnTile& t = w.t;
@@ -1026,7 +1070,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             __syncwarp();
             arrive_leader(ofree);
         }
-        for (int i = end + blockIdx.x; i < a.tokens; i += gridDim.x)
+        // output rows past the requests' are zeros
+        const int last_start = __ldg(a.q_start + a.R);
+        for (int i = min(max(last_start, 0), a.tokens) + blockIdx.x; i < a.tokens; i += gridDim.x)
             for (int e = tid; e < a.heads * a.group * (D / 8); e += kAttnSoftmaxWarps * 32)
                 reinterpret_cast<uint4*>(a.out + i * a.out_stride)[e] = make_uint4(0, 0, 0, 0);
         if (tid == 0) {
