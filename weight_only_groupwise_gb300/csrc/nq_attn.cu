@@ -83,9 +83,9 @@ int pair_capacity(int sms) {
 // Whether a call of 256 columns runs on pairs of blocks: where its requests bring on average rows
 // for two pairs' query tiles or more, all its heads enough to fill the SMs, and no window makes the tiles
 // short (the lengths are on the device; any split of the tokens is right either way). Measured,
-// pairs against single blocks, 24 query and 4 KV heads: 2048 tokens over 16384 keys 534 us
-// against 566 (page 16: 535, 670), 8 x 128 over up to 8000 173 against 204, 4 x 1000 without a cache 129, 132; but
-// 512 over 4096 73, 72, 86 over 16000 69, 63, and 700 in a window of 1024 58, 52.
+// pairs against single blocks, 24 query and 4 KV heads: 2048 tokens over 16384 keys 531 us
+// against 572 (page 16: 535, 717), 8 x 128 over up to 8000 165 against 200, 4 x 1000 without a cache 114, 119; but
+// 512 over 4096 68, 69, 86 over 16000 62, 59, and 700 in a window of 1024 56, 50.
 bool attn_uses_pairs(int tokens, int R, int group, int q_heads, int window) {
     return (long long)tokens * group >= 512ll * R && (long long)tokens * q_heads >= 16384 && (window == 0 || window >= 4096);
 }
