@@ -31,12 +31,13 @@ cudaError_t attn_launch(const AttnArgs& a, int blocks, bool splits, cudaStream_t
     cudaError_t e = step_launch(kern, dim3(blocks), dim3(kAttnThreads), AttnGeo<D, PAIR>::kSmem, stream, pdl && !PAIR,
                                 PAIR ? 2 : 1, a);
     if (e != cudaSuccess || !splits) return e;
-    // a block takes 32 items of a split with many parts; launched without dependent launch: waiting
-    // blocks slowed the kernel before them (one token over 4099 keys: 21.4 us with, 15.5 without)
+    // a block takes 32 items of a split with many parts. Its launch follows the exit of the attention
+    // kernel's blocks, which do not ask for it themselves: join blocks that wait beside working ones slow them (one
+    // token over 4099 keys: 18.0 us as an ordinary launch, 15.5 so, 19 if asked for at the end of a block)
     const int rows = (a.tokens < a.block_tokens ? a.tokens : a.block_tokens) * a.group;
     const int y = (rows * (D / 8) + 31) / 32;
     return step_launch(attn_join_kernel<D, BF16>, dim3(blocks, y < kJoinBlocksY ? y : kJoinBlocksY), dim3(kJoinThreads), 0,
-                       stream, false, 1, a);
+                       stream, pdl && !PAIR, 1, a);
 }
 
 template <bool BF16>
