@@ -256,6 +256,27 @@ def test_repeatable_and_on_another_stream(nq):
     assert torch.equal(got, want)
 
 
+def test_calls_in_a_row_share_the_workspace(nq):
+    """Calls that split their tiles differently, one after the other without a wait: the same bits as alone."""
+    shapes = [([4100], [1], 24, 4, 256, 64), ([9000, 300], [2, 1], 8, 2, 128, 16), ([700] * 5, [60] * 5, 16, 16, 64, 32),
+              ([100], [900], 12, 2, 256, 64), ([20000], [1], 32, 8, 128, 16), ([5], [3], 8, 8, 128, 32),
+              ([3000] * 40, [1] * 40, 10, 1, 256, 128)]
+    todo = []
+    for i, (old, new, heads, kv_heads, dim, page) in enumerate(shapes):
+        p = problem(old, new, heads, kv_heads, dim, page, BF if i % 2 else FP, seed=i)
+        args = (p["q"], p["k"], p["v"], p["table"], p["q_start"], p["kv"])
+        alone = nq.attn_paged(*args, scale=dim ** -0.5)
+        torch.cuda.synchronize()
+        todo.append((args, dim ** -0.5, alone, torch.empty_like(p["q"])))
+    order = np.random.default_rng(2).integers(0, len(todo), 200)
+    for i in order.tolist():
+        args, scale, _, out = todo[i]
+        nq.attn_paged(*args, scale=scale, out=out)
+    nq.device_error()
+    for args, scale, alone, out in todo:
+        assert torch.equal(alone, out)
+
+
 def test_in_a_graph_with_growing_lengths(nq):
     p = problem([200], [1], 8, 2, 128, 32, BF, seed=8)
     nq.attn_reserve()
