@@ -1,0 +1,35 @@
+"""Edges of the serving-step calls that were once wrong, each against its definition."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_sample import check as check_tokens
+from tests.test_gpu_sample import settings
+
+pytestmark = pytest.mark.gpu
+
+BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def nq():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from weight_only_groupwise_gb300 import build
+    build.build()
+    from weight_only_groupwise_gb300 import nq
+    return nq
+
+
+def test_short_rows_over_whole_clusters(nq):
+    """Rows so short that a block's first store into another comes at once, over as many clusters as fit, call after
+    call: the barrier at the start lets every way through a row end, and the tokens stay the same."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    V, B = 65, 38
+    x = torch.randn((B, V), device="cuda", generator=g)
+    e = torch.empty((B, V), device="cuda").exponential_(generator=g)
+    s = settings(B, [1.0, 0.0, 0.7, 1.3] * 9 + [1.0] * 2, [0, 0, 5, 0, 60] * 7 + [0] * 3, [1.0, 0.9, 0.5] * 12 + [0.3] * 2, [0.0, 0.1] * 19)
+    want = torch.as_tensor(check_tokens(nq, x, e, s))
+    got = [nq.sample(x, e, **s) for _ in range(300)]
+    assert all(torch.equal(t.cpu(), want) for t in got)

@@ -228,6 +228,11 @@ struct Row {
     }
 };
 
+// The cluster's first barrier, in two halves: a block may address another's shared memory only once that
+// one has begun to run, which being placed together does not make sure.
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_begun() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // Block-wide maximum of v, in every thread.
 __device__ __forceinline__ u64 block_max(u64 v, SaShared& s) {
 #pragma unroll
@@ -428,6 +433,7 @@ __global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleA
     const int r = blockIdx.x / C;
     constexpr int E = Row<T>::E;
 
+    if (C > 1) cluster_begun();            // waited for below, where the slice has been loaded
     grid_launch_dependents();
     grid_dependency_wait();
 
@@ -498,6 +504,7 @@ __global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleA
 #pragma unroll
         for (int e = 0; e < E; ++e) high = fmaxf(high, x[e]);   // ignores NaN
     }
+    if (C > 1) cluster_wait_begun();       // from here on blocks store into one another's shared memory
 
     // ---------------------------------------------------------------- a cut that few tokens pass
     u64 row_top = 0;
