@@ -33,3 +33,16 @@ def test_short_rows_over_whole_clusters(nq):
     want = torch.as_tensor(check_tokens(nq, x, e, s))
     got = [nq.sample(x, e, **s) for _ in range(300)]
     assert all(torch.equal(t.cpu(), want) for t in got)
+
+
+@pytest.mark.parametrize("dtype,V", [(F32, 400001), (F32, 1001), (BF, 1001), (FP, 30003)])
+def test_what_lies_before_a_row_is_no_token(nq, dtype, V):
+    """Rows that begin inside a 16-byte chunk, and noise aligned otherwise: the elements before them would win."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    for off in (0, 1, 3, 7):
+        for noise_off in (8, 9):
+            x = torch.full((5, 16 + V + 3), 60.0, device="cuda", dtype=dtype)
+            x[:, off + 8:off + 8 + V] = torch.randn((5, V), device="cuda", generator=g).to(dtype)
+            e = torch.full((5, 16 + V + 3), 1e-6, device="cuda")
+            e[:, noise_off:noise_off + V].exponential_(generator=g)
+            check_tokens(nq, x[:, off + 8:off + 8 + V], e[:, noise_off:noise_off + V], settings(5, 1.0, 0, 1.0, 0.0))

@@ -127,7 +127,8 @@ struct Above {
           index((int)min(0xFFFFFFFFu - (uint32_t)rank, 0x7FFFFFFFu)) {}
     // for a chunk of n tokens from i0: values from here up, and whether the index falls inside
     __device__ __forceinline__ float least(int i0, int n) const { return i0 + n <= index ? at : next; }
-    __device__ __forceinline__ bool inside(int i0, int n) const { return i0 < index && i0 + n > index; }
+    // (no token is below index 0, which a chunk may begin before)
+    __device__ __forceinline__ bool inside(int i0, int n) const { return index > 0 && i0 < index && i0 + n > index; }
 };
 
 struct Share {             // what a block hands to the settling one besides its first tokens
