@@ -990,12 +990,15 @@ __global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleA
                 y += v[e] >= l1 ? w : 0u;
             }
         }
-        // equal values below the index in the chunk that the index falls in
+        // equal values below the index in the chunk that the index falls in, if it is one of this slice's (the next
+        // slice may share it, and an index between two tokens' ranks may be any number)
         auto rest = [&](const Above& a) {
-            const int c = (a.index - row.first(0)) / E, i0 = row.first(c);
             u64 n = 0;
-            if (a.index > row.first(0) && c < row.chunks && c % kSaThreads == tid)
-                for (int i = i0; i < a.index; ++i) n += i >= row.begin && row.value(i) == a.at ? 1 : 0;
+            if (a.index > row.first(0) && a.index < row.first(row.chunks)) {
+                const int c = (a.index - row.first(0)) / E;
+                if (c % kSaThreads == tid)
+                    for (int i = max(row.first(c), row.begin); i < min(a.index, row.end); ++i) n += row.value(i) == a.at ? 1 : 0;
+            }
             return n * weigh(a.at);
         };
         if (!bins) x += rest(a0);
