@@ -509,8 +509,9 @@ nq_status nq_attn_reserve(void);
  *   temperature, top_p, min_p  fp32 [B], top_k int32 [B]; each may be NULL (1, all, all, all)
  *   temperature <= 0 or NaN: the first token; noise is then not read
  *   tokens  int32 [B], written; -1 for a row with no logit above -inf
- * Tokens of -inf logits are never kept. Masses are summed in 2^-30 of the first token's weight, as
- * integers: the result does not depend on the order of summation. 1 <= V <= 524160; B <= 2^20. Logits need
+ * Tokens of -inf logits are never kept. Masses are sums of whole numbers of 2^-44 of the first token's weight,
+ * each token's exp(d) rounded to one: the result depends neither on the order of summation nor on the
+ * other rows of the call, and a cut is off by V x 2^-45 of that weight and 4e-6 of the mass behind it at most. 1 <= V <= 524160; B <= 2^20. Logits need
  * the alignment of their type only. Noise is read at kept tokens only.
  */
 nq_status nq_sample(const void* logits, int dtype, long long stride, const float* noise, long long noise_stride,

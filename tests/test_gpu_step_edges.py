@@ -75,3 +75,57 @@ def test_few_levels_in_rows_too_long_for_shared_memory(nq, V):
         x = torch.randint(0, 4, (6, V + 4), device="cuda", generator=g).float()[:, off:off + V]
         e = torch.empty((6, V), device="cuda").exponential_(generator=g)
         check_tokens(nq, x, e, settings(6, 1.0, [5000, V // 2, V - 3, 0, 0, V // 3], [1.0, 1.0, 1.0, 0.9, 0.3, 0.7], 0.0))
+
+
+def last_kept_wins(x, t=1.0):
+    """Noise for which the best token of any set of first tokens is its last: (noise, order, distances)."""
+    V = x.shape[1]
+    order = torch.argsort(x.double(), dim=1, descending=True, stable=True)
+    place = torch.empty_like(order).scatter_(1, order, torch.arange(V, device="cuda").expand(x.shape[0], V).contiguous())
+    d = (x.double() - x.double().amax(1, keepdim=True)) / t
+    return torch.exp(d - place.double() * (20 / V)).float(), place, d.gather(1, order)
+
+
+@pytest.mark.parametrize("dtype,V", [(F32, 152064), (F32, 524160), (BF, 152064), (FP, 300007), (F32, 9000)])
+def test_shares_cut_beside_and_inside_a_far_tail(nq, dtype, V):
+    """A first token, thirty of 1e-5 and a tail that holds 1e-4 in all: shares cut among the thirty (few tokens settle
+    them) and inside the tail (trials). The cut may be off by the rounding of the weights alone: V 2^-45 of the first
+    token's weight, and what three roundings of exponents up to 31 and the exponential's 2 ulp do to the
+    masses behind it, 4e-6 of them."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = math.log(1e-4 / V) + 0.3 * torch.randn((1, V), device="cuda", generator=g)
+    at = torch.randperm(V, device="cuda", generator=g)[:31]
+    x[0, at[0]] = 0.0
+    x[0, at[1:]] = math.log(1e-5) + 0.2 * torch.rand(30, device="cuda", generator=g)
+    x = x.to(dtype)
+    e, place, d = last_kept_wins(x)
+    w = torch.exp(d[0]).cpu().numpy()
+    before, total = np.cumsum(w) - w, w.sum()
+    cuts = [0.5 * (before[j] + before[j + 1]) for j in (1, 3, 8, 17, 28)] + [before[31] + f * (total - before[31]) for f in (0.05, 0.3, 0.5, 0.9)]
+    p = np.asarray(cuts / total, np.float32)
+    B = len(p)
+    got = nq.sample(x.expand(B, V).contiguous(), e.expand(B, V).contiguous(), **settings(B, 1.0, 0, p, 0.0))
+    for share, token in zip(p.astype(np.float64) * total, got.tolist()):
+        off = V * 2.0 ** -45 + 4e-6 * (total - 1)
+        least, most = ((before < share + s).sum() - 1 for s in (-off, off))
+        assert least <= int(place[0, token]) <= most, (share, least, most, int(place[0, token]))
+
+
+@pytest.mark.parametrize("dtype,hot", [(F32, 12), (F32, 0), (BF, 0), (BF, 12)])
+def test_a_cut_does_not_depend_on_the_batch(nq, dtype, hot):
+    """One row with many neighbouring shares, alone (eight blocks a row) and with 255 others (fewer), the
+    last kept token winning: the same tokens, as few tokens settle the row or trials do."""
+    V, B = 152064, 256
+    g = torch.Generator(device="cuda").manual_seed(hot)
+    x = torch.randn((1, V), device="cuda", generator=g) * 2.2
+    if hot:
+        x[0, torch.randperm(V, device="cuda", generator=g)[:hot]] += 14
+    x = x.to(dtype)
+    e, _, d = last_kept_wins(x)
+    p = [0.9]
+    for _ in range(B - 1):
+        p.append(float(np.nextafter(np.float32(p[-1]), np.float32(1))))
+    s = settings(B, 1.0, 0, p, 0.0)
+    together = nq.sample(x.expand(B, V).contiguous(), e.expand(B, V).contiguous(), **s)
+    alone = torch.cat([nq.sample(x, e, **{n: v[i:i + 1] for n, v in s.items()}) for i in range(B)])
+    assert torch.equal(together, alone)

@@ -30,8 +30,11 @@
 //     cut again by the bits of the logits' ordered integers, at most three times.
 // The race lists the tokens that may be kept in shared memory, so that all threads share them
 // (64 rows with min-p 31 -> 20 us); a race over all tokens needs no list.
-// Weights are summed as 2^-30 fixed point in integers, or by each thread in a fixed order: no sum
-// depends on the order of atomics.
+// A token's weight is one whole number of 2^-44 of the maximum's, whichever way its row takes, and sums of
+// weights are integers: a cut depends neither on an order of summation nor on the blocks of a row. (V 2^-45 of the
+// mass, 1.6e-8 at the largest vocabulary, is the most that the rounding moves. With 2^-30 a tail of half a million tokens
+// could be 2e-4 off.) The mass of a row whose top-p is tried with few tokens is first known as a float sum; a winner
+// that lies within that sum's error of the cut is left to the trials.
 //
 // Bound by the latency of these few steps for few rows, by instructions per token and barriers
 // for many (the logits' bytes alone would take a fraction of it). Measured: one row of 152064 bf16,
@@ -71,7 +74,12 @@ constexpr int kSaSliceBytes = 160 * 1024;      // most shared memory for a slice
 constexpr int kSaTwoBytes = 86 * 1024;          // up to here two blocks fit an SM
 constexpr float kSaRange = 32.f;               // distance to the maximum covered by the bins
 constexpr float kSaLeastT = 0.75f;             // in units of max(T, this)
-constexpr float kSaOne = 1073741824.f;         // 2^30: the weight of the maximum
+constexpr float kSaOne = 1073741824.f;         // 2^30: the unit of the try's float sums
+constexpr int kSaHigh = 23;                    // a weight is a sum of two parts, of 2^-21 and of 2^-(21 + this)
+constexpr u64 kSaWhole = 1ull << (21 + kSaHigh);   // the weight of the maximum
+// Error of the try's mass, relative: 136 fp32 sums a thread (8.1e-6), exponents up to 31 rounded three times (3.9e-6), 512
+// truncations a block (4.8e-7), and the weights' own rounding: below 1.3e-5.
+constexpr float kSaMassError = 3.0517578e-5f;
 constexpr uint32_t kSaNone = 0x007FFFFFu;      // ordered integer of -inf
 
 struct SampleArgs {
@@ -340,16 +348,32 @@ struct Scaler {
     }
 };
 
-// A token's weight in 2^-30 of the maximum's, from e = top - l, for sums over many tokens.
+// A token's weight relative to the maximum's, from e = top - l.
+struct WeightParts {
+    unsigned high;         // of 2^-21, and of 2^-44: up to 2^21, and 2^22 either way
+    int low;
+};
 struct Weigher {
     float c;
-    __device__ __forceinline__ explicit Weigher(float temp) : c(-1.4426950408889634f * fminf(1.f / temp, 1e30f)) {}
+    // (never 0, so that an infinite distance weighs nothing at an infinite temperature)
+    __device__ __forceinline__ explicit Weigher(float temp)
+        : c(-fmaxf(1.4426950408889634f * fminf(1.f / temp, 1e30f), 1e-45f)) {}
     __device__ __forceinline__ float exp(float e) const {
         float y;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(e * c));
         return y;
     }
-    __device__ __forceinline__ unsigned operator()(float e) const { return __float2uint_rn(exp(e) * kSaOne); }
+    // Rounded to 2^-44, without conversions: a sum with 1.5 x 2^n has its value in its low bits. Threads add the
+    // parts in 32 bits (136 tokens at most).
+    __device__ __forceinline__ WeightParts parts(float e) const {
+        const float w = exp(e), a = w + 6.f, b = (w - (a - 6.f)) + 0x1.8p-21f;
+        return {__float_as_uint(a) - __float_as_uint(6.f), (int)(__float_as_uint(b) - __float_as_uint(0x1.8p-21f))};
+    }
+    static __device__ __forceinline__ u64 sum(unsigned high, int low) { return ((u64)high << kSaHigh) + (u64)(long long)low; }
+    __device__ __forceinline__ u64 operator()(float e) const {
+        const WeightParts w = parts(e);
+        return sum(w.high, w.low);
+    }
 };
 
 struct Settings {
@@ -359,10 +383,11 @@ struct Settings {
 };
 
 // The settling block: the row's token from the cluster's first tokens (n of them, gathered in
-// s.list), N a thread. Returns the token, or -1 if top-p alone cannot be settled among them.
+// s.list), N a thread. Returns the token, or -1 if top-p alone cannot be settled among them: because they
+// may not hold the share, or because the winner is kept by one bound of the share (least, most) and not by the other.
 template <int N>
-__device__ __forceinline__ int settle(SaShared& s, int n, float m, uint32_t bound, u64 mass, const Settings& o,
-                                      const Scaler& scaled, const float* noise) {
+__device__ __forceinline__ int settle(SaShared& s, int n, float m, uint32_t bound, u64 least, u64 most, const Settings& o,
+                                      const Scaler& scaled, const Weigher& weight, const float* noise) {
     const int tid = threadIdx.x;
     u64 v[N];
 #pragma unroll
@@ -381,15 +406,15 @@ __device__ __forceinline__ int settle(SaShared& s, int n, float m, uint32_t boun
             const uint32_t key = (uint32_t)(v[j] >> 32);
             z[j] = __ldg(noise + index_of(v[j]));
             if (key != top) d[j] = scaled(m - key_value(key));
-            wt[j] = (u64)rintf(expf(d[j]) * kSaOne);
+            wt[j] = weight(key != top ? m - key_value(key) : 0.f);
         }
         y += wt[j];
     }
     const u64 own = y;
     block_scan(x, y, unused, sum, s);
     y -= own;
-    const u64 target = o.by_p ? share_of(o.p, o.by_k ? sum : mass) : ~0ull;
-    u64 best = 0;
+    const u64 target = !o.by_p ? ~0ull : (o.by_k ? share_of(o.p, sum) : most);
+    u64 best = 0, best_unsure = 0;             // the best of all that may be kept, of those that `least` does not keep
     bool reached = false;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -398,6 +423,7 @@ __device__ __forceinline__ int settle(SaShared& s, int n, float m, uint32_t boun
             if (at == 0 || (y < target && d[j] >= o.floor_d)) {
                 const u64 c = ranked(order_key(d[j] - logf(z[j])), index_of(v[j]));
                 best = c > best ? c : best;
+                if (!o.by_k && at > 0 && y >= least) best_unsure = c;
             }
             y += wt[j];
             // the cut has to lie among tokens that no block has kept back
@@ -405,8 +431,10 @@ __device__ __forceinline__ int settle(SaShared& s, int n, float m, uint32_t boun
         }
     }
     best = block_max(best, s);
-    const bool settled = o.by_k || bound == 0 || __syncthreads_or(reached);
-    return settled ? index_of(best) : -1;
+    if (o.by_k) return index_of(best);
+    const bool unsure = __syncthreads_or(best_unsure == best);
+    const bool settled = bound == 0 || __syncthreads_or(reached);
+    return settled && !unsure ? index_of(best) : -1;
 }
 
 // The at-th (from 0) of the n tokens in s.list, in the row's order.
@@ -583,7 +611,7 @@ __global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleA
             }
         }
         // top-p alone: the listed tokens must be able to hold the share
-        if (!by_k) fail |= listed < p * mass * 0.9999f;
+        if (!by_k) fail |= !(listed >= p * mass * 0.9999f);
         if (!fail) {
             if (rank == 0) {
                 // the blocks' parts, brought together (each is read before it is written over)
@@ -606,9 +634,15 @@ __global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleA
                 int token = -1;
                 bool settled = n == 0;
                 if (n > 0) {
-                    token = n <= kSaThreads       ? settle<1>(s, n, m, bound, (u64)mass, set, scaled, noise)
-                            : n <= 2 * kSaThreads ? settle<2>(s, n, m, bound, (u64)mass, set, scaled, noise)
-                                                  : settle<4>(s, n, m, bound, (u64)mass, set, scaled, noise);
+                    const float unit = (float)kSaWhole / kSaOne;
+                    u64 lo = 0, hi = 0;
+                    if (!by_k) {
+                        lo = share_of(p, (u64)(mass * unit * (1.f - kSaMassError)));
+                        hi = share_of(p, (u64)(mass * unit * (1.f + kSaMassError)));
+                    }
+                    token = n <= kSaThreads       ? settle<1>(s, n, m, bound, lo, hi, set, scaled, weight, noise)
+                            : n <= 2 * kSaThreads ? settle<2>(s, n, m, bound, lo, hi, set, scaled, weight, noise)
+                                                  : settle<4>(s, n, m, bound, lo, hi, set, scaled, weight, noise);
                     settled = token >= 0;
                 }
                 if (settled && tid == 0) a.tokens[r] = token;
@@ -968,9 +1002,10 @@ __global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleA
 
     // ---------------------------------------------------------------- the winner, if it is kept
     // Sums over the cluster of two sets' tokens: their number or, for top-p, their weight.
-    auto weigh = [&](float l) { return by_p ? weight(below(l)) : 1u; };
+    auto weigh = [&](float l) { return by_p ? weight(below(l)) : 1ull; };
     auto sums = [&](const Above& a0, const Above& a1, bool bins, bool whole, u64& s0, u64& s1) {
-        u64 x = 0, y = 0;
+        unsigned x_high = 0, y_high = 0;
+        int x_low = 0, y_low = 0;
         const float edge = key_value(order_key(-(float)f.bin) + 1);        // the least number above -f.bin
         for (int c = tid; c < row.chunks; c += kSaThreads) {
             float v[E];
@@ -985,11 +1020,15 @@ __global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleA
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const unsigned w = weigh(v[e]);
-                x += (bins ? -(below(v[e]) * scale) : v[e]) >= l0 ? w : 0u;
-                y += v[e] >= l1 ? w : 0u;
+                const bool in0 = (bins ? -(below(v[e]) * scale) : v[e]) >= l0, in1 = v[e] >= l1;
+                const WeightParts w = by_p ? weight.parts(below(v[e])) : WeightParts{0u, 1};
+                x_high += in0 ? w.high : 0u;
+                x_low += in0 ? w.low : 0;
+                y_high += in1 ? w.high : 0u;
+                y_low += in1 ? w.low : 0;
             }
         }
+        u64 x = Weigher::sum(x_high, x_low), y = Weigher::sum(y_high, y_low);
         // equal values below the index in the chunk that the index falls in, if it is one of this slice's (the next
         // slice may share it, and an index between two tokens' ranks may be any number)
         auto rest = [&](const Above& a) {
@@ -1035,7 +1074,7 @@ __global__ void __launch_bounds__(kSaThreads, PerSm) sample_kernel(const SampleA
         if (round == 0 && by_p) {
             u64 most = 0, fewest = 0;
             if (loose) {
-                const u64 w0 = f.bin > 0 ? weight(f.bin / scale * 0.999999f) : (u64)kSaOne;
+                const u64 w0 = f.bin > 0 ? weight(f.bin / scale * 0.999999f) : kSaWhole;
                 const u64 w1 = weight((f.bin + 1) / scale * 1.000001f);
                 most = (u64)(k - f.before) * (w0 + (w0 >> 13) + 1);
                 fewest = f.bin < kSaBins - 1 && w1 > 0 ? (u64)(k - f.before) * (w1 - (w1 >> 13) - 1) : 0;
