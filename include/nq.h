@@ -512,7 +512,8 @@ nq_status nq_attn_reserve(void);
  * Tokens of -inf logits are never kept. Masses are sums of whole numbers of 2^-44 of the first token's weight,
  * each token's exp(d) rounded to one: the result depends neither on the order of summation nor on the
  * other rows of the call, and a cut is off by V x 2^-45 of that weight and 4e-6 of the mass behind it at most. 1 <= V <= 524160; B <= 2^20. Logits need
- * the alignment of their type only. Noise is read at kept tokens only.
+ * the alignment of their type only. All of noise may be read, whatever is kept (of a row with temperature <= 0 none
+ * is); its values at tokens that are not kept do not change the result.
  */
 nq_status nq_sample(const void* logits, int dtype, long long stride, const float* noise, long long noise_stride,
                     int B, int V, const float* temperature, const int* top_k, const float* top_p, const float* min_p,

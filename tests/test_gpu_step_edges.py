@@ -129,3 +129,35 @@ def test_a_cut_does_not_depend_on_the_batch(nq, dtype, hot):
     together = nq.sample(x.expand(B, V).contiguous(), e.expand(B, V).contiguous(), **s)
     alone = torch.cat([nq.sample(x, e, **{n: v[i:i + 1] for n, v in s.items()}) for i in range(B)])
     assert torch.equal(together, alone)
+
+
+@pytest.mark.parametrize("bad", [0.0, math.nan, math.inf, -1.0, 1e-38])
+@pytest.mark.parametrize("dtype,V", [(F32, 152064), (BF, 40007), (F32, 400001), (FP, 300)])
+def test_noise_of_tokens_that_are_not_kept_changes_nothing(nq, dtype, V, bad):
+    """On each way through a row: few tokens, trials by count and by mass, both cuts, min-p, none."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    k = [20, 0, V // 5, 0, V // 3, V // 3, 0, 0]
+    p = [0.9, 0.3, 1.0, 0.9, 0.7, 0.8, 1.0, 1.0]
+    m = [0.0, 0.0, 0.0, 0.0, 0.0, 0.01, 0.02, 0.0]
+    B = len(k)
+    x = (torch.randn((B, V), device="cuda", generator=g) * 2.2).to(dtype)
+    x[:, ::11] = -math.inf
+    x[1, 5:25] = 30.0                       # a share that few tokens hold
+    e = torch.empty((B, V), device="cuda").exponential_(generator=g)
+    s = settings(B, 1.0, k, p, m)
+    want = check_tokens(nq, x, e, s)
+    v = x.double()
+    order = torch.argsort(v, dim=1, descending=True, stable=True)
+    rank = torch.empty_like(order).scatter_(1, order, torch.arange(V, device="cuda").expand(B, V).contiguous())
+    d = v - v.amax(1, keepdim=True)
+    w = torch.exp(d).gather(1, order)
+    n = torch.arange(V, device="cuda")
+    for i in range(B):
+        kept = (n < k[i]) if k[i] else n >= 0
+        mass = (w[i] * kept).cumsum(0)
+        # a little more than is kept, so that no cut hangs on a rounding
+        kept &= (mass - w[i] < (p[i] + 1e-6) * mass[-1]) | (p[i] >= 1)
+        hidden = ~kept[rank[i]] | (v[i] == -math.inf) | (d[i] < (math.log(m[i]) - 1e-5 if m[i] else -math.inf))
+        assert hidden.any()
+        e[i, hidden] = bad
+    assert nq.sample(x, e, **s).tolist() == want.tolist()
