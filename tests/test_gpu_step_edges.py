@@ -161,3 +161,43 @@ def test_noise_of_tokens_that_are_not_kept_changes_nothing(nq, dtype, V, bad):
         assert hidden.any()
         e[i, hidden] = bad
     assert nq.sample(x, e, **s).tolist() == want.tolist()
+
+
+def hide(p, page, window, sinks, give_back):
+    """NaN in every row that no new token sees; `give_back`: entries of pages without seen rows become -1."""
+    for r, (old, n) in enumerate(zip(p["old"].tolist(), p["new"].tolist())):
+        if n == 0:
+            continue
+        lo = old - window + 1
+        keys = torch.arange(sinks, max(sinks, lo), device="cuda")
+        block = p["table"][r, keys // page].long()
+        p["k"][block, keys % page] = math.nan
+        p["v"][block, keys % page] = math.nan
+        if give_back:
+            for b in range(-(-sinks // page), max(0, lo) // page):
+                p["table"][r, b] = -1
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("window,sinks", [(4096, 0), (4097, 4), (4100, 130), (5000, 200), (4224, 300)])
+def test_pairs_see_nothing_below_the_window(nq, window, sinks, page):
+    """Prompts of 256 columns that two blocks share: rows between the sinks and the window in pages partly seen."""
+    from tests.test_gpu_attn import check, problem
+    p = problem([6000, 4500, 4090, 0], [500, 300, 77, 130], 24, 4, 256, page, BF, seed=window + page)
+    hide(p, page, window, sinks, False)
+    first = check(nq, p, window, sinks)
+    hide(p, page, window, sinks, True)
+    assert torch.equal(first, check(nq, p, window, sinks))
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (4096, 33)])
+def test_pairs_with_more_requests_than_lanes(nq, window, sinks):
+    from tests.test_gpu_attn import check, problem
+    g = np.random.default_rng(7)
+    p = problem(g.choice([0, 5, 63, 700, 4200], 40), g.integers(60, 130, 40), 24, 4, 256, 32, FP, seed=8)
+    if window:
+        hide(p, 32, window, sinks, True)
+    first = check(nq, p, window, sinks)
+    for _ in range(10):
+        assert torch.equal(first, nq.attn_paged(p["q"], p["k"], p["v"], p["table"], p["q_start"], p["kv"], window=window, sinks=sinks))
+    nq.device_error()

@@ -45,3 +45,18 @@ def test_sampling_blocks_know_that_their_cluster_runs_before_the_first_remote_ac
         assert text[:at].count("{") - text[:at].count("}") == 1
         assert text[:at].rstrip().endswith("if (C > 1)")
     assert "return" not in re.sub(r"\[&\]\([^)]*\) *\{.*?\};", "", text[arrive:wait], flags=re.S)
+
+
+def test_paired_attention_publishes_zeroed_rows_at_cluster_scope():
+    """Rows of V that the second block's softmax warps zero are read by the leading block's products: the arrival that
+    tells the leader so releases at cluster scope, after every lane's stores."""
+    text = body("nq_attn.cuh", "attn_kernel")
+    helper = text[text.index("auto arrive_leader"):]
+    helper = helper[:helper.index("};")]
+    assert re.search(r"if \(lane == 0 && published\) mbar_arrive_remote\(", helper)
+    calls = re.findall(r"\barrive_leader\(pready0 \+ 8 \* buf, (\w+)\)", text)
+    assert calls == ["published"]
+    # set where the zeros have been written, after the fence for the tensor cores' view of them, before the warp meets
+    zeros = text[text.index("auto zero ="):]
+    order = [zeros.index(x) for x in ("fence_proxy_async_smem();", "published = true;", "__syncwarp();", "arrive_leader(pready0")]
+    assert order == sorted(order)

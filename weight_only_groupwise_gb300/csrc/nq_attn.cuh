@@ -381,11 +381,10 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar, bool issue) {
         : "memory");
 }
 
-// Arrival on a barrier of another block of the cluster, and the fence for what it has to publish.
+// Arrival on a barrier of another block of the cluster that publishes nothing outside TMEM.
 __device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 #define NQ_R4(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3])
 #define NQ_O4(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3])
@@ -663,13 +662,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)flags[3];
-    // One arrival of the warp on a barrier of the leading block. The second block's is released at block
-    // scope, which is cheap (at cluster scope it cost a tile 1100 cycles): TMEM is ordered by tcgen05's
-    // own fences, and what else it has written it fences itself.
+    // One arrival of the warp on a barrier of the leading block. The second block's releases at cluster scope
+    // where the warp's lanes have written shared memory that the leader's products read (`published`: the rows of
+    // V that they zeroed before their last __syncwarp). Else block scope will do, and is much cheaper: what is in TMEM
+    // is ordered by tcgen05's own fences, and a copy's writes are released by the copy itself, at cluster scope, on the
+    // barrier that the arrival passes on. (At cluster scope every softmax arrival cost a tile 1100 cycles; those
+    // of the copies alone took 2048 tokens over 16384 from 590 us to 650.)
     const uint32_t to_leader = PAIR ? cluster_map(full0, 0) - full0 : 0;
-    auto arrive_leader = [&](uint32_t bar) {
+    auto arrive_leader = [&](uint32_t bar, bool published) {
         if (PAIR && rank == 1) {
-            if (lane == 0) mbar_arrive_remote_cta(bar + to_leader);
+            if (lane == 0 && published) mbar_arrive_remote(bar + to_leader);
+            if (lane == 0 && !published) mbar_arrive_remote_cta(bar + to_leader);
         } else {
             mbar_arrive_if(bar, lane == 0);
         }
@@ -745,11 +748,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             const int n = w.tiles();
             if (n == 0) continue;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(qfull, seg & 1, flags, a.dev_err, wait_ns));
-            if (ok) arrive_leader(qfull_other);
+            if (ok) arrive_leader(qfull_other, false);
             for (int i = 0; i < n * (kKS + kVS) && ok; ++i, ++seq) {
                 const int slot = seq % kSlots;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(full0 + 8 * slot, (seq / kSlots) & 1, flags, a.dev_err, wait_ns));
-                if (ok) arrive_leader(full_other0 + 8 * slot);
+                if (ok) arrive_leader(full_other0 + 8 * slot, false);
             }
             ++seg;
         }
@@ -917,6 +920,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             bool ok = true;
             for (int j = 0; j < n; ++j, ++g) {
                 const int buf = g & 1, key0 = w.key_tile(j) * kAttnKeys;
+                bool published = false;        // whether rows of V have been zeroed
                 ok = mbar_wait(sfull0 + 8 * buf, (g >> 1) & 1, flags, a.dev_err, wait_ns);
                 tc_fence_after();
                 if (active) {
@@ -1023,12 +1027,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                         if (key0 == head) zero(max(t.lo & -page, a.sinks), t.lo);
                         if (key0 == first) zero(a.sinks, min((a.sinks + page - 1) & -page, t.lo));
                         fence_proxy_async_smem();
-                        if (PAIR) fence_acq_rel_cluster();
+                        published = true;
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                arrive_leader(pready0 + 8 * buf);
+                arrive_leader(pready0 + 8 * buf, published);
             }
             seq += n * (kKS + kVS);
             // the tile's rows: finished, or a partial with its maximum and sum
@@ -1068,7 +1072,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             }
             tc_fence_before();
             __syncwarp();
-            arrive_leader(ofree);
+            arrive_leader(ofree, false);
         }
         // output rows past the requests' are zeros
         const int last_start = __ldg(a.q_start + a.R);
