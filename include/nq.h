@@ -439,7 +439,7 @@ typedef struct nq_kv_cache {
  *   slots           int64 [max_tokens], written: block * page + row of each token (nq_kv_append)
  *   counts          int32 [3], written: tokens, blocks taken from the free list, requests refused
  * A request is refused, and its tokens get position and slot -1, when a length is negative, when
- * it needs more than max_blocks blocks, when its tokens pass max_tokens, or when it needs blocks
+ * it would pass max_blocks blocks or 2^31 - 1 tokens, when its tokens pass max_tokens, or when it needs blocks
  * and the needs of the requests up to it, refused ones among them, pass the free list. Entries
  * past the last token are -1 too. The caller drops counts[1] ids from the front of its list.
  * 0 <= R <= NQ_MAX_REQUESTS; max_tokens <= 2^28; max_blocks <= 2^24. R = 0 needs max_tokens = 0 and

@@ -201,3 +201,19 @@ def test_pairs_with_more_requests_than_lanes(nq, window, sinks):
     for _ in range(10):
         assert torch.equal(first, nq.attn_paged(p["q"], p["k"], p["v"], p["table"], p["q_start"], p["kv"], window=window, sinks=sinks))
     nq.device_error()
+
+
+def test_page_tables_refuse_lengths_past_31_bits(nq):
+    """A table wide enough for 2^31 tokens and more: a request that would pass 2^31 - 1 is refused, one below is not."""
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    most, page = 2 ** 31 - 1, 256
+    table = torch.full((4, 2 ** 23 + 1), -7, dtype=torch.int32, device="cuda")
+    table[1, 0], table[2, 2 ** 23 - 1], table[3, 2 ** 23 - 1] = 5, 11, 13
+    lens, new = i32(most - 4, 3, most - 20, most - 1), i32(10, 2, 10, 1)
+    before = table.clone()
+    q_start, kv, pos, slots, counts = nq.page_tables(lens, new, i32(1, 2), i32(2), table, page, 23)
+    assert q_start.tolist() == [0, 10, 12, 22, 23] and counts.tolist() == [23, 0, 1]
+    assert kv.tolist() == [0, 5, most - 10, most]
+    assert pos.tolist() == [-1] * 10 + [3, 4] + list(range(most - 20, most - 10)) + [most - 1]
+    assert slots.tolist() == [-1] * 10 + [5 * 256 + 3, 5 * 256 + 4] + [11 * 256 + (p % 256) for p in range(most - 20, most - 10)] + [13 * 256 + 254]
+    assert torch.equal(table, before)

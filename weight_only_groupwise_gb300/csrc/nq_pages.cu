@@ -47,7 +47,8 @@ __device__ __forceinline__ PageNeed page_need(const PageArgs& a, int r) {
     p.n = n > 0 ? n : 0;
     const int mask = (1 << a.page_shift) - 1;
     const long long end = (long long)p.old + p.n;
-    p.valid = p.old >= 0 && n >= 0 && end <= ((long long)a.max_blocks << a.page_shift);
+    // (positions are 32-bit: a table may be wide enough for more)
+    p.valid = p.old >= 0 && n >= 0 && end <= min((long long)a.max_blocks << a.page_shift, 0x7FFFFFFFll);
     p.owned = p.valid ? (int)(((long long)p.old + mask) >> a.page_shift) : 0;
     p.need = p.valid ? (int)((end + mask) >> a.page_shift) - p.owned : 0;
     return p;
