@@ -217,3 +217,26 @@ def test_page_tables_refuse_lengths_past_31_bits(nq):
     assert pos.tolist() == [-1] * 10 + [3, 4] + list(range(most - 20, most - 10)) + [most - 1]
     assert slots.tolist() == [-1] * 10 + [5 * 256 + 3, 5 * 256 + 4] + [11 * 256 + (p % 256) for p in range(most - 20, most - 10)] + [13 * 256 + 254]
     assert torch.equal(table, before)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("log2", [20.0, 24.9, 25.1, 27.0])
+def test_many_keys_of_small_probability_count(nq, dtype, dim, log2):
+    """One key far above 2^18 others (one table row for as many requests as there are SMs, so that a block goes
+    through a whole one): V is 0 at it and 1 at the others, so O says what they weigh together. Off by the rounding of
+    the others' probability, the same for all (2^-7 where fp16 has six bits left), 2^14 fp32 sums (2^-9) and the output's."""
+    keys, page, R = 2 ** 18, 256, 152
+    k = torch.zeros((keys // page, page, 1, dim), device="cuda", dtype=dtype)
+    v = torch.ones_like(k)
+    q = torch.zeros((R, 1, dim), device="cuda", dtype=dtype)
+    q[..., 0] = 1.0
+    k[0, 5, 0, 0] = 1.0
+    v[0, 5] = 0.0
+    i32 = lambda x: torch.as_tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.arange(keys // page, device="cuda", dtype=torch.int32).expand(R, -1).contiguous()
+    out = nq.attn_paged(q, k, v, table, i32(range(R + 1)), i32([keys] * R), scale=log2 * math.log(2.0)).double()
+    nq.device_error()
+    rest = (keys - 1) * 2.0 ** -log2
+    want = rest / (1.0 + rest)
+    assert (out - want).abs().max().item() <= want * (2.0 ** -7 + 2.0 ** -9 + (2.0 ** -8 if dtype is BF else 2.0 ** -11))

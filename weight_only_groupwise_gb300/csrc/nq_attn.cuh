@@ -80,6 +80,9 @@ constexpr int kAttnCtrlBytes = 3072;
 constexpr int kAttnSnap = 6;                      // units by which a range may grow or shrink to avoid a split
 constexpr int kAttnWhole = 4;                     // a query tile of up to so many units is never split
 constexpr float kAttnLazy = 8.f;                  // log2 of the growth that forces a rescale
+// fp16 probabilities are stored times 2^7 (sums too, so that it cancels): at most 2^15, and keys count down to 2^-32
+// of the largest instead of 2^-25, of which 2^18 keys have 0.8 % of the sum.
+constexpr float kAttnLift = 7.f;
 
 // Shared-memory geometry for a head dimension: the K slot holds 128 keys x min(D, 128) columns,
 // the V slot as many bytes: 128 keys x D, or 64 keys x 256. (Slots of 16 KB, twice as many barrier
@@ -973,7 +976,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                         l *= f;
                     }
                     if (grow) m = mx;
-                    const float off = m == -INFINITY ? 0.f : -m * c;
+                    const float off = m == -INFINITY ? 0.f : fmaf(-m, c, BF16 ? 0.f : kAttnLift);
                     // p = 2^(c s + off), rounded, over S; their sum joins l. In two parts, so that the first is
                     // stored while the second is computed.
                     const uint64_t cc = pack2(__float_as_uint(c), __float_as_uint(c));
