@@ -398,7 +398,7 @@ void nq_program_destroy(nq_program* prog);
  * above (asynchronous on `stream`, arguments checked on the host before anything is launched,
  * programmatic dependent launch with every read and write after the preceding kernel) with these
  * differences: element pointers need 16-byte alignment, index arrays that of their type; strides
- * are in elements. Values inside device arrays cannot be checked on the host: each call says
+ * are in elements, and what a tensor spans is below 2^38 of them. Values inside device arrays cannot be checked on the host: each call says
  * what an unusable one does; none reads or writes outside the arrays it was given.
  */
 

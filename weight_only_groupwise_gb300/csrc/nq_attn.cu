@@ -131,15 +131,19 @@ nq_status nq_attn_paged(const void* q, long long q_stride, const nq_kv_cache* ca
     if (!(scale > 0.f) || !std::isfinite(scale)) return NQ_ERR_SHAPE;
     const long long row = (long long)q_heads * cache->dim;
     if (q_stride < row || out_stride < row) return NQ_ERR_SHAPE;
+    if (tokens == 1) q_stride = out_stride = row;       // between rows: nothing
+    const long long qb = 2 * step_span(tokens, q_stride, row), ob = 2 * step_span(tokens, out_stride, row);
+    const long long tb = max_blocks > 0 ? 4 * step_span(R, table_stride, max_blocks) : 0;
+    if (qb < 0 || ob < 0 || tb < 0) return NQ_ERR_SHAPE;
     if (tokens == 0) return NQ_OK;
     if (!q || !out || !q_start || (R > 0 && (!kv_lens || (max_blocks > 0 && !block_table)))) return NQ_ERR_NULL;
     if (mis16(q) || mis16(out) || q_stride % 8 || out_stride % 8) return NQ_ERR_ALIGN;
     for (const void* p : {(const void*)block_table, (const void*)q_start, (const void*)kv_lens})
         if (reinterpret_cast<uintptr_t>(p) & 3u) return NQ_ERR_ALIGN;
-    const long long ob = ((tokens - 1) * out_stride + row) * 2, span = kv_cache_span(cache);
-    if (meet(out, ob, q, ((tokens - 1) * q_stride + row) * 2) || meet(out, ob, cache->K, span) ||
+    const long long span = kv_cache_span(cache);
+    if (meet(out, ob, q, qb) || meet(out, ob, cache->K, span) ||
         meet(out, ob, cache->V, span) || meet(out, ob, q_start, (R + 1) * 4ll) || meet(out, ob, kv_lens, R * 4ll) ||
-        (R > 0 && meet(out, ob, block_table, ((R - 1) * table_stride + max_blocks) * 4)))
+        meet(out, ob, block_table, tb))
         return NQ_ERR_ALIAS;
     StepDevice d;
     st = step_device(&d);

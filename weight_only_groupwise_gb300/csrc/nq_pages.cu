@@ -288,6 +288,9 @@ int check_kv_cache(const nq_kv_cache* c) {
         c->block_stride >= (1ll << 38) || c->row_stride >= (1ll << 38) || c->head_stride >= (1ll << 38))
         return NQ_ERR_SHAPE;
     if (c->num_blocks == 0) return NQ_OK;
+    if (step_span(c->num_blocks, c->block_stride,
+                  step_span(c->page, c->row_stride, step_span(c->heads, c->head_stride, c->dim))) < 0)
+        return NQ_ERR_SHAPE;
     if (!c->K || !c->V) return NQ_ERR_NULL;
     if (mis16(c->K) || mis16(c->V) || c->block_stride % 8 || c->row_stride % 8 || c->head_stride % 8)
         return NQ_ERR_ALIGN;
@@ -295,9 +298,8 @@ int check_kv_cache(const nq_kv_cache* c) {
 }
 
 long long kv_cache_span(const nq_kv_cache* c) {
-    if (c->num_blocks == 0) return 0;
-    return ((c->num_blocks - 1) * c->block_stride + (c->page - 1) * c->row_stride + (c->heads - 1) * c->head_stride +
-            c->dim) * 2;
+    return 2 * step_span(c->num_blocks, c->block_stride,
+                         step_span(c->page, c->row_stride, step_span(c->heads, c->head_stride, c->dim)));
 }
 
 }  // namespace nq
@@ -314,6 +316,8 @@ nq_status nq_page_tables(const int* lens, const int* new_lens, int R, const int*
         return NQ_ERR_SHAPE;
     if (R == 0 && max_tokens == 0) return NQ_OK;
     if (R == 0) return NQ_ERR_SHAPE;   // tokens without requests
+    const long long table_span = max_blocks > 0 ? step_span(R, table_stride, max_blocks) : 0;
+    if (table_span < 0) return NQ_ERR_SHAPE;
     if (!lens || !new_lens || (free_capacity > 0 && !free_blocks) || !num_free || !q_start || !kv_lens || !counts ||
         (max_blocks > 0 && !block_table) || (max_tokens > 0 && (!positions || !slots)))
         return NQ_ERR_NULL;
@@ -323,7 +327,7 @@ nq_status nq_page_tables(const int* lens, const int* new_lens, int R, const int*
     struct {
         const void* p;
         long long n;
-    } out[] = {{block_table, max_blocks > 0 ? ((R - 1) * table_stride + max_blocks) * 4 : 0},
+    } out[] = {{block_table, table_span * 4},
                {q_start, (R + 1) * 4ll},
                {kv_lens, R * 4ll},
                {positions, max_tokens * 4ll},
@@ -382,12 +386,13 @@ nq_status nq_kv_append(const void* k, long long k_stride, const void* v, long lo
     if (st != NQ_OK) return st;
     const long long row = (long long)cache->heads * cache->dim;
     if (tokens < 0 || tokens > (1 << 28) || k_stride < row || v_stride < row) return NQ_ERR_SHAPE;
+    const long long kb = 2 * step_span(tokens, k_stride, row), vb = 2 * step_span(tokens, v_stride, row);
+    if (kb < 0 || vb < 0) return NQ_ERR_SHAPE;
     if (tokens == 0 || cache->num_blocks == 0) return NQ_OK;
     if (!k || !v || !slots) return NQ_ERR_NULL;
     if (mis16(k) || mis16(v) || k_stride % 8 || v_stride % 8 || (reinterpret_cast<uintptr_t>(slots) & 7u))
         return NQ_ERR_ALIGN;
     const long long span = kv_cache_span(cache);
-    const long long kb = ((tokens - 1) * k_stride + row) * 2, vb = ((tokens - 1) * v_stride + row) * 2;
     for (const void* c : {(const void*)cache->K, (const void*)cache->V})
         if (meet(c, span, k, kb) || meet(c, span, v, vb) || meet(c, span, slots, tokens * 8ll)) return NQ_ERR_ALIAS;
     StepDevice d;

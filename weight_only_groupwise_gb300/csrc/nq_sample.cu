@@ -1165,6 +1165,8 @@ extern "C" nq_status nq_sample(const void* logits, int dtype, long long stride, 
     if (B < 0 || B > (1 << 20) || V < 1 || V > kSaMaxVocab || stride < V || noise_stride < V) return NQ_ERR_SHAPE;
     if (dtype != NQ_BF16 && dtype != NQ_FP16 && dtype != NQ_FP32) return NQ_ERR_SHAPE;
     if (B == 0) return NQ_OK;
+    const long long logits_span = step_span(B, stride, V), noise_span = step_span(B, noise_stride, V);
+    if (logits_span < 0 || noise_span < 0) return NQ_ERR_SHAPE;
     if (!logits || !noise || !tokens) return NQ_ERR_NULL;
     const int size = dtype == NQ_FP32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(logits) % size) return NQ_ERR_ALIGN;
@@ -1172,7 +1174,7 @@ extern "C" nq_status nq_sample(const void* logits, int dtype, long long stride, 
                           (const void*)min_p, (const void*)tokens})
         if (reinterpret_cast<uintptr_t>(p) & 3u) return NQ_ERR_ALIGN;
     const long long tb = B * 4ll;
-    if (meet(tokens, tb, logits, ((B - 1) * stride + V) * size) || meet(tokens, tb, noise, ((B - 1) * noise_stride + V) * 4) ||
+    if (meet(tokens, tb, logits, logits_span * size) || meet(tokens, tb, noise, noise_span * 4) ||
         meet(tokens, tb, temperature, tb) || meet(tokens, tb, top_k, tb) || meet(tokens, tb, top_p, tb) ||
         meet(tokens, tb, min_p, tb))
         return NQ_ERR_ALIAS;

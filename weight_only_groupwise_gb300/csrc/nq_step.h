@@ -23,6 +23,15 @@ int step_device(StepDevice* out);
 // bytes of scratch.
 int attn_workspace(uint8_t** ws);
 
+// Elements from the first of `rows` rows, `stride` apart, to the end of the last; -1 from 2^38 on, which no tensor
+// of this GPU can have (the limit keeps spans and offsets in 64 bits, and strides in a tensor map's range).
+inline long long step_span(long long rows, long long stride, long long row) {
+    if (rows <= 0) return 0;
+    constexpr long long most = 1ll << 38;
+    if (row < 0 || row >= most || (rows > 1 && stride > (most - 1 - row) / (rows - 1))) return -1;
+    return (rows - 1) * stride + row;
+}
+
 constexpr size_t kAttnErrBytes = 256;
 constexpr int kAttnRows = 128;      // query rows of an attention tile
 constexpr int kAttnMaxDim = 256;
