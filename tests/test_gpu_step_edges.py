@@ -240,3 +240,15 @@ def test_many_keys_of_small_probability_count(nq, dtype, dim, log2):
     rest = (keys - 1) * 2.0 ** -log2
     want = rest / (1.0 + rest)
     assert (out - want).abs().max().item() <= want * (2.0 ** -7 + 2.0 ** -9 + (2.0 ** -8 if dtype is BF else 2.0 ** -11))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+def test_infinite_logits_are_cut_among_themselves(nq, dtype):
+    """Three infinite logits among ties: top-k and top-p over trials keep the first, the first two, all."""
+    V = 8884
+    x = torch.full((6, V), 3.0, device="cuda", dtype=dtype)
+    e = torch.full((6, V), 1e-9, device="cuda")
+    for i, z in ((4087, 4.0), (4910, 0.8), (8002, 0.4)):
+        x[:, i], e[:, i] = math.inf, z
+    s = settings(6, 1.3, [60, 60, 60, 3000, 3000, 3000], [-1.0, 0.5, 1.0, 0.3, 0.6, 0.9], 0.0)
+    assert nq.sample(x, e, **s).tolist() == [4087, 4910, 8002, 4087, 4910, 8002]
