@@ -37,9 +37,11 @@ L2_BYTES = 129 * 1000 * 1000
 FALLBACK_HBM_GBS = 6800.0
 METRIC = "µs/call and achieved HBM GB/s (% of roofline) for Q4/Q5 skinny GEMM, T=1..8"
 MAX_T = 64
-# The device code and work split of the projection kernels (not the library's other kernels or its
-# host runtime, whose changes leave the captured traffic valid).
-KERNEL_SOURCES = ["nq_common.cuh", "nq_proj.cuh", "nq_tc.cuh"]
+# What decides a projection's DRAM traffic: its kernels, their work split, the tensor maps and the choice of
+# kernel, grid and cluster on the host. All sources but those of the serving step's own kernels.
+STEP_SOURCES = {"nq_attn.cu", "nq_attn.cuh", "nq_pages.cu", "nq_sample.cu", "nq_step.h"}
+KERNEL_SOURCES = sorted(f for f in os.listdir(os.path.join(ROOT, "weight_only_groupwise_gb300", "csrc"))
+                        if f.endswith((".cu", ".cuh", ".h")) and f not in STEP_SOURCES)
 
 
 # ---------------------------------------------------------------- ranks
