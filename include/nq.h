@@ -453,7 +453,7 @@ nq_status nq_page_tables(const int* lens, const int* new_lens, int R, const int*
 /*
  * nq_kv_append: store the step's keys and values through the slot map: token t's K row
  * ([heads][dim], k + t * k_stride) and V row go to slot slots[t] = block * page + row. A slot
- * outside the cache (-1) stores nothing. Two tokens with one slot: either may win. The 16-bit
+ * outside the cache (-1) stores nothing. Two tokens with one slot: either may win, for K and for V each by itself. The 16-bit
  * elements are copied as they are. k and v must not overlap the cache.
  */
 nq_status nq_kv_append(const void* k, long long k_stride, const void* v, long long v_stride, const int64_t* slots,
@@ -477,7 +477,8 @@ nq_status nq_kv_append(const void* k, long long k_stride, const void* v, long lo
  * not used (a window's old pages may have been given back, page by page); an entry outside the
  * cache reads as rows of zeros. Cache rows that no new token sees may hold anything, NaN included. A NaN or infinity in
  * a V row that one of a tile's tokens sees reaches the other tokens of that tile (up to 128 / G
- * consecutive ones), as 0 * NaN does in a plain product.
+ * consecutive ones, 256 / G where two blocks share a tile: large prompts of 256 columns), as 0 * NaN does in a
+ * plain product.
  * q_start is clamped to 0..tokens and taken as non-decreasing, kv_lens to 0..max_blocks * page.
  * One launch over all SMs and one that joins query tiles whose keys were spread over several (left
  * out where max_blocks or the window bounds every tile to a few hundred keys); deterministic for a

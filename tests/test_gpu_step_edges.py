@@ -252,3 +252,17 @@ def test_infinite_logits_are_cut_among_themselves(nq, dtype):
         x[:, i], e[:, i] = math.inf, z
     s = settings(6, 1.3, [60, 60, 60, 3000, 3000, 3000], [-1.0, 0.5, 1.0, 0.3, 0.6, 0.9], 0.0)
     assert nq.sample(x, e, **s).tolist() == [4087, 4910, 8002, 4087, 4910, 8002]
+
+
+@pytest.mark.parametrize("dim,heads,tile", [(128, 8, 64), (256, 24, 42)])
+def test_nan_in_a_seen_row_of_v_stays_in_its_tile(nq, dim, heads, tile):
+    """The last token's V row is NaN: it reaches itself and at most its tile's other tokens, 128 / G of one
+    block, 256 / G of a pair (rounded down to a block's whole tokens)."""
+    from tests.test_gpu_attn import problem, reference
+    p = problem([0], [700], heads, 4, dim, 64, BF, seed=dim)
+    ref, bound = reference(p, dim ** -0.5)
+    p["v"][int(p["table"][0, 699 // 64]), 699 % 64] = math.nan
+    out = nq.attn_paged(p["q"], p["k"], p["v"], p["table"], p["q_start"], p["kv"])
+    assert out[699].isnan().all()
+    first = 700 - tile
+    assert ((out[:first].double() - ref[:first]).abs() <= bound[:first]).all()
