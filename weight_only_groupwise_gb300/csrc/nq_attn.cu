@@ -32,8 +32,9 @@ cudaError_t attn_launch(const AttnArgs& a, int blocks, bool splits, cudaStream_t
                                 PAIR ? 2 : 1, a);
     if (e != cudaSuccess || !splits) return e;
     // a block takes 32 items of a split with many parts. Its launch follows the exit of the attention
-    // kernel's blocks, which do not ask for it themselves: join blocks that wait beside working ones slow them (one
-    // token over 4099 keys: 18.0 us as an ordinary launch, 15.5 so, 19 if asked for at the end of a block)
+    // kernel's blocks, which do not ask for it themselves: join blocks that wait beside working ones slow them. One
+    // token over 4100 keys, in a stream and in a graph: 15.5 and 15.2 us so, 18.0 and 15.4 as an ordinary launch, 19.0 and
+    // 18.5 if the blocks ask at their end, 21.3 and 21.0 at their start.
     const int rows = (a.tokens < a.block_tokens ? a.tokens : a.block_tokens) * a.group;
     const int y = (rows * (D / 8) + 31) / 32;
     return step_launch(attn_join_kernel<D, BF16>, dim3(blocks, y < kJoinBlocksY ? y : kJoinBlocksY), dim3(kJoinThreads), 0,

@@ -37,7 +37,8 @@
 //     halves of a row exchange maxima through shared memory. The accumulator is rescaled only
 //     when a row's maximum grows by more than 2^8 in the exponential's argument (p <= 256 stays
 //     exact enough in 16 bits, the sum is fp32); p is rounded to the 16-bit type of the cache
-//     for the second product: its error averages out below the output's own rounding. (Alternate
+//     for the second product, which takes 16-bit operands: against 64 bits O is off by 0.0021 (bf16, relative) where
+//     probabilities of 32 bits and the output's rounding alone leave 0.0017, 0.00027 and 0.00021 in fp16. (Alternate
 //     tiles for the two groups of four warps, each with an accumulator of its own, were slower: 267
 //     us against 253 for 64 one-token requests of 128 columns.)
 //   * warps 8 and 11 -- producers of K and of V: TMA copies of pages (a 4-D map of the cache: dim,

@@ -15,8 +15,8 @@
 //     them bounds the block's k-th token from below, so the tokens from there up, little more than k,
 //     hold its first k. They are handed to one block, which sorts them and settles the row: one
 //     barrier of the cluster. top-p alone tries the same with the first 48 of each block, if
-//     those can hold the share (one row of 152064 then takes 13 us; with 96 it takes 18, with 24 they
-//     more often do not hold it: 12 or 26).
+//     those can hold the share (one row of 152064 then takes 13 us, 23 where they cannot; with 96 tokens 19 and
+//     24, with 24 tokens 13 and 27, and fewer rows are settled).
 //   * a cut among many tokens: the race over all tokens, then one pass that sums what lies before
 //     its winner. If that is less than k tokens, or than the share p, the winner is kept, and so
 //     is the winner of the kept ones. Else all kept tokens lie before it, and the race is run
@@ -37,9 +37,9 @@
 // that lies within that sum's error of the cut is left to the trials.
 //
 // Bound by the latency of these few steps for few rows, by instructions per token and barriers
-// for many (the logits' bytes alone would take a fraction of it). Measured: one row of 152064 bf16,
-// top-k 50 and top-p 0.9, 10.2 us; 64 of them 17; 64 with mixed settings 47; 256 of 128257 fp32 124. With
-// histograms of the mass in place of the trials the mixed ones took 79 and 157.
+// for many (the logits' bytes alone would take a fraction of it). Measured, replayed in a graph: one row of 152064
+// bf16, top-k 50 and top-p 0.9, 10.3 us; 64 of them 17; 64 with mixed settings 47 to 67, 256 of 128257 fp32 121 to 152
+// (by the random numbers). With histograms of the mass in place of the trials the mixed ones took 79 and 157.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1137,7 +1137,9 @@ nq_status sample_rows(SampleArgs a, int B, const StepDevice& d, cudaStream_t str
     // Eight blocks a row while every block of the call can be resident at once (two an SM); past
     // that fewer and larger slices, up to 40000 tokens (fp32: what fits shared memory), which saves
     // cluster barriers. Measured, mixed settings: 64 rows of 152064 bf16 51 us at 8, 47 at 4; 256
-    // rows of 128257 fp32 157 at 8, 124 at 4, 267 at 2; top-k 50 on 256 rows of 32001 25 at 2, 16 at 1.
+    // rows of 128257 fp32 157 at 8, 124 at 4, 267 at 2; top-k 50 on 256 rows of 32001 25 at 2, 16 at 1. 16-bit slices
+    // up to 65000, which would fit too: 256 rows of 200000 150 us against 215, 64 of them 64 against 69, but 256 of
+    // 128256 with top-k 50 and top-p 0.9 66 against 59; 152064, 160000 and 262144 the same within 3 %.
     int C = kSaMaxCluster;
     while (C > 1 && (long long)B * C > 2 * d.sms && a.V / (C / 2) <= 40000) C /= 2;
     a.slice = ((a.V + C - 1) / C + 15) / 16 * 16;
