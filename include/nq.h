@@ -480,6 +480,7 @@ nq_status nq_kv_append(const void* k, long long k_stride, const void* v, long lo
  * consecutive ones, 256 / G where two blocks share a tile: large prompts of 256 columns), as 0 * NaN does in a
  * plain product.
  * q_start is clamped to 0..tokens and taken as non-decreasing, kv_lens to 0..max_blocks * page.
+ * Rows of out before q_start[0] are left as they are.
  * One launch over all SMs and one that joins query tiles whose keys were spread over several (left
  * out where max_blocks or the window bounds every tile to a few hundred keys); deterministic for a
  * given device. Uses a library workspace of about 40 MB, allocated on the
