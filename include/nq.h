@@ -402,7 +402,7 @@ void nq_program_destroy(nq_program* prog);
  * what an unusable one does; none reads or writes outside the arrays it was given.
  */
 
-enum { NQ_BF16 = 0, NQ_FP16 = 1, NQ_FP32 = 2 };   /* dtype arguments */
+enum { NQ_BF16 = 0, NQ_FP16 = 1, NQ_FP32 = 2, NQ_E4M3 = 3 };   /* dtype arguments */
 
 /* Most requests of one call. */
 #define NQ_MAX_REQUESTS 8192
@@ -520,6 +520,114 @@ nq_status nq_attn_reserve(void);
 nq_status nq_sample(const void* logits, int dtype, long long stride, const float* noise, long long noise_stride,
                     int B, int V, const float* temperature, const int* top_k, const float* top_p, const float* min_p,
                     int* tokens, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit products and experts */
+
+/*
+ * Products of e4m3 codes with a scale for each block of 128 ("prompts": any number of rows, where the
+ * projections above end at 64 tokens), dense or by expert, and what a layer of experts needs around them. The
+ * calls follow the serving step's conventions: index arrays and lengths are DEVICE arrays, strides are in
+ * elements, spans are below 2^38 elements; they use no workspace, so calls of several streams, and graphs of them, may overlap.
+ * The pages name mixture-of-experts models without describing their kernels: formats and calls are this
+ * library's definition.
+ *
+ *   x[t, k] = sx[t, k / 128] * e4m3(cx[t, k]),   w[n, k] = sw[n / 128, k / 128] * e4m3(cw[n, k])
+ *
+ * The last block of a row or column may be short. Codes are bytes (e4m3 "fn": no infinity, S.1111.111 is NaN),
+ * scales fp32.
+ */
+
+/* Rows of activations: codes [rows][K], `stride` apart (a multiple of 16), scales [rows][ceil(K / 128)],
+ * `scale_stride` apart. */
+typedef struct nq_fp8_rows {
+    const void* codes;
+    const float* scales;
+    long long stride, scale_stride;
+    int rows;
+} nq_fp8_rows;
+
+/* A weight, or one for each expert: codes [E][N][K], rows row_stride and experts expert_stride apart
+ * (multiples of 16), scales [E][ceil(N / 128)][ceil(K / 128)], scale_row_stride and scale_expert_stride apart. */
+typedef struct nq_fp8_weight {
+    const void* codes;
+    const float* scales;
+    long long row_stride, expert_stride, scale_row_stride, scale_expert_stride;
+} nq_fp8_weight;
+
+/* A result: NQ_BF16 or NQ_FP16 [rows][N], `stride` apart (any; the alignment of the type will do, 32 bytes are
+ * fastest); or, of the SwiGLU calls with N a multiple of 16, NQ_E4M3: codes (16-byte aligned, stride a multiple of
+ * 16) and fp32 scales [rows][ceil(N / 128)], `scale_stride` apart, quantised as nq_quant_fp8 does. */
+typedef struct nq_fp8_out {
+    void* data;
+    float* scales;
+    long long stride, scale_stride;
+    int dtype;
+} nq_fp8_out;
+
+/*
+ * nq_quant_fp8: x (dtype NQ_BF16, NQ_FP16 or NQ_FP32) [rows][K] as codes and scales:
+ *   s[r, b] = max(max_{k in b} |x[r, k]| / 448, 2^-126),   c[r, k] = e4m3(x[r, k] / s[r, b]),
+ * in fp32, rounded to nearest even. A block with a NaN gets scale NaN and codes NaN; one with an infinity scale inf
+ * (codes NaN where x is infinite, else 0): its products are NaN. K a multiple of 16, at most 2^20; rows <= 2^24. Rows of x
+ * and codes 16-byte aligned.
+ */
+nq_status nq_quant_fp8(const void* x, int dtype, long long x_stride, int rows, int K, void* codes,
+                       long long codes_stride, float* scales, long long scale_stride, void* stream);
+
+/*
+ * nq_gemm_fp8: y[t, n] = sum_k x[t, k] w[n, k] for all rows of x. Products within a block of 128 are summed by the
+ * tensor cores, blocks in fp32; y is rounded once. nq_swiglu_fp8: h = silu(g) u (fp32) of the two
+ * products g = x wg and u = x wu.
+ *   K a multiple of 16, 16 <= K <= 2^20; 1 <= N <= 2^20; rows <= 2^24. Nothing may overlap the result.
+ */
+nq_status nq_gemm_fp8(const nq_fp8_rows* x, const nq_fp8_weight* w, const nq_fp8_out* y, int K, int N, void* stream);
+nq_status nq_swiglu_fp8(const nq_fp8_rows* x, const nq_fp8_weight* wg, const nq_fp8_weight* wu, const nq_fp8_out* h,
+                        int K, int N, void* stream);
+
+/*
+ * nq_gemm_fp8_experts / nq_swiglu_fp8_experts: the same for M rows that lie in the order of their experts: rows
+ * offsets[e] <= i < offsets[e + 1] (device int32 [E + 1]) take expert e's weight.
+ *   rows  device int32 [M]: row i is row rows[i] of x (any order, any number of times; one outside x reads
+ *         as zeros); NULL: row i of x, and then M <= x->rows
+ * offsets are clamped to 0..M and taken as non-decreasing. Rows of the result before offsets[0] and from offsets[E] on
+ * are left as they are. 1 <= E <= 1024. The tensors of experts without rows are not read.
+ */
+nq_status nq_gemm_fp8_experts(const nq_fp8_rows* x, const int* rows, int M, const int* offsets, int E,
+                              const nq_fp8_weight* w, const nq_fp8_out* y, int K, int N, void* stream);
+nq_status nq_swiglu_fp8_experts(const nq_fp8_rows* x, const int* rows, int M, const int* offsets, int E,
+                                const nq_fp8_weight* wg, const nq_fp8_weight* wu, const nq_fp8_out* h, int K, int N,
+                                void* stream);
+
+enum { NQ_SOFTMAX = 0, NQ_SIGMOID = 1 };   /* score arguments */
+
+/*
+ * nq_moe_route: each token's k experts of E, their weights, and the order of the rows by expert.
+ *   logits  dtype NQ_BF16, NQ_FP16 or NQ_FP32 [T][E], rows `stride` apart; NaN counts as -inf
+ *   score   NQ_SOFTMAX: s = softmax of the row; NQ_SIGMOID: s = 1 / (1 + e^-l)
+ *   bias    fp32 [E] or NULL, NQ_SIGMOID only: choose by s + bias (in 64 bits), weigh by s; NaN counts as -inf
+ *   ids     int32 [T][k], written: the experts with the largest logits (or s + bias), in descending order, the lower
+ *           index first where two are equal; -1 behind the last where fewer than k have a logit (and bias) above
+ *           -inf: a padded row of -inf takes none
+ *   weights fp32 [T][k], written: scale * s, with `normalize` scale * s / (the chosen ones' sum), also of scores
+ *           that fp32 cannot hold; 0 where ids is -1
+ *   offsets int32 [E + 1], written: expert e's rows are offsets[e]..offsets[e + 1] - 1
+ *   rows    int32 [T * k], written: the token of each row, ascending within an expert; -1 from offsets[E] on
+ *   slots   int32 [T][k], written: the row of each choice, -1 where ids is -1
+ * 0 <= T <= 2^20 (0: offsets only), 1 <= k <= min(E, 32), E <= 1024, 0 < scale < inf. Logits need the alignment of their type.
+ */
+nq_status nq_moe_route(const void* logits, int dtype, long long stride, const float* bias, int T, int E, int k,
+                       int score, int normalize, float scale, int* ids, float* weights, int* offsets, int* rows,
+                       int* slots, void* stream);
+
+/*
+ * nq_moe_combine: out[t] = base[t] + sum_j weights[t, j] y[slots[t, j]], fp32, in the order of j, rounded once.
+ *   y, base (may be NULL: none), out  NQ_BF16 or NQ_FP16 [M][N], [T][N], [T][N]; 16-byte aligned rows
+ *   slots int32 [T][k]: one outside 0..M-1 adds nothing, whatever its weight
+ * N a multiple of 8; k <= 32; T <= 2^20, M <= 2^24. out may be base; else it must not overlap an input.
+ */
+nq_status nq_moe_combine(const void* y, int dtype, long long y_stride, int M, const int* slots, const float* weights,
+                         int T, int k, int N, const void* base, long long base_stride, void* out, long long out_stride,
+                         void* stream);
 
 /* ---------------------------------------------------------------- runtime */
 

@@ -1,0 +1,536 @@
+// nq_moe.cu -- around the experts of a layer: which experts a token takes and where its rows lie (nq_moe_route), and
+// the sum of their results (nq_moe_combine).
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "nq.h"
+#include "nq_common.cuh"
+#include "nq_fp8.h"
+#include "nq_step.h"
+
+namespace nq {
+namespace {
+
+namespace cg = cooperative_groups;
+
+// ---------------------------------------------------------------- router
+
+// Choice of experts: a warp a token, expert 32 v + lane in the lane's register v. Logits become whole numbers of
+// the same order, so that a round is one redux for the largest and one for the lowest index that has it.
+//
+// With a bias the order is that of sigmoid(l) + b in 64 bits, which this GPU has few units for. It is computed in 32 bits with
+// an error below kRtTol (1 + |value|), and only where two neighbours of the chosen (or the best of the others) are
+// nearer than that, and not the same number twice, is the token done again in 64.
+//
+// Places: a stable counting sort by expert, by one cluster of blocks, each with a share of the tokens in order. A
+// block counts its tokens' choices, the blocks exchange their counts, and each finds its tokens' places from a
+// bit set of tokens for each expert (the tokens before this one that chose it: a population count), so that no
+// order of atomics shows. Calls of few tokens choose and place in one launch.
+
+constexpr int kRtThreads = 1024;
+constexpr int kRtWarps = kRtThreads / 32;
+constexpr int kRtCluster = 8;                    // blocks of the placing cluster
+constexpr int kRtChooseThreads = 256;            // of a choosing block of a large call
+constexpr int kRtMostChosen = 32;
+constexpr int kRtMostTokens = 1 << 20;
+constexpr int kRtBits = 24576;                   // words of bit sets in shared memory
+constexpr float kRtTol = 0x1p-20f;
+
+struct RouteArgs {
+    const void* logits;
+    long long stride;
+    const float* bias;                           // sigmoid only; may be NULL
+    int* ids;
+    float* weights;
+    int* offsets;
+    int* rows;
+    int* slots;
+    int T, E, k;
+    float scale;
+    int dtype;
+    bool sigmoid, normalize;
+    int share;                                   // tokens of a block of the placing cluster
+    int words;                                   // of a bit set: tokens of a pass / 32
+};
+
+__device__ __forceinline__ float route_load(const void* p, long long i, int dtype) {
+    if (dtype == NQ_FP32) return __ldg(static_cast<const float*>(p) + i);
+    const uint16_t h = __ldg(static_cast<const unsigned short*>(p) + i);
+    return dtype == NQ_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+}
+
+// A number that orders as f does (both zeros equal); 0, below all, for NaN and -inf.
+__device__ __forceinline__ uint32_t route_key(float f) {
+    if (!(f > -INFINITY)) return 0;
+    const uint32_t b = __float_as_uint(f + 0.f);
+    return (b >> 31) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float route_value(uint32_t key) {
+    return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
+}
+
+__device__ __forceinline__ float sigmoid_f(float l) { return 1.f / (1.f + expf(-l)); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    return v;
+}
+
+// The choice of one token in 64 bits: lane j gets the j-th expert, or -1.
+template <int V>
+__device__ __noinline__ int route_choose_64(const RouteArgs& a, long long row) {
+    const int lane = threadIdx.x & 31;
+    uint32_t taken = 0;
+    int mine = -1;
+    for (int j = 0; j < a.k; ++j) {
+        double best = -INFINITY;
+        int at = -1;
+        for (int v = 0; v < V; ++v) {
+            const int e = 32 * v + lane;
+            if (e >= a.E || ((taken >> v) & 1)) continue;
+            const float l = route_load(a.logits, row + e, a.dtype);
+            if (!(l > -INFINITY)) continue;
+            const double s = 1.0 / (1.0 + exp(-(double)l)) + (double)__ldg(a.bias + e);
+            if (s > best) {
+                best = s;
+                at = e;
+            }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            const double s = __shfl_xor_sync(0xFFFFFFFFu, best, d);
+            const int e = __shfl_xor_sync(0xFFFFFFFFu, at, d);
+            if (e >= 0 && (at < 0 || s > best || (s == best && e < at))) {
+                best = s;
+                at = e;
+            }
+        }
+        if (at < 0) break;
+        if ((at & 31) == lane) taken |= 1u << (at >> 5);
+        if (lane == j) mine = at;
+    }
+    return mine;
+}
+
+// Chooses token t's experts and writes them with their weights.
+template <int V>
+__device__ __forceinline__ void route_choose(const RouteArgs& a, int t) {
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)t * a.stride;
+    float l[V];
+    uint32_t key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 32 * v + lane;
+        l[v] = e < a.E ? route_load(a.logits, row + e, a.dtype) : -INFINITY;
+    }
+    const bool biased = a.bias != nullptr;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 32 * v + lane;
+        float f = l[v];
+        if (biased && e < a.E && f > -INFINITY) f = sigmoid_f(f) + __ldg(a.bias + e);
+        key[v] = route_key(f);
+    }
+    int mine = -1;                               // lane j: the j-th choice
+    float value = 0.f;                           // biased: its value
+    uint32_t first = 0, last = 0;
+    bool unsure = false;
+    const int rounds = biased ? a.k + 1 : a.k;
+    for (int j = 0; j < rounds; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) m = max(m, key[v]);
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (m == 0) break;
+        uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+            if (key[v] == m) at = 32 * v + lane;
+        at = __reduce_min_sync(0xFFFFFFFFu, at);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (at == 32 * v + lane) key[v] = 0;
+        if (biased && j > 0) {
+            // (the same number twice, a tie in any precision, is left to 64 bits too: what follows it could pass both)
+            const float hi = route_value(last), lo = route_value(m);
+            unsure = unsure || !(hi - lo > kRtTol * (1.f + fabsf(hi)));
+        }
+        last = m;
+        if (j == 0) first = m;
+        if (lane == j && j < a.k) {
+            mine = (int)at;
+            value = route_value(m);
+        }
+    }
+    if (biased && unsure) mine = route_choose_64<V>(a, row);
+    // weights of the chosen
+    const float c = mine >= 0 ? route_load(a.logits, row + mine, a.dtype) : -INFINITY;
+    float w;
+    if (a.sigmoid) {
+        float top = c;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        // far below zero the sigmoid is e^l: taken relative to the largest, it does not vanish
+        const bool far = a.normalize && top < -60.f;
+        w = mine < 0 ? 0.f : (far ? expf(c - top) : sigmoid_f(c));
+        if (a.normalize) {
+            const float sum = warp_sum(w);
+            if (mine >= 0) w = w / sum;
+        }
+    } else {
+        const float top = route_value(first);
+        w = mine < 0 ? 0.f : (c == top ? 1.f : expf(c - top));
+        float sum;
+        if (a.normalize) {
+            sum = warp_sum(w);
+        } else {
+            float part = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (l[v] > -INFINITY) part += l[v] == top ? 1.f : expf(l[v] - top);
+            sum = warp_sum(part);
+        }
+        if (mine >= 0) w = w / sum;
+    }
+    if (lane < a.k) {
+        a.ids[(long long)t * a.k + lane] = mine;
+        a.weights[(long long)t * a.k + lane] = w * a.scale;
+    }
+    (void)value;
+}
+
+// Places of the tokens' rows, by a cluster of blocks (see above). Shared memory: counts of the block [E], places
+// [E], then bit sets [E][words] and their running counts [E][words].
+__device__ __forceinline__ void route_place(const RouteArgs& a, int* sm) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank(), blocks = (int)cl.num_blocks(), tid = threadIdx.x;
+    int* const count = sm;
+    int* const place = sm + a.E;
+    uint32_t* const bits = reinterpret_cast<uint32_t*>(sm + 2 * a.E);
+    int* const before = reinterpret_cast<int*>(bits + (size_t)a.E * a.words);
+    __shared__ int warp_total[kRtWarps];
+    const int t0 = min(a.T, rank * a.share), t1 = min(a.T, t0 + a.share);
+    const int total = a.T * a.k;
+    for (int e = tid; e < a.E; e += kRtThreads) count[e] = 0;
+    __syncthreads();
+    for (int i = t0 * a.k + tid; i < t1 * a.k; i += kRtThreads) {
+        const int e = a.ids[i];
+        if (e >= 0) atomicAdd(count + e, 1);
+    }
+    cl.sync();
+    // experts' totals and the rows of the blocks before this one
+    int mine = 0, ahead = 0;
+    if (tid < a.E)
+        for (int b = 0; b < blocks; ++b) {
+            const int c = *cl.map_shared_rank(count + tid, b);
+            if (b < rank) ahead += c;
+            mine += c;
+        }
+    // scan over experts: at most 1024, one a thread
+    int upto = mine;
+    const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += u;
+    }
+    if (lane == 31) warp_total[warp] = upto;
+    __syncthreads();
+    int base = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kRtWarps; ++w) {
+        const int c = warp_total[w];
+        if (w < warp) base += c;
+        all += c;
+    }
+    if (tid < a.E) {
+        place[tid] = base + upto - mine + ahead;
+        if (rank == 0) {
+            a.offsets[tid] = base + upto - mine;
+            if (tid == a.E - 1) a.offsets[a.E] = all;
+        }
+    }
+    // the entries behind the last row
+    for (int i = all + rank * kRtThreads + tid; i < total; i += blocks * kRtThreads) a.rows[i] = -1;
+    const int pass = 32 * a.words;
+    for (int p0 = t0; p0 < t1; p0 += pass) {
+        const int p1 = min(t1, p0 + pass);
+        for (int i = tid; i < a.E * a.words; i += kRtThreads) bits[i] = 0;
+        __syncthreads();
+        for (int i = p0 * a.k + tid; i < p1 * a.k; i += kRtThreads) {
+            const int e = a.ids[i], t = i / a.k - p0;
+            if (e >= 0) atomicOr(bits + e * a.words + (t >> 5), 1u << (t & 31));
+        }
+        __syncthreads();
+        for (int e = tid; e < a.E; e += kRtThreads) {
+            int n = place[e];
+            for (int w = 0; w < a.words; ++w) {
+                before[e * a.words + w] = n;
+                n += __popc(bits[e * a.words + w]);
+            }
+            place[e] = n;
+        }
+        __syncthreads();
+        for (int i = p0 * a.k + tid; i < p1 * a.k; i += kRtThreads) {
+            const int e = a.ids[i], token = i / a.k, t = token - p0;
+            int at = -1;
+            if (e >= 0) {
+                const int w = e * a.words + (t >> 5);
+                at = before[w] + __popc(bits[w] & ((1u << (t & 31)) - 1));
+                a.rows[at] = token;
+            }
+            a.slots[i] = at;
+        }
+        __syncthreads();
+    }
+    cl.sync();                                   // no block leaves while another reads its counts
+}
+
+template <int V>
+__global__ void __launch_bounds__(kRtChooseThreads) route_choose_kernel(const RouteArgs a) {
+    const int t = blockIdx.x * (kRtChooseThreads / 32) + (threadIdx.x >> 5);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (t < a.T) route_choose<V>(a, t);
+}
+
+template <int V>
+__global__ void __launch_bounds__(kRtThreads, 1) route_few_kernel(const RouteArgs a) {
+    extern __shared__ int route_smem[];
+    const int rank = (int)cluster_rank();
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int t0 = min(a.T, rank * a.share), t1 = min(a.T, t0 + a.share);
+    for (int t = t0 + (threadIdx.x >> 5); t < t1; t += kRtWarps) route_choose<V>(a, t);
+    __syncthreads();
+    route_place(a, route_smem);
+}
+
+__global__ void __launch_bounds__(kRtThreads, 1) route_place_kernel(const RouteArgs a) {
+    extern __shared__ int route_smem[];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    route_place(a, route_smem);
+}
+
+template <int V>
+cudaError_t route_launch(RouteArgs a, cudaStream_t stream, bool pdl) {
+    // one launch while a warp of the cluster has few tokens
+    const bool few = a.T <= kRtCluster * kRtWarps * 2;
+    const int blocks = few ? min(kRtCluster, (a.T + kRtWarps - 1) / kRtWarps) : kRtCluster;
+    a.share = (a.T + blocks - 1) / blocks;
+    a.words = min((a.share + 31) / 32, max(1, kRtBits / a.E));
+    const size_t smem = (size_t)(2 * a.E + 2 * a.E * a.words) * 4;
+    const void* kern = few ? (const void*)route_few_kernel<V> : (const void*)route_place_kernel;
+    if (smem > 40 * 1024) {
+        static thread_local int set_for_device[2] = {-1, -1};
+        int dev = 0;
+        cudaGetDevice(&dev);
+        if (set_for_device[few] != dev) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 208 * 1024);
+            if (e != cudaSuccess) return e;
+            set_for_device[few] = dev;
+        }
+    }
+    if (few) return step_launch(route_few_kernel<V>, dim3(blocks), dim3(kRtThreads), smem, stream, pdl, blocks, a);
+    const int per = kRtChooseThreads / 32;
+    const cudaError_t e = step_launch(route_choose_kernel<V>, dim3((a.T + per - 1) / per), dim3(kRtChooseThreads), 0, stream,
+                                      pdl, 1, a);
+    if (e != cudaSuccess) return e;
+    return step_launch(route_place_kernel, dim3(blocks), dim3(kRtThreads), smem, stream, pdl, blocks, a);
+}
+
+// ---------------------------------------------------------------- combination
+
+// A thread a token's 8 columns: its k rows' loads are in flight together; the sum is fp32, in the order of the choices.
+// Bound by memory: each row of y once.
+
+constexpr int kCbThreads = 128;
+constexpr int kCbRows = 4;                       // rows whose loads are in flight together
+
+struct CombineArgs {
+    const uint8_t* y;
+    const int* slots;
+    const float* weights;
+    const uint8_t* base;
+    uint8_t* out;
+    long long y_stride, base_stride, out_stride; // bytes
+    int M, T, k, N;
+    uint32_t segments;                           // blocks of kCbThreads x 8 columns in a row
+};
+
+template <bool BF16>
+__device__ __forceinline__ void add_eight(float (&sum)[8], uint4 v, float w) {
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 p;
+        if constexpr (BF16) {
+            p.x = __uint_as_float(x[i] << 16);
+            p.y = __uint_as_float(x[i] & 0xFFFF0000u);
+        } else {
+            p = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
+        }
+        sum[2 * i] = fmaf(w, p.x, sum[2 * i]);
+        sum[2 * i + 1] = fmaf(w, p.y, sum[2 * i + 1]);
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kCbThreads) combine_kernel(const CombineArgs a) {
+    const int t = (int)(blockIdx.x / a.segments);
+    const int col = ((int)(blockIdx.x - (uint32_t)t * a.segments) * kCbThreads + threadIdx.x) * 8;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (col >= a.N) return;
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint4 base;
+    if (a.base) base = *reinterpret_cast<const uint4*>(a.base + t * a.base_stride + col * 2);
+    for (int j0 = 0; j0 < a.k; j0 += kCbRows) {
+        uint4 v[kCbRows];
+        float w[kCbRows];
+#pragma unroll
+        for (int j = 0; j < kCbRows; ++j) {
+            w[j] = 0.f;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (j0 + j < a.k) {
+                const int slot = __ldg(a.slots + (long long)t * a.k + j0 + j);
+                if (slot >= 0 && slot < a.M) {
+                    w[j] = __ldg(a.weights + (long long)t * a.k + j0 + j);
+                    v[j] = __ldg(reinterpret_cast<const uint4*>(a.y + slot * a.y_stride + col * 2));
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kCbRows; ++j) add_eight<BF16>(sum, v[j], w[j]);
+    }
+    if (a.base) add_eight<BF16>(sum, base, 1.f);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(sum[2 * i], sum[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t*>(&p);
+        } else {
+            const __half2 p = __floats2half2_rn(sum[2 * i], sum[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+    }
+    *reinterpret_cast<uint4*>(a.out + t * a.out_stride + col * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+}  // namespace
+}  // namespace nq
+
+using namespace nq;
+
+extern "C" {
+
+nq_status nq_moe_route(const void* logits, int dtype, long long stride, const float* bias, int T, int E, int k,
+                       int score, int normalize, float scale, int* ids, float* weights, int* offsets, int* rows,
+                       int* slots, void* stream) {
+    if (dtype != NQ_BF16 && dtype != NQ_FP16 && dtype != NQ_FP32) return NQ_ERR_SHAPE;
+    if (T < 0 || T > kRtMostTokens || E < 1 || E > kMostExperts || k < 1 || k > E || k > kRtMostChosen) return NQ_ERR_SHAPE;
+    if ((score != NQ_SOFTMAX && score != NQ_SIGMOID) || (bias && score != NQ_SIGMOID)) return NQ_ERR_SHAPE;
+    if (stride < E || !(scale > 0.f) || !(scale < INFINITY)) return NQ_ERR_SHAPE;
+    if (T == 1) stride = E;
+    const int el = dtype == NQ_FP32 ? 4 : 2;
+    const long long lb = step_span(T, stride, E) * el, n = (long long)T * k * 4;
+    if (lb < 0) return NQ_ERR_SHAPE;
+    if (!offsets) return NQ_ERR_NULL;
+    if (mis(offsets, 4)) return NQ_ERR_ALIGN;
+    if (T > 0) {
+        if (!logits || !ids || !weights || !rows || !slots) return NQ_ERR_NULL;
+        if (mis(logits, el) || mis(bias, 4) || mis(ids, 4) || mis(weights, 4) || mis(rows, 4) || mis(slots, 4))
+            return NQ_ERR_ALIGN;
+    }
+    const struct {
+        const void* p;
+        long long n;
+    } out[] = {{ids, n}, {weights, n}, {rows, n}, {slots, n}, {offsets, (E + 1) * 4ll}};
+    for (int i = 0; i < 5; ++i) {
+        if (meet(out[i].p, out[i].n, logits, lb) || meet(out[i].p, out[i].n, bias, E * 4ll)) return NQ_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i].p, out[i].n, out[j].p, out[j].n)) return NQ_ERR_ALIAS;
+    }
+    StepDevice d;
+    const int st = step_device(&d);
+    if (st != NQ_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0) return cudaMemsetAsync(offsets, 0, (E + 1) * 4, s) == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+    RouteArgs a;
+    a.logits = logits;
+    a.stride = stride;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.slots = slots;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.scale = scale;
+    a.dtype = dtype;
+    a.sigmoid = score == NQ_SIGMOID;
+    a.normalize = normalize != 0;
+    const cudaError_t e = E <= 32    ? route_launch<1>(a, s, d.pdl)
+                          : E <= 64  ? route_launch<2>(a, s, d.pdl)
+                          : E <= 128 ? route_launch<4>(a, s, d.pdl)
+                          : E <= 256 ? route_launch<8>(a, s, d.pdl)
+                          : E <= 512 ? route_launch<16>(a, s, d.pdl)
+                                     : route_launch<32>(a, s, d.pdl);
+    return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+}
+
+nq_status nq_moe_combine(const void* y, int dtype, long long y_stride, int M, const int* slots, const float* weights,
+                         int T, int k, int N, const void* base, long long base_stride, void* out, long long out_stride,
+                         void* stream) {
+    if (dtype != NQ_BF16 && dtype != NQ_FP16) return NQ_ERR_SHAPE;
+    if (M < 0 || M > kFp8MostRows || T < 0 || T > kRtMostTokens || k < 1 || k > kRtMostChosen) return NQ_ERR_SHAPE;
+    if (N < 8 || N % 8 || N > kFp8MostCols || y_stride < N || out_stride < N || (base && base_stride < N)) return NQ_ERR_SHAPE;
+    if (M <= 1) y_stride = N;                    // between rows: nothing
+    if (T == 1) base_stride = out_stride = N;
+    const long long yb = 2 * step_span(M, y_stride, N), bb = base ? 2 * step_span(T, base_stride, N) : 0;
+    const long long ob = 2 * step_span(T, out_stride, N), n = (long long)T * k * 4;
+    if (yb < 0 || bb < 0 || ob < 0) return NQ_ERR_SHAPE;
+    if (T == 0) return NQ_OK;
+    if ((M > 0 && !y) || !slots || !weights || !out) return NQ_ERR_NULL;
+    if (mis(y, 16) || mis(base, 16) || mis(out, 16) || y_stride % 8 || out_stride % 8 || (base && base_stride % 8) ||
+        mis(slots, 4) || mis(weights, 4))
+        return NQ_ERR_ALIGN;
+    // out may be base itself: each of its elements is read by the thread that writes it
+    const bool same = base == out && base_stride == out_stride;
+    if (meet(out, ob, y, yb) || meet(out, ob, slots, n) || meet(out, ob, weights, n) || (!same && meet(out, ob, base, bb)))
+        return NQ_ERR_ALIAS;
+    StepDevice d;
+    const int st = step_device(&d);
+    if (st != NQ_OK) return st;
+    CombineArgs a;
+    a.y = static_cast<const uint8_t*>(y);
+    a.slots = slots;
+    a.weights = weights;
+    a.base = static_cast<const uint8_t*>(base);
+    a.out = static_cast<uint8_t*>(out);
+    a.y_stride = y_stride * 2;
+    a.base_stride = base_stride * 2;
+    a.out_stride = out_stride * 2;
+    a.M = M;
+    a.T = T;
+    a.k = k;
+    a.N = N;
+    a.segments = (uint32_t)((N / 8 + kCbThreads - 1) / kCbThreads);
+    const long long blocks = (long long)T * a.segments;
+    if (blocks > 0x7FFFFFFFll) return NQ_ERR_SHAPE;
+    auto kern = dtype == NQ_BF16 ? combine_kernel<true> : combine_kernel<false>;
+    return step_launch(kern, dim3((unsigned)blocks), dim3(kCbThreads), 0, reinterpret_cast<cudaStream_t>(stream), d.pdl, 1,
+                       a) == cudaSuccess
+               ? NQ_OK
+               : NQ_ERR_CUDA;
+}
+
+}  // extern "C"

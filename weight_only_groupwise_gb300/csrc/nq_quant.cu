@@ -1,0 +1,144 @@
+// nq_quant.cu -- activations into 8-bit codes with a scale for each 128 columns of a row (nq_quant_fp8):
+//
+//   s[r, b] = max(max over the block of |x| / 448, 2^-126),   c[r, k] = e4m3(x[r, k] / s[r, k / 128])
+//
+// 448 is e4m3's largest value; the floor keeps s normal, so that x / s is at most 448 for any x and a block of zeros
+// needs no case of its own. Bound by memory: x once, a byte an element and 4 / 128 for the scales. Nothing is
+// reused, so a warp takes 1024 columns of a row straight from memory: its lanes have 8 columns of four pairs of
+// blocks, all loads in flight at once, and 16 lanes find a block's largest by shuffles.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "nq.h"
+#include "nq_common.cuh"
+#include "nq_fp8.h"
+#include "nq_step.h"
+
+namespace nq {
+namespace {
+
+constexpr int kQtThreads = 256;
+constexpr int kQtSteps = 4;                      // loads of 8 columns a lane
+constexpr int kQtCols = 32 * 8 * kQtSteps;       // columns of a warp
+
+struct QuantArgs {
+    const uint8_t* x;
+    uint8_t* codes;
+    float* scales;
+    long long x_stride, codes_stride, scale_stride;   // between rows: bytes, bytes, floats
+    int K;
+    uint32_t segments;                           // of kQtCols columns in a row
+    long long total;                             // rows x segments
+};
+
+// 8 columns as floats.
+template <int DTYPE>
+struct Eight {
+    uint4 lo, hi;                                // hi: fp32 only
+    __device__ __forceinline__ void load(const uint8_t* p) {
+        lo = __ldg(reinterpret_cast<const uint4*>(p));
+        if (DTYPE == NQ_FP32) hi = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { lo = hi = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void floats(float (&f)[8]) const {
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DTYPE == NQ_FP32) {
+                f[i] = __uint_as_float(w[i]);
+                f[4 + i] = __uint_as_float(w[4 + i]);
+            } else if constexpr (DTYPE == NQ_BF16) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            } else {
+                const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                f[2 * i] = p.x;
+                f[2 * i + 1] = p.y;
+            }
+        }
+    }
+};
+
+template <int DTYPE>
+__global__ void __launch_bounds__(kQtThreads) quant_kernel(const QuantArgs a) {
+    const long long at = (long long)blockIdx.x * (kQtThreads / 32) + (threadIdx.x >> 5);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (at >= a.total) return;
+    const int lane = threadIdx.x & 31;
+    const long long r = a.segments == 1 ? at : at / a.segments;
+    const int col0 = (int)(at - r * a.segments) * kQtCols + lane * 8;
+    const uint8_t* x = a.x + r * a.x_stride + (long long)col0 * (DTYPE == NQ_FP32 ? 4 : 2);
+    Eight<DTYPE> v[kQtSteps];
+#pragma unroll
+    for (int i = 0; i < kQtSteps; ++i) {
+        if (col0 + i * 256 < a.K)
+            v[i].load(x + i * 256 * (DTYPE == NQ_FP32 ? 4 : 2));
+        else
+            v[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < kQtSteps; ++i) {
+        float f[8];
+        v[i].floats(f);
+        // magnitudes in the order of their bits: a NaN is the largest of all, so that it reaches the scale
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        const float s = fp8_scale(__uint_as_float(m));
+        const int col = col0 + i * 256;
+        if (col < a.K) {
+            uint2 c;
+            c.x = fp8_codes(f[0] / s, f[1] / s, f[2] / s, f[3] / s);
+            c.y = fp8_codes(f[4] / s, f[5] / s, f[6] / s, f[7] / s);
+            *reinterpret_cast<uint2*>(a.codes + r * a.codes_stride + col) = c;
+            if ((lane & 15) == 0) a.scales[r * a.scale_stride + col / kFp8Block] = s;
+        }
+    }
+}
+
+}  // namespace
+}  // namespace nq
+
+using namespace nq;
+
+extern "C" nq_status nq_quant_fp8(const void* x, int dtype, long long x_stride, int rows, int K, void* codes,
+                                  long long codes_stride, float* scales, long long scale_stride, void* stream) {
+    if (dtype != NQ_BF16 && dtype != NQ_FP16 && dtype != NQ_FP32) return NQ_ERR_SHAPE;
+    if (rows < 0 || rows > kFp8MostRows || K < 16 || K > kFp8MostCols || K % 16) return NQ_ERR_SHAPE;
+    const int el = dtype == NQ_FP32 ? 4 : 2, blocks = (K + kFp8Block - 1) / kFp8Block;
+    if (x_stride < K || codes_stride < K || scale_stride < blocks) return NQ_ERR_SHAPE;
+    if (rows == 1) {                             // between rows: nothing
+        x_stride = codes_stride = K;
+        scale_stride = blocks;
+    }
+    const long long xb = step_span(rows, x_stride, K), cb = step_span(rows, codes_stride, K);
+    const long long sb = step_span(rows, scale_stride, blocks);
+    if (xb < 0 || cb < 0 || sb < 0) return NQ_ERR_SHAPE;
+    if (rows == 0) return NQ_OK;
+    if (!x || !codes || !scales) return NQ_ERR_NULL;
+    if (mis(x, 16) || mis(codes, 16) || mis(scales, 4) || x_stride * el % 16 || codes_stride % 16) return NQ_ERR_ALIGN;
+    if (meet(codes, cb, x, xb * el) || meet(scales, sb * 4, x, xb * el) || meet(codes, cb, scales, sb * 4))
+        return NQ_ERR_ALIAS;
+    StepDevice d;
+    const int st = step_device(&d);
+    if (st != NQ_OK) return st;
+    QuantArgs a;
+    a.x = static_cast<const uint8_t*>(x);
+    a.codes = static_cast<uint8_t*>(codes);
+    a.scales = scales;
+    a.x_stride = x_stride * el;
+    a.codes_stride = codes_stride;
+    a.scale_stride = scale_stride;
+    a.K = K;
+    a.segments = (uint32_t)((K + kQtCols - 1) / kQtCols);
+    a.total = (long long)rows * a.segments;
+    const dim3 grid((unsigned)((a.total + kQtThreads / 32 - 1) / (kQtThreads / 32)));
+    auto kern = dtype == NQ_BF16 ? quant_kernel<NQ_BF16> : (dtype == NQ_FP16 ? quant_kernel<NQ_FP16> : quant_kernel<NQ_FP32>);
+    return step_launch(kern, grid, dim3(kQtThreads), 0, reinterpret_cast<cudaStream_t>(stream), d.pdl, 1, a) == cudaSuccess
+               ? NQ_OK
+               : NQ_ERR_CUDA;
+}

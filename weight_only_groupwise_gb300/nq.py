@@ -113,6 +113,16 @@ def lib() -> ctypes.CDLL:
         L.nq_attn_paged.argtypes = [P, LL, P, P, LL, I, P, P, I, I, I, F, I, I, I, P, LL, P]
         L.nq_attn_reserve.argtypes = []
         L.nq_sample.argtypes = [P, I, LL, P, LL, I, I, P, P, P, P, P, P]
+        L.nq_quant_fp8.argtypes = [P, I, LL, I, I, P, LL, P, LL, P]
+        L.nq_gemm_fp8.argtypes = [P, P, P, I, I, P]
+        L.nq_swiglu_fp8.argtypes = [P, P, P, P, I, I, P]
+        L.nq_gemm_fp8_experts.argtypes = [P, P, I, P, I, P, P, I, I, P]
+        L.nq_swiglu_fp8_experts.argtypes = [P, P, I, P, I, P, P, P, I, I, P]
+        L.nq_moe_route.argtypes = [P, I, LL, P, I, I, I, I, I, F, P, P, P, P, P, P]
+        L.nq_moe_combine.argtypes = [P, I, LL, I, P, P, I, I, I, P, LL, P, LL, P]
+        for f in ("nq_quant_fp8", "nq_gemm_fp8", "nq_swiglu_fp8", "nq_gemm_fp8_experts", "nq_swiglu_fp8_experts",
+                  "nq_moe_route", "nq_moe_combine"):
+            getattr(L, f).restype = I
         for f in ("nq_sample", "nq_page_tables", "nq_kv_append", "nq_attn_paged", "nq_attn_reserve"):
             getattr(L, f).restype = I
         for f in ("nq_pack_q4", "nq_pack_q5", "nq_gemm_q4", "nq_gemm_q5", "nq_gemm_q4_noalloc", "nq_swiglu_q4",
@@ -608,6 +618,173 @@ def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, 
     return out
 
 
+# ---------------------------------------------------------------- 8-bit products and experts
+
+_E4M3 = torch.float8_e4m3fn
+_F8_ROWS = struct.Struct("PPqqi4x")      # struct nq_fp8_rows
+_F8_WEIGHT = struct.Struct("PPqqqq")     # struct nq_fp8_weight
+_F8_OUT = struct.Struct("PPqqi4x")       # struct nq_fp8_out
+_F8_DTYPES = {torch.bfloat16: 0, torch.float16: 1, _E4M3: 3}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def quant_fp8(x, out=None, stream=None):
+    """x [rows][K] (bfloat16, float16 or float32) as e4m3 codes [rows][K] and float32 scales
+    [rows][ceil(K / 128)], one for each 128 columns of a row (nq_quant_fp8). `out`: (codes, scales), to be reused."""
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
+        raise ValueError("x must be bfloat16, float16 or float32")
+    rows = x.shape[0]
+    xp, K, stride = _rows(x, "x", x.dtype, rows)
+    if out is None:
+        out = (torch.empty((rows, K), dtype=_E4M3, device=x.device),
+               torch.empty((rows, -(-K // 128)), dtype=torch.float32, device=x.device))
+    codes, scales = out
+    cp, K_c, cs = _rows(codes, "codes", _E4M3, rows)
+    sp, blocks, ss = _rows(scales, "scales", torch.float32, rows)
+    if K_c != K or blocks != -(-K // 128):
+        raise ValueError("codes must have x's shape and scales a column for each 128 of it")
+    _check(lib().nq_quant_fp8(xp, dtype, stride, rows, K, cp, cs, sp, ss, _raw_stream(stream)))
+    return out
+
+
+def _fp8_weight(codes, scales, E, name: str):
+    """(struct nq_fp8_weight, N, K) of codes [N][K] and scales [ceil(N / 128)][ceil(K / 128)], with experts (E not
+    None) [E][..][..] both."""
+    try:
+        if codes.dtype is _E4M3 and scales.dtype is torch.float32 and codes.is_cuda and scales.is_cuda:
+            shape, block, st, ss = codes.shape, scales.shape, codes.stride(), scales.stride()
+            if E is None:
+                (N, K), (nb, kb), e, se = shape, block, 0, 0
+            else:
+                (n, N, K), (m, nb, kb), e, se = shape, block, st[0], ss[0]
+                if n != E or m != E:
+                    raise ValueError
+            if nb == -(-N // 128) and kb == -(-K // 128) and (st[-1] == 1 or K <= 1) and (ss[-1] == 1 or kb <= 1):
+                return _F8_WEIGHT.pack(codes.data_ptr(), scales.data_ptr(), st[-2], e, ss[-2], se), N, K
+    except (AttributeError, ValueError):
+        pass
+    raise ValueError(f"{name} must be CUDA tensors of float8_e4m3fn codes {'' if E is None else '[experts]'}[N][K] and float32 "
+                     "scales, one for each 128 x 128, contiguous along K")
+
+
+def _fp8(fn, xq, xs, weights, dtype, out, stream, experts=None):
+    """The four products; experts: (offsets, rows)."""
+    x_rows = xq.shape[0]
+    xp, K, stride = _rows(xq, "xq", _E4M3, x_rows)
+    sp, kb, ss = _rows(xs, "xs", torch.float32, x_rows)
+    E, M = None, x_rows
+    if experts is not None:
+        offsets, rows = experts
+        E = offsets.numel() - 1
+        offsets = _flat(offsets, "offsets", torch.int32, E + 1)
+        if rows is not None:
+            M = rows.numel()
+            rows = _flat(rows, "rows", torch.int32, M)
+    packed = []
+    for codes, scales in weights:
+        w, N, K_w = _fp8_weight(codes, scales, E, "the weights")
+        if K_w != K or (packed and N != width):
+            raise ValueError("the weights must have xq's K, and the same N")
+        width = N
+        packed.append(w)
+    if kb != -(-K // 128):
+        raise ValueError("xs must have a column for each 128 of xq")
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=xq.device)
+        if dtype is _E4M3:
+            out = (out, torch.empty((M, -(-N // 128)), dtype=torch.float32, device=xq.device))
+    if dtype is _E4M3:
+        yp, N_y, ys = _rows(out[0], "out", dtype, M)
+        yc, nb, yss = _rows(out[1], "out's scales", torch.float32, M)
+        if nb != -(-N // 128):
+            raise ValueError("out's scales must have a column for each 128 of it")
+    else:
+        yp, N_y, ys = _rows(out, "out", dtype, M)
+        yc = yss = 0
+    if N_y != N:
+        raise ValueError("out must have a column for each row of the weights")
+    x = _F8_ROWS.pack(xp, sp, stride, ss, x_rows)
+    y = _F8_OUT.pack(yp, yc, ys, yss, _F8_DTYPES.get(dtype, -1))
+    if experts is None:
+        _check(fn(x, *packed, y, K, N, _raw_stream(stream)))
+    else:
+        _check(fn(x, rows, M, offsets, E, *packed, y, K, N, _raw_stream(stream)))
+    return out
+
+
+def gemm_fp8(xq, xs, wq, ws, dtype=torch.bfloat16, out=None, stream=None):
+    """y [rows][N] (bfloat16 or float16) = x w^T of e4m3 codes with block scales (nq_gemm_fp8): xq [rows][K] with
+    float32 xs [rows][ceil(K / 128)] (quant_fp8), wq [N][K] with ws [ceil(N / 128)][ceil(K / 128)]."""
+    return _fp8(lib().nq_gemm_fp8, xq, xs, ((wq, ws),), dtype, out, stream)
+
+
+def swiglu_fp8(xq, xs, wg, sg, wu, su, dtype=torch.bfloat16, out=None, stream=None):
+    """silu(x wg^T) * (x wu^T), weights as in gemm_fp8 (nq_swiglu_fp8). dtype float8_e4m3fn returns (codes, scales), quantised
+    as quant_fp8 does: what the down projection takes."""
+    return _fp8(lib().nq_swiglu_fp8, xq, xs, ((wg, sg), (wu, su)), dtype, out, stream)
+
+
+def gemm_fp8_experts(xq, xs, wq, ws, offsets, rows=None, dtype=torch.bfloat16, out=None, stream=None):
+    """gemm_fp8 with a weight for each expert: row i, offsets[e] <= i < offsets[e + 1] (int32 [E + 1], on the GPU),
+    is row rows[i] of x (int32; None: i) times wq[e] [E][N][K] with ws [E][..][..] (nq_gemm_fp8_experts)."""
+    return _fp8(lib().nq_gemm_fp8_experts, xq, xs, ((wq, ws),), dtype, out, stream, (offsets, rows))
+
+
+def swiglu_fp8_experts(xq, xs, wg, sg, wu, su, offsets, rows=None, dtype=torch.bfloat16, out=None, stream=None):
+    """swiglu_fp8 with gate and up weights for each expert, rows as in gemm_fp8_experts (nq_swiglu_fp8_experts)."""
+    return _fp8(lib().nq_swiglu_fp8_experts, xq, xs, ((wg, sg), (wu, su)), dtype, out, stream, (offsets, rows))
+
+
+def moe_route(logits, k: int, bias=None, score: str = "softmax", normalize: bool = True, scale: float = 1.0, out=None,
+              stream=None):
+    """Each token's k experts from logits [T][E] (nq_moe_route). score "softmax" or "sigmoid"; bias float32 [E]
+    (sigmoid: choose by score + bias); normalize: the weights sum to `scale`. Returns (ids [T][k], weights [T][k] float32, offsets
+    [E + 1], rows [T * k], slots [T][k]), int32: `out`, to be reused."""
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None or score not in _SCORES:
+        raise ValueError("logits must be bfloat16, float16 or float32, and score softmax or sigmoid")
+    T, i32 = logits.shape[0], torch.int32
+    lp, E, stride = _rows(logits, "logits", logits.dtype, T)
+    if out is None:
+        dev = logits.device
+        out = (torch.empty((T, k), dtype=i32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev),
+               torch.empty(E + 1, dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev),
+               torch.empty((T, k), dtype=i32, device=dev))
+    ids, weights, offsets, rows, slots = out
+    n = T * k
+    _check(lib().nq_moe_route(lp, dtype, stride, None if bias is None else _flat(bias, "bias", torch.float32, E), T, E, k,
+                              _SCORES[score], int(normalize), scale, _flat(ids, "ids", i32, n),
+                              _flat(weights, "weights", torch.float32, n), _flat(offsets, "offsets", i32, E + 1),
+                              _flat(rows, "rows", i32, n), _flat(slots, "slots", i32, n), _raw_stream(stream)))
+    return out
+
+
+def moe_combine(y, slots, weights, base=None, out=None, stream=None):
+    """out [T][N] = base + sum_j weights[:, j] * y[slots[:, j]] (nq_moe_combine): y [rows][N] (bfloat16 or
+    float16), slots int32 and weights float32 [T][k] as moe_route gives them, base [T][N] or None. out may be base."""
+    dt = y.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError("y must be bfloat16 or float16")
+    T, k = slots.shape
+    M = y.shape[0]
+    yp, N, ys = _rows(y, "y", dt, M)
+    bp, bs = None, 0
+    if base is not None:
+        bp, N_b, bs = _rows(base, "base", dt, T)
+        if N_b != N:
+            raise ValueError("base must have y's columns")
+    if out is None:
+        out = torch.empty((T, N), dtype=dt, device=y.device)
+    op, N_o, os_ = _rows(out, "out", dt, T)
+    if N_o != N:
+        raise ValueError("out must have y's columns")
+    _check(lib().nq_moe_combine(yp, _DTYPES[dt], ys, M, _flat(slots, "slots", torch.int32, T * k),
+                                _flat(weights, "weights", torch.float32, T * k), T, k, N, bp, bs, op, os_,
+                                _raw_stream(stream)))
+    return out
+
+
 # ---------------------------------------------------------------- runtime / plan
 
 def reserve(T_max: int, K_max: int, N_max: int) -> None:
@@ -714,3 +891,6 @@ nq_reserve, nq_device_error, nq_shutdown, nq_wait_limit = reserve, device_error,
 nq_plan_info, nq_plan_segments = plan_info, plan_segments
 nq_page_tables, nq_kv_append, nq_attn_paged, nq_attn_reserve = page_tables, kv_append, attn_paged, attn_reserve
 nq_sample = sample
+nq_quant_fp8, nq_gemm_fp8, nq_swiglu_fp8 = quant_fp8, gemm_fp8, swiglu_fp8
+nq_gemm_fp8_experts, nq_swiglu_fp8_experts = gemm_fp8_experts, swiglu_fp8_experts
+nq_moe_route, nq_moe_combine = moe_route, moe_combine
