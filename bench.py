@@ -39,7 +39,7 @@ METRIC = "µs/call and achieved HBM GB/s (% of roofline) for Q4/Q5 skinny GEMM, 
 MAX_T = 64
 # What decides a projection's DRAM traffic: its kernels, their work split, the tensor maps and the choice of
 # kernel, grid and cluster on the host. All sources but those of the serving step's own kernels.
-STEP_SOURCES = {"nq_attn.cu", "nq_attn.cuh", "nq_fp8.cu", "nq_fp8.h", "nq_moe.cu", "nq_pages.cu", "nq_quant.cu", "nq_sample.cu",
+STEP_SOURCES = {"nq_attn.cu", "nq_attn.cuh", "nq_fp8.cu", "nq_fp8.cuh", "nq_fp8.h", "nq_moe.cu", "nq_pages.cu", "nq_quant.cu", "nq_sample.cu",
                 "nq_step.h"}
 KERNEL_SOURCES = sorted(f for f in os.listdir(os.path.join(ROOT, "weight_only_groupwise_gb300", "csrc"))
                         if f.endswith((".cu", ".cuh", ".h")) and f not in STEP_SOURCES)

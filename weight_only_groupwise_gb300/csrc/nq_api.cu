@@ -10,6 +10,7 @@
 
 #include "nq.h"
 #include "nq_launch.h"
+#include "nq_fp8.h"
 #include "nq_step.h"
 
 using namespace nq;
@@ -1027,8 +1028,12 @@ nq_status nq_device_error(void) {
     if (st != NQ_OK) return st;
     if (cudaDeviceSynchronize() != cudaSuccess) return NQ_ERR_CUDA;
     // The fixed scratch of nq_gemm_q4_noalloc has its own error word.
-    const nq_status st_static = noalloc_take_error(dev);
+    nq_status st_static = noalloc_take_error(dev);
     if (st_static == NQ_ERR_CUDA) return st_static;
+    // So have the 8-bit products.
+    const nq_status st_fp8 = fp8_take_error(dev);
+    if (st_fp8 == NQ_ERR_CUDA) return st_fp8;
+    if (st_fp8 != NQ_OK) st_static = st_fp8;
     std::lock_guard<std::mutex> lk(g_mu);
     int attn_err = 0;
     if (d->attn_ws) {

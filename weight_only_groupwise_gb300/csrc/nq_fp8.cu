@@ -1,118 +1,102 @@
-// nq_fp8.cu -- products of 8-bit codes with block scales: dense and by expert, plain and SwiGLU.
+// nq_fp8.cu -- host side of the products of 8-bit codes with block scales (nq_fp8.cuh), dense and by expert, plain and
+// SwiGLU: argument checks, tensor maps, the choice of kernel.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cstdlib>
+#include <mutex>
+
 #include "nq.h"
-#include "nq_common.cuh"
-#include "nq_fp8.h"
+#include "nq_fp8.cuh"
 #include "nq_step.h"
 
 namespace nq {
 namespace {
 
-constexpr int kSimpleRows = 32, kSimpleThreads = 256, kSimpleK = 32;
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-struct Fp8Args {
-    const uint8_t* x;
-    const float* xs;
-    long long x_stride, xs_stride;
-    int x_rows;
-    const int* rows;                             // NULL: row i
-    const int* offsets;                          // NULL: one group of M rows
-    int E, M, K, N;
-    const uint8_t* w[2];
-    const float* ws[2];
-    long long w_row[2], w_expert[2], ws_row[2], ws_expert[2];
-    uint8_t* y;
-    float* ys;
-    long long y_stride, ys_stride;               // elements
-    int dtype;
-    bool glu;
-};
-
-__device__ __forceinline__ float e4m3_float(uint8_t c) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-    return __half2float(__ushort_as_half((uint16_t)h));
+EncodeFn encode_tiled() {
+    static std::once_flag once;
+    static EncodeFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(p);
+    });
+    return fn;
 }
 
-// A block 32 rows x 128 columns; a thread a row's 16 columns.
-__global__ void __launch_bounds__(kSimpleThreads) fp8_simple_kernel(const Fp8Args a) {
-    __shared__ float sx[kSimpleRows][kSimpleK + 1], sw[2][128][kSimpleK + 1];
-    grid_launch_dependents();
-    grid_dependency_wait();
-    int tile = blockIdx.y, e = 0, r0 = 0, r1 = a.M;
-    if (a.offsets) {
-        for (;; ++e) {
-            if (e == a.E) return;
-            r0 = min(max(a.offsets[e], 0), a.M);
-            r1 = min(max(a.offsets[e + 1], r0), a.M);
-            const int n = (r1 - r0 + kSimpleRows - 1) / kSimpleRows;
-            if (tile < n) break;
-            tile -= n;
-        }
+// Rows of codes as a 2-D map {K, rows}: boxes of 128 codes (a 128-byte swizzled row, zeros past K) of `box` rows.
+bool encode_rows(CUtensorMap* map, const void* codes, long long stride, int K, int rows, int box) {
+    const EncodeFn fn = encode_tiled();
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
+    const cuuint32_t boxes[2] = {kFp8Block, (cuuint32_t)box}, each[2] = {1, 1};
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, boxes, each,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Weights as a 3-D map {K, N, E}; a box is 128 codes of `box` rows of one expert.
+bool encode_weights(CUtensorMap* map, const nq_fp8_weight& w, int K, int N, int E, int box) {
+    const EncodeFn fn = encode_tiled();
+    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)E};
+    const cuuint64_t strides[2] = {(cuuint64_t)w.row_stride, (cuuint64_t)w.expert_stride};
+    const cuuint32_t boxes[3] = {kFp8Block, (cuuint32_t)box, 1}, each[3] = {1, 1, 1};
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w.codes), dims, strides, boxes, each,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The error word of bounded waits: one in the memory of each device that the library is loaded on.
+__device__ int g_error;
+constexpr int kDevices = 64;
+std::mutex g_lock;
+int* g_error_at[kDevices] = {};
+
+int* error_word(int dev) {
+    if (dev < 0 || dev >= kDevices) return nullptr;
+    std::lock_guard<std::mutex> lk(g_lock);
+    if (!g_error_at[dev]) {
+        void* p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_error) == cudaSuccess) g_error_at[dev] = static_cast<int*>(p);
     }
-    r0 += tile * kSimpleRows;
-    const int n0 = blockIdx.x * 128, tid = threadIdx.x, row = tid >> 3, c0 = tid & 7;
-    const int live = min(kSimpleRows, r1 - r0);
-    float acc[2][16] = {};
-    auto source = [&](int r) { return r < live ? (a.rows ? a.rows[r0 + r] : r0 + r) : -1; };
-    const int mine = source(row);
-    const bool there = mine >= 0 && mine < a.x_rows;
-    for (int b0 = 0; b0 < a.K; b0 += 128) {
-        const float s = there ? a.xs[mine * a.xs_stride + b0 / 128] : 0.f;
-        float part[2][16] = {};
-        for (int k0 = b0; k0 < min(a.K, b0 + 128); k0 += kSimpleK) {
-            __syncthreads();
-            for (int i = tid; i < kSimpleRows * kSimpleK; i += kSimpleThreads) {
-                const int r = i / kSimpleK, k = k0 + i % kSimpleK, at = source(r);
-                sx[r][i % kSimpleK] = at >= 0 && at < a.x_rows && k < a.K ? e4m3_float(a.x[at * a.x_stride + k]) : 0.f;
-            }
-            for (int g = 0; g <= (int)a.glu; ++g)
-                for (int i = tid; i < 128 * kSimpleK; i += kSimpleThreads) {
-                    const int n = i / kSimpleK, k = k0 + i % kSimpleK;
-                    sw[g][n][i % kSimpleK] = n0 + n < a.N && k < a.K
-                                                 ? e4m3_float(a.w[g][e * a.w_expert[g] + (n0 + n) * a.w_row[g] + k])
-                                                 : 0.f;
-                }
-            __syncthreads();
-            for (int k = 0; k < kSimpleK; ++k)
-                for (int g = 0; g <= (int)a.glu; ++g)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) part[g][i] = fmaf(sx[row][k], sw[g][c0 + 8 * i][k], part[g][i]);
-        }
-        for (int g = 0; g <= (int)a.glu; ++g) {
-            const float f = s * a.ws[g][e * a.ws_expert[g] + (n0 / 128) * a.ws_row[g] + b0 / 128];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[g][i] = fmaf(f, part[g][i], acc[g][i]);
-        }
+    return g_error_at[dev];
+}
+
+// A launch with as much shared memory as the kernel asks for (allowed once a device and thread).
+template <typename Kern>
+cudaError_t fp8_launch(Kern kern, int& set_for_device, int dev, int blocks, int threads, int smem, cudaStream_t stream,
+                       bool pdl, const Fp8Args& a) {
+    if (set_for_device != dev) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        if (e != cudaSuccess) return e;
+        set_for_device = dev;
     }
-    float m = 0.f;
-    if (a.glu)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            acc[0][i] = silu_mul(acc[0][i], acc[1][i]);
-            if (n0 + c0 + 8 * i < a.N)
-                m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(acc[0][i]) & 0x7FFFFFFFu));
-        }
-    float q = 1.f;
-    if (a.dtype == NQ_E4M3) {
-        for (int d = 4; d > 0; d >>= 1)
-            m = __uint_as_float(max(__float_as_uint(m), __shfl_xor_sync(0xFFFFFFFFu, __float_as_uint(m), d)));
-        q = fp8_scale(m);
-        if (row < live && c0 == 0) a.ys[(r0 + row) * a.ys_stride + n0 / 128] = q;
-    }
-    if (row >= live) return;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int n = n0 + c0 + 8 * i;
-        if (n >= a.N) continue;
-        const long long at = (r0 + row) * a.y_stride + n;
-        if (a.dtype == NQ_E4M3)
-            a.y[at] = (uint8_t)fp8_codes(acc[0][i] / q, 0.f, 0.f, 0.f);
-        else
-            reinterpret_cast<uint16_t*>(a.y)[at] =
-                a.dtype == NQ_BF16 ? bf16_bits_rn(acc[0][i]) : __half_as_ushort(__float2half_rn(acc[0][i]));
+    return step_launch(kern, dim3(blocks), dim3(threads), (size_t)smem, stream, pdl, 1, a);
+}
+template <bool GLU>
+cudaError_t launch_rows(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
+    using Geo = Fp8RowsGeo<GLU>;
+    static thread_local int set = -1;
+    return fp8_launch(fp8_rows_kernel<GLU>, set, dev, blocks, Geo::kThreads, Geo::smem(a.c.E), stream, pdl, a);
+}
+template <int BN, bool GLU>
+cudaError_t launch_cols(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
+    using Geo = Fp8ColsGeo<BN, GLU>;
+    static thread_local int set = -1;
+    return fp8_launch(fp8_cols_kernel<BN, GLU>, set, dev, blocks, Geo::kThreads, Geo::smem(a.c.E), stream, pdl, a);
+}
+template <bool GLU>
+cudaError_t launch_cols_of(int bn, const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
+    switch (bn) {
+        case 16: return launch_cols<16, GLU>(a, dev, blocks, stream, pdl);
+        case 32: return launch_cols<32, GLU>(a, dev, blocks, stream, pdl);
+        case 64: return launch_cols<64, GLU>(a, dev, blocks, stream, pdl);
+        default: return launch_cols<128, GLU>(a, dev, blocks, stream, pdl);
     }
 }
 
@@ -157,7 +141,7 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
         if (N == 1) v[g].row_stride = K;         // between one row and the next: nothing
         if (nb == 1) v[g].scale_row_stride = kb;
         if (E == 1) {
-            v[g].expert_stride = (long long)K;
+            v[g].expert_stride = (K + 15) / 16 * 16;
             v[g].scale_expert_stride = kb;
         }
         if (v[g].row_stride < K || v[g].scale_row_stride < kb || v[g].expert_stride < 0 || v[g].scale_expert_stride < 0)
@@ -187,44 +171,78 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     StepDevice d;
     const int st = step_device(&d);
     if (st != NQ_OK) return st;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return NQ_ERR_CUDA;
     Fp8Args a;
-    a.x = static_cast<const uint8_t*>(x->codes);
-    a.xs = x->scales;
-    a.x_stride = xst;
-    a.xs_stride = xss;
-    a.x_rows = x->rows;
-    a.rows = rows;
-    a.offsets = offsets;
-    a.E = E;
-    a.M = M;
-    a.K = K;
-    a.N = N;
+    Fp8Call& c = a.c;
+    c.err = error_word(dev);
+    if (!c.err) return NQ_ERR_CUDA;
+    c.xs = x->scales;
+    c.rows = rows;
+    c.offsets = offsets;
     for (int g = 0; g < 2; ++g) {
-        a.w[g] = static_cast<const uint8_t*>(v[g].codes);
-        a.ws[g] = v[g].scales;
-        a.w_row[g] = v[g].row_stride;
-        a.w_expert[g] = v[g].expert_stride;
-        a.ws_row[g] = v[g].scale_row_stride;
-        a.ws_expert[g] = v[g].scale_expert_stride;
+        c.ws[g] = v[g].scales;
+        c.ws_row[g] = v[g].scale_row_stride;
+        c.ws_expert[g] = v[g].scale_expert_stride;
     }
-    a.y = static_cast<uint8_t*>(y->data);
-    a.ys = y->scales;
-    a.y_stride = yst;
-    a.ys_stride = yss;
-    a.dtype = y->dtype;
-    a.glu = glu;
-    const dim3 grid((N + 127) / 128, (M + kSimpleRows - 1) / kSimpleRows + (experts ? E : 0));
-    if (grid.y > 65535) return NQ_ERR_SHAPE;
-    return step_launch(fp8_simple_kernel, grid, dim3(kSimpleThreads), 0, reinterpret_cast<cudaStream_t>(stream), d.pdl, 1,
-                       a) == cudaSuccess
-               ? NQ_OK
-               : NQ_ERR_CUDA;
+    c.xs_stride = xss;
+    c.y = static_cast<uint8_t*>(y->data);
+    c.ys = y->scales;
+    c.y_stride = yst;
+    c.ys_stride = yss;
+    c.x_rows = x->rows;
+    c.x_past = x->rows > 0 ? x->rows : 1;
+    c.E = E;
+    c.M = M;
+    c.K = K;
+    c.N = N;
+    c.dtype = y->dtype;
+    c.wide = !mis(y->data, 32) && yst % 16 == 0;
+    c.quads = !mis(x->scales, 16) && xss % 4 == 0;
+    c.wait_ns = d.wait_ns;
+    const int each = (M + E - 1) / E;            // rows a group, on average
+    int bn = each <= 12 ? 16 : each <= 24 ? 32 : each <= 48 ? 64 : 128;
+    if (!experts) bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    bool few = each <= 128;
+    if (const char* f = getenv("NQ_F8")) {
+        few = atoi(f) > 0;
+        if (few) bn = atoi(f);
+    }
+    // a map needs a row; of none, any memory that is there
+    const void* codes_at = x->rows > 0 ? x->codes : v[0].codes;
+    if (!encode_rows(&a.xmap, codes_at, x->rows > 1 ? xst : K, K, c.x_past, rows ? 1 : (few ? bn : kF8Tile))) return NQ_ERR_CUDA;
+    for (int g = 0; g <= (int)glu; ++g)
+        if (!encode_weights(&a.wmap[g], v[g], K, N, E, few || glu ? kF8Tile : 256)) return NQ_ERR_CUDA;
+    if (!glu) a.wmap[1] = a.wmap[0];
+    // a block an SM, or one a tile where the tiles cannot be more
+    const int wide = few || glu ? kF8Tile : 256, high = few ? bn : kF8Tile;
+    const long long most = (long long)((N + wide - 1) / wide) * (experts ? (M + high - 1) / high + (E < M ? E : M) : (M + high - 1) / high);
+    const int blocks = (int)(most < d.sms ? most : d.sms);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = few ? (glu ? launch_cols_of<true>(bn, a, dev, blocks, s, d.pdl) : launch_cols_of<false>(bn, a, dev, blocks, s, d.pdl))
+                              : (glu ? launch_rows<true>(a, dev, blocks, s, d.pdl) : launch_rows<false>(a, dev, blocks, s, d.pdl));
+    return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
 }  // namespace
 }  // namespace nq
 
 using namespace nq;
+
+int nq::fp8_take_error(int dev) {
+    int* at = nullptr;
+    {
+        if (dev < 0 || dev >= kDevices) return NQ_OK;
+        std::lock_guard<std::mutex> lk(g_lock);
+        at = g_error_at[dev];
+    }
+    if (!at) return NQ_OK;                       // nothing has run there
+    int err = 0;
+    if (cudaMemcpy(&err, at, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return NQ_ERR_CUDA;
+    if (err == 0) return NQ_OK;
+    if (cudaMemset(at, 0, sizeof(int)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return NQ_ERR_CUDA;
+    return NQ_ERR_TIMEOUT;
+}
 
 extern "C" {
 
