@@ -82,13 +82,13 @@ template <bool GLU>
 cudaError_t launch_rows(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
     using Geo = Fp8RowsGeo<GLU>;
     static thread_local int set = -1;
-    return fp8_launch(fp8_rows_kernel<GLU>, set, dev, blocks, Geo::kThreads, Geo::smem(a.c.E), stream, pdl, a);
+    return fp8_launch(fp8_rows_kernel<GLU>, set, dev, blocks, kF8Threads, Geo::smem(a.c.E), stream, pdl, a);
 }
 template <int BN, bool GLU>
 cudaError_t launch_cols(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
     using Geo = Fp8ColsGeo<BN, GLU>;
     static thread_local int set = -1;
-    return fp8_launch(fp8_cols_kernel<BN, GLU>, set, dev, blocks, Geo::kThreads, Geo::smem(a.c.E), stream, pdl, a);
+    return fp8_launch(fp8_cols_kernel<BN, GLU>, set, dev, blocks, kF8Threads, Geo::smem(a.c.E), stream, pdl, a);
 }
 template <bool GLU>
 cudaError_t launch_cols_of(int bn, const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {

@@ -29,6 +29,11 @@ namespace nq {
 
 constexpr int kF8Epilogue = 8;                   // epilogue warps: 0..7, quarter = warp % 4, half = warp / 4
 constexpr int kF8Producer = 8, kF8Mma = 9, kF8Scales = 10;
+constexpr int kF8Threads = 12 * 32;              // (warp 11 only gives its registers away)
+// Registers a thread: a block begins with 168; warps 8..11 hand theirs to the epilogue's 128 sums and 64 loads:
+// 256 x 216 + 128 x 72 = 384 x 168.
+constexpr int kF8EpilogueRegs = 216, kF8OtherRegs = 72;
+static_assert(256 * kF8EpilogueRegs + 128 * kF8OtherRegs == kF8Threads * 168, "registers of a block");
 constexpr int kF8MaxStages = 16;
 constexpr int kF8Row = 128;                      // bytes (codes) of a stage's row: one block of K, one swizzled row
 constexpr int kF8Tile = 128;                     // rows of a block's MMA operand A
@@ -59,6 +64,15 @@ struct alignas(64) Fp8Args {
 };
 
 // ---------------------------------------------------------------- instructions
+
+template <int n>
+__device__ __forceinline__ void regs_more() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
+}
+template <int n>
+__device__ __forceinline__ void regs_fewer() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
+}
 
 __device__ __forceinline__ void f8_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate, bool issue) {
@@ -240,6 +254,20 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Call& c, const Fp8Groups& g
     return o;
 }
 
+// A producer lane's four rows of x, and how many lanes have rows of the tile (0: x is not gathered). A row that x has
+// not is past the last, which reads as zeros; the last lane's rows behind the tile's repeat one that is there (a
+// gather of rows outside takes several times as long: 128 rows of which one is in the tile, 2.9 us a block of K).
+__device__ __forceinline__ int f8_gather_rows(const Fp8Call& c, const Fp8Tile& tile, int (&at)[4]) {
+    if (!c.rows) return 0;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int s = __ldg(c.rows + tile.row0 + min(4 * lane + i, tile.rows - 1));
+        at[i] = s >= 0 && s < c.x_rows ? s : c.x_past;
+    }
+    return (tile.rows + 3) / 4;
+}
+
 // ---------------------------------------------------------------- many rows a group
 
 template <bool GLU>
@@ -248,14 +276,13 @@ struct Fp8RowsGeo {
     static constexpr int kOut = GLU ? 128 : 256; // columns of the result
     static constexpr int kStageBytes = (kF8Tile + kCols) * kF8Row;
     static constexpr int kStages = 4;
-    static constexpr int kThreads = 10 * 32;
     static constexpr int kTurnBytes = GLU ? kF8Epilogue * 32 * 34 * 2 : kF8Epilogue * 32 * 34 * 2;  // a warp's 32 x 32 results
     static constexpr int kCtrlBytes = 512 + 1024 + kTurnBytes;
     static int smem(int E) { return 1024 + kStages * kStageBytes + kCtrlBytes + f8_group_bytes(E); }
 };
 
 template <bool GLU>
-__global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(const __grid_constant__ Fp8Args a) {
+__global__ void __launch_bounds__(kF8Threads, 1) fp8_rows_kernel(const __grid_constant__ Fp8Args a) {
     using Geo = Fp8RowsGeo<GLU>;
     constexpr int kStages = Geo::kStages;
     const Fp8Call& c = a.c;
@@ -301,6 +328,9 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
     tc_fence_after();
     const uint32_t tmem = (uint32_t)flags[3];
 
+    // (each branch begins with its own count: where the paths met again, everything would have to fit the smaller)
+    if (warp >= kF8Epilogue) {
+        regs_fewer<kF8OtherRegs>();
     if (warp == kF8Producer) {
         // ------------------------------------------------------------ copies
         int seq = 0, e = 0;
@@ -308,15 +338,8 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
         for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
             const Fp8Tile tile = fp8_tile(c, groups, t, e, kF8Tile, cols, false);
             e = tile.e;
-            int at[4];                           // gather: this lane's four rows
-            if (c.rows) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 4 * lane + i;
-                    const int s = r < tile.rows ? __ldg(c.rows + tile.row0 + r) : -1;
-                    at[i] = s >= 0 && s < c.x_rows ? s : c.x_past;   // past the last: zeros
-                }
-            }
+            int at[4];
+            const int fours = f8_gather_rows(c, tile, at);
             for (int kb = 0; kb < KB && ok; ++kb, ++seq) {
                 const int st = seq % kStages;
                 if (seq >= kStages) ok = mbar_wait(empty0 + 8 * st, ((seq / kStages) - 1) & 1, flags, err, wait_ns);
@@ -324,7 +347,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
                 if (!ok) break;
                 const uint32_t xa = smem_u32(ring + st * Geo::kStageBytes), wa = xa + kF8Tile * kF8Row, bar = full0 + 8 * st;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, (uint32_t)Geo::kStageBytes);
+                    mbar_arrive_expect_tx(bar, (uint32_t)(Geo::kCols * kF8Row + (c.rows ? fours * 4 : kF8Tile) * kF8Row));
                     if (GLU) {
                         tma_load_3d(wa, &a.wmap[0], kb * kFp8Block, tile.col * 128, tile.e, bar);
                         tma_load_3d(wa + 128 * kF8Row, &a.wmap[1], kb * kFp8Block, tile.col * 128, tile.e, bar);
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
                     if (!c.rows) tma_load_2d(xa, &a.xmap, kb * kFp8Block, tile.row0, bar);
                 }
                 __syncwarp();
-                if (c.rows) tma_gather4(xa + 4 * lane * kF8Row, &a.xmap, kb * kFp8Block, at, bar);
+                if (lane < fours) tma_gather4(xa + 4 * lane * kF8Row, &a.xmap, kb * kFp8Block, at, bar);
             }
         }
         if (!ok)
@@ -367,8 +390,10 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
         }
         tc_commit(done, leader);                 // every MMA has completed before TMEM can be freed
         mbar_wait_drain(done, 0, kDrainNs);
+    }
     } else {
         // ------------------------------------------------------------ epilogue
+        regs_more<kF8EpilogueRegs>();
         // Thread: a row and 128 columns of D (GLU: 64 of gate and the same 64 of up). The row's scales are fetched four
         // blocks ahead, the next tile's first ones during this tile's last blocks.
         const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
@@ -449,18 +474,22 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
                 ok = mbar_wait(tfull0 + 8 * buf, (seq >> 1) & 1, flags, err, wait_ns);
                 tc_fence_after();
                 const uint32_t base = lane_base + 256 * buf + col0;
+                // 32 columns at a time (GLU: two of gate, two of up), the next ones on their way during the sums
+                uint32_t v[2][32];
+                f8_ld<32>(base, v[0]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {    // 32 columns; GLU: two of gate, two of up
-                    uint32_t v[32];
-                    f8_ld<32>(base + (GLU ? (i >> 1) * 128 + (i & 1) * 32 : i * 32), v);
-                    f8_wait_ld<32>(v);
-                    if (i == 3) {
+                for (int i = 0; i < 4; ++i) {
+                    f8_wait_ld<32>(v[i & 1]);
+                    if (i < 3) {
+                        f8_ld<32>(base + (GLU ? ((i + 1) >> 1) * 128 + ((i + 1) & 1) * 32 : (i + 1) * 32), v[(i + 1) & 1]);
+                    } else {
                         tc_fence_before();
                         __syncwarp();
                         mbar_arrive_if(tempty0 + 8 * buf, lane == 0);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f2_fma(acc[16 * i + j], f2_pack(v[2 * j], v[2 * j + 1]), GLU && i >= 2 ? g1 : g0);
+                    for (int j = 0; j < 16; ++j)
+                        f2_fma(acc[16 * i + j], f2_pack(v[i & 1][2 * j], v[i & 1][2 * j + 1]), GLU && i >= 2 ? g1 : g0);
                 }
             }
             // the results: 128 columns, or 64 of silu(g) u
@@ -568,7 +597,6 @@ struct Fp8ColsGeo {
     static constexpr int kScaleBlocks = 4;       // blocks of K of a step of the scales' ring
     static constexpr int kScaleSteps = 3;
     static constexpr int kScaleBytes = kScaleSteps * kScaleBlocks * kParts * BN * 4;
-    static constexpr int kThreads = 11 * 32;
     static constexpr int kCtrlBytes = 640 + 2048;   // barriers, flags; the warps' largest values [4][128]
     static constexpr int stages(int extra) {
         const int s = (kSmemLimit - 1024 - kScaleBytes - kCtrlBytes - f8_group_bytes(kMostExperts) - extra) / kStageBytes;
@@ -579,7 +607,7 @@ struct Fp8ColsGeo {
 };
 
 template <int BN, bool GLU>
-__global__ void __launch_bounds__(Fp8ColsGeo<BN, GLU>::kThreads, 1) fp8_cols_kernel(const __grid_constant__ Fp8Args a) {
+__global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_constant__ Fp8Args a) {
     using Geo = Fp8ColsGeo<BN, GLU>;
     constexpr int kStages = Geo::kStages, kParts = Geo::kParts, kBufs = Geo::kBufs, kBlocks = Geo::kScaleBlocks;
     constexpr int kSteps = Geo::kScaleSteps;
@@ -630,6 +658,9 @@ __global__ void __launch_bounds__(Fp8ColsGeo<BN, GLU>::kThreads, 1) fp8_cols_ker
     tc_fence_after();
     const uint32_t tmem = (uint32_t)flags[3];
 
+    // (each branch begins with its own count: where the paths met again, everything would have to fit the smaller)
+    if (warp >= kF8Epilogue) {
+        regs_fewer<kF8OtherRegs>();
     if (warp == kF8Producer) {
         // ------------------------------------------------------------ copies
         int seq = 0, e = 0;
@@ -638,14 +669,7 @@ __global__ void __launch_bounds__(Fp8ColsGeo<BN, GLU>::kThreads, 1) fp8_cols_ker
             const Fp8Tile tile = fp8_tile(c, groups, t, e, BN, cols, true);
             e = tile.e;
             int at[4];
-            if (c.rows) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 4 * lane + i;
-                    const int s = r < tile.rows ? __ldg(c.rows + tile.row0 + r) : -1;
-                    at[i] = s >= 0 && s < c.x_rows ? s : c.x_past;
-                }
-            }
+            const int fours = f8_gather_rows(c, tile, at);
             for (int kb = 0; kb < KB && ok; ++kb, ++seq) {
                 const int st = seq % kStages;
                 if (seq >= kStages) ok = mbar_wait(empty0 + 8 * st, ((seq / kStages) - 1) & 1, flags, err, wait_ns);
@@ -653,14 +677,14 @@ __global__ void __launch_bounds__(Fp8ColsGeo<BN, GLU>::kThreads, 1) fp8_cols_ker
                 if (!ok) break;
                 const uint32_t wa = smem_u32(ring + st * Geo::kStageBytes), xa = wa + kParts * kF8Tile * kF8Row, bar = full0 + 8 * st;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, (uint32_t)Geo::kStageBytes);
+                    mbar_arrive_expect_tx(bar, (uint32_t)(kParts * kF8Tile * kF8Row + (c.rows ? fours * 4 : BN) * kF8Row));
 #pragma unroll
                     for (int g = 0; g < kParts; ++g)
                         tma_load_3d(wa + g * kF8Tile * kF8Row, &a.wmap[g], kb * kFp8Block, tile.col * kF8Tile, tile.e, bar);
                     if (!c.rows) tma_load_2d(xa, &a.xmap, kb * kFp8Block, tile.row0, bar);
                 }
                 __syncwarp();
-                if (c.rows && lane < BN / 4) tma_gather4(xa + 4 * lane * kF8Row, &a.xmap, kb * kFp8Block, at, bar);
+                if (lane < fours) tma_gather4(xa + 4 * lane * kF8Row, &a.xmap, kb * kFp8Block, at, bar);
             }
         }
         if (!ok)
@@ -754,8 +778,10 @@ __global__ void __launch_bounds__(Fp8ColsGeo<BN, GLU>::kThreads, 1) fp8_cols_ker
                 mbar_arrive_if(sfull0 + 8 * slot, lane == 0);
             }
         }
-    } else if (warp < kF8Epilogue) {
+    }
+    } else {
         // ------------------------------------------------------------ epilogue
+        regs_more<kF8EpilogueRegs>();
         // Thread: a column of the result (a row of the weight) for half of the tile's rows.
         constexpr int kMine = BN / 2, kChunk = kMine < 32 ? kMine : 32;
         const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
