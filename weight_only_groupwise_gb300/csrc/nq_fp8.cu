@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdlib>
 #include <mutex>
 
@@ -70,25 +71,56 @@ int* error_word(int dev) {
 // A launch with as much shared memory as the kernel asks for (allowed once a device and thread).
 template <typename Kern>
 cudaError_t fp8_launch(Kern kern, int& set_for_device, int dev, int blocks, int threads, int smem, cudaStream_t stream,
-                       bool pdl, const Fp8Args& a) {
+                       bool pdl, int cluster, const Fp8Args& a) {
     if (set_for_device != dev) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
         set_for_device = dev;
     }
-    return step_launch(kern, dim3(blocks), dim3(threads), (size_t)smem, stream, pdl, 1, a);
+    return step_launch(kern, dim3(blocks), dim3(threads), (size_t)smem, stream, pdl, cluster, a);
 }
-template <bool GLU>
+template <bool GLU, bool PAIR>
 cudaError_t launch_rows(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
-    using Geo = Fp8RowsGeo<GLU>;
+    using Geo = Fp8RowsGeo<GLU, PAIR>;
     static thread_local int set = -1;
-    return fp8_launch(fp8_rows_kernel<GLU>, set, dev, blocks, kF8Threads, Geo::smem(a.c.E), stream, pdl, a);
+    return fp8_launch(fp8_rows_kernel<GLU, PAIR>, set, dev, PAIR ? 2 * blocks : blocks, Geo::kThreads, Geo::smem(a.c.E), stream,
+                      pdl && !PAIR, PAIR ? 2 : 1, a);
+}
+
+// Pairs of blocks that can be resident at once (queried once; at most half of the SMs).
+int pair_capacity(int sms) {
+    static std::atomic<int> known{-1};
+    int n = known.load();
+    if (n >= 0) return n;
+    using Geo = Fp8RowsGeo<false, true>;
+    auto kern = fp8_rows_kernel<false, true>;
+    n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(sms / 2 * 2);
+        cfg.blockDim = dim3(Geo::kThreads);
+        cfg.dynamicSmemBytes = (size_t)Geo::smem(kMostExperts);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+    }
+    if (n > sms / 2) n = sms / 2;
+    known.store(n);
+    return n;
 }
 template <int BN, bool GLU>
 cudaError_t launch_cols(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
     using Geo = Fp8ColsGeo<BN, GLU>;
     static thread_local int set = -1;
-    return fp8_launch(fp8_cols_kernel<BN, GLU>, set, dev, blocks, kF8Threads, Geo::smem(a.c.E), stream, pdl, a);
+    return fp8_launch(fp8_cols_kernel<BN, GLU>, set, dev, blocks, kF8Threads, Geo::smem(a.c.E), stream, pdl, a.c.split, a);
 }
 template <bool GLU>
 cudaError_t launch_cols_of(int bn, const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
@@ -204,23 +236,30 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     int bn = each <= 12 ? 16 : each <= 24 ? 32 : each <= 48 ? 64 : 128;
     if (!experts) bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     bool few = each <= 128;
+    bool pair = !few && each >= 512 && pair_capacity(d.sms) > 0;
     if (const char* f = getenv("NQ_F8")) {
         few = atoi(f) > 0;
         if (few) bn = atoi(f);
+        pair = atoi(f) < 0;
     }
     // a map needs a row; of none, any memory that is there
     const void* codes_at = x->rows > 0 ? x->codes : v[0].codes;
     if (!encode_rows(&a.xmap, codes_at, x->rows > 1 ? xst : K, K, c.x_past, rows ? 1 : (few ? bn : kF8Tile))) return NQ_ERR_CUDA;
     for (int g = 0; g <= (int)glu; ++g)
-        if (!encode_weights(&a.wmap[g], v[g], K, N, E, few || glu ? kF8Tile : 256)) return NQ_ERR_CUDA;
+        if (!encode_weights(&a.wmap[g], v[g], K, N, E, few || glu || pair ? kF8Tile : 256)) return NQ_ERR_CUDA;
     if (!glu) a.wmap[1] = a.wmap[0];
     // a block an SM, or one a tile where the tiles cannot be more
-    const int wide = few || glu ? kF8Tile : 256, high = few ? bn : kF8Tile;
+    const int wide = few || glu ? kF8Tile : 256, high = few ? bn : (pair ? 256 : kF8Tile);
     const long long most = (long long)((N + wide - 1) / wide) * (experts ? (M + high - 1) / high + (E < M ? E : M) : (M + high - 1) / high);
-    const int blocks = (int)(most < d.sms ? most : d.sms);
+    c.split = 1;
+    if (few && !experts && getenv("NQ_F8S")) c.split = atoi(getenv("NQ_F8S"));
+    const bool pdl = d.pdl && !(c.split > 1 && getenv("NQ_F8P"));
+    const int room = pair ? pair_capacity(d.sms) : d.sms;
+    const int blocks = c.split > 1 ? (int)(most * c.split) : (int)(most < room ? most : room);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = few ? (glu ? launch_cols_of<true>(bn, a, dev, blocks, s, d.pdl) : launch_cols_of<false>(bn, a, dev, blocks, s, d.pdl))
-                              : (glu ? launch_rows<true>(a, dev, blocks, s, d.pdl) : launch_rows<false>(a, dev, blocks, s, d.pdl));
+    const cudaError_t e = few ? (glu ? launch_cols_of<true>(bn, a, dev, blocks, s, pdl) : launch_cols_of<false>(bn, a, dev, blocks, s, pdl))
+                              : pair ? (glu ? launch_rows<true, true>(a, dev, blocks, s, pdl) : launch_rows<false, true>(a, dev, blocks, s, pdl))
+                                     : (glu ? launch_rows<true, false>(a, dev, blocks, s, pdl) : launch_rows<false, false>(a, dev, blocks, s, pdl));
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
