@@ -554,8 +554,8 @@ typedef struct nq_fp8_weight {
     long long row_stride, expert_stride, scale_row_stride, scale_expert_stride;
 } nq_fp8_weight;
 
-/* A result: NQ_BF16 or NQ_FP16 [rows][N], `stride` apart (any; the alignment of the type will do, 32 bytes are
- * fastest); or, of the SwiGLU calls with N a multiple of 16, NQ_E4M3: codes (16-byte aligned, stride a multiple of
+/* A result: NQ_BF16 or NQ_FP16 [rows][N], `stride` apart (any; the alignment of the type will do, 16 bytes are
+ * faster); or, of the SwiGLU calls with N a multiple of 16, NQ_E4M3: codes (16-byte aligned, stride a multiple of
  * 16) and fp32 scales [rows][ceil(N / 128)], `scale_stride` apart, quantised as nq_quant_fp8 does. */
 typedef struct nq_fp8_out {
     void* data;
@@ -589,14 +589,19 @@ nq_status nq_swiglu_fp8(const nq_fp8_rows* x, const nq_fp8_weight* wg, const nq_
  * offsets[e] <= i < offsets[e + 1] (device int32 [E + 1]) take expert e's weight.
  *   rows  device int32 [M]: row i is row rows[i] of x (any order, any number of times; one outside x reads
  *         as zeros); NULL: row i of x, and then M <= x->rows
+ *   scratch  nq_fp8_scratch_bytes(M, E, K) bytes of device memory, 16-byte aligned, for many gathered rows, which are
+ *         copied together there first; NULL: they are gathered by the product's own copies, which takes longer
  * offsets are clamped to 0..M and taken as non-decreasing. Rows of the result before offsets[0] and from offsets[E] on
- * are left as they are. 1 <= E <= 1024. The tensors of experts without rows are not read.
+ * are left as they are. 1 <= E <= 512. The tensors of experts without rows are not read.
  */
 nq_status nq_gemm_fp8_experts(const nq_fp8_rows* x, const int* rows, int M, const int* offsets, int E,
-                              const nq_fp8_weight* w, const nq_fp8_out* y, int K, int N, void* stream);
+                              const nq_fp8_weight* w, const nq_fp8_out* y, int K, int N, void* scratch, void* stream);
 nq_status nq_swiglu_fp8_experts(const nq_fp8_rows* x, const int* rows, int M, const int* offsets, int E,
                                 const nq_fp8_weight* wg, const nq_fp8_weight* wu, const nq_fp8_out* h, int K, int N,
-                                void* stream);
+                                void* scratch, void* stream);
+
+/* Bytes of scratch memory that an expert call with `rows` of this size makes use of; 0: none (host only). */
+size_t nq_fp8_scratch_bytes(int M, int E, int K);
 
 enum { NQ_SOFTMAX = 0, NQ_SIGMOID = 1 };   /* score arguments */
 
@@ -613,7 +618,7 @@ enum { NQ_SOFTMAX = 0, NQ_SIGMOID = 1 };   /* score arguments */
  *   offsets int32 [E + 1], written: expert e's rows are offsets[e]..offsets[e + 1] - 1
  *   rows    int32 [T * k], written: the token of each row, ascending within an expert; -1 from offsets[E] on
  *   slots   int32 [T][k], written: the row of each choice, -1 where ids is -1
- * 0 <= T <= 2^20 (0: offsets only), 1 <= k <= min(E, 32), E <= 1024, 0 < scale < inf. Logits need the alignment of their type.
+ * 0 <= T <= 2^20 (0: offsets only), 1 <= k <= min(E, 32), E <= 512, 0 < scale < inf. Logits need the alignment of their type.
  */
 nq_status nq_moe_route(const void* logits, int dtype, long long stride, const float* bias, int T, int E, int k,
                        int score, int normalize, float scale, int* ids, float* weights, int* offsets, int* rows,

@@ -34,8 +34,8 @@ def swiglu(L, x=None, wg=None, wu=None, y=None, K=512, N=288):  # noqa: F811
     return L.nq_swiglu_fp8(x or rows_of(), wg or weight(), wu or weight(codes=5 * A, scales=6 * A), y or out(), K, N, 0)
 
 
-def experts(L, x=None, rows=9 * A, M=70, offsets=10 * A, E=5, w=None, y=None, K=512, N=300):  # noqa: F811
-    return L.nq_gemm_fp8_experts(x or rows_of(), rows, M, offsets, E, w or weight(), y or out(), K, N, 0)
+def experts(L, x=None, rows=9 * A, M=70, offsets=10 * A, E=5, w=None, y=None, K=512, N=300, scratch=0):  # noqa: F811
+    return L.nq_gemm_fp8_experts(x or rows_of(), rows, M, offsets, E, w or weight(), y or out(), K, N, scratch, 0)
 
 
 def route(L, logits=A, dtype=BF16, stride=64, bias=0, T=40, E=64, k=4, score=0, normalize=1, scale=1.0, ids=2 * A, w=3 * A, offsets=4 * A,  # noqa: F811
@@ -94,15 +94,16 @@ def test_results_of_codes_are_the_swiglu_calls_alone(L):  # noqa: F811
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(K=0), SHAPE), (dict(K=500), SHAPE), (dict(N=0), SHAPE), (dict(N=(1 << 20) + 1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(M=-1), SHAPE),
+    (dict(K=0), SHAPE), (dict(K=500), SHAPE), (dict(N=0), SHAPE), (dict(N=(1 << 20) + 1), SHAPE), (dict(E=0), SHAPE), (dict(E=513), SHAPE), (dict(M=-1), SHAPE),
     (dict(M=(1 << 24) + 1), SHAPE), (dict(rows=0), SHAPE), (dict(offsets=0), NULL), (dict(rows=9 * A + 2), ALIGN), (dict(offsets=10 * A + 1), ALIGN),
-    (dict(rows=7 * A), ALIAS), (dict(offsets=7 * A + 4), ALIAS)])
+    (dict(rows=7 * A), ALIAS), (dict(offsets=7 * A + 4), ALIAS), (dict(scratch=11 * A + 8), ALIGN), (dict(M=10000, scratch=7 * A + 512), ALIAS),
+    (dict(M=10000, scratch=A), ALIAS), (dict(M=10000, scratch=3 * A - 64), ALIAS)])
 def test_groups(L, change, status):  # noqa: F811
     assert experts(L, **change) == status
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(dtype=3), SHAPE), (dict(T=-1), SHAPE), (dict(T=(1 << 20) + 1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025, stride=1025), SHAPE), (dict(k=0), SHAPE),
+    (dict(dtype=3), SHAPE), (dict(T=-1), SHAPE), (dict(T=(1 << 20) + 1), SHAPE), (dict(E=0), SHAPE), (dict(E=513, stride=513), SHAPE), (dict(k=0), SHAPE),
     (dict(k=33), SHAPE), (dict(E=3), SHAPE), (dict(stride=63), SHAPE), (dict(stride=HUGE), SHAPE), (dict(score=2), SHAPE), (dict(bias=7 * A), SHAPE),
     (dict(scale=0.0), SHAPE), (dict(scale=float("inf")), SHAPE), (dict(scale=float("nan")), SHAPE), (dict(logits=0), NULL), (dict(ids=0), NULL), (dict(w=0), NULL),
     (dict(offsets=0), NULL), (dict(rows=0), NULL), (dict(slots=0), NULL), (dict(logits=A + 1), ALIGN), (dict(dtype=FP32, logits=A + 2), ALIGN),
@@ -121,6 +122,11 @@ def test_combine(L, change, status):  # noqa: F811
     assert combine(L, **change) == status
 
 
+def test_scratch_is_asked_for_where_groups_are_large(L):  # noqa: F811
+    assert L.nq_fp8_scratch_bytes(10000, 5, 528) == 10000 * (528 + 4 * 8)
+    assert L.nq_fp8_scratch_bytes(64, 64, 512) == 0 and L.nq_fp8_scratch_bytes(0, 5, 512) == 0 and L.nq_fp8_scratch_bytes(10000, 0, 512) == 0
+
+
 def test_empty_calls_are_accepted(L):  # noqa: F811
     assert quant(L, rows=0, x=0) == 0 and combine(L, T=0) == 0
     assert gemm(L, x=rows_of(rows=0, codes=0, scales=0)) == 0 and swiglu(L, x=rows_of(rows=0)) == 0 and experts(L, M=0, rows=0) == 0
@@ -131,7 +137,7 @@ def test_good_calls_pass_the_checks(L):  # noqa: F811
         pytest.skip("fake addresses: only where no GPU could be reached")
     assert all(passes(c(L)) for c in (quant, gemm, swiglu, experts, route, combine))
     assert passes(swiglu(L, y=out(dtype=E4M3, stride=304))) and passes(quant(L, dtype=FP32)) and passes(route(L, T=0, logits=0))
-    assert passes(experts(L, rows=0, M=50)) and passes(route(L, score=1, bias=7 * A)) and passes(combine(L, o=4 * A)) and passes(combine(L, base=0, bs=0))
+    assert passes(experts(L, rows=0, M=50)) and passes(experts(L, M=10000, scratch=11 * A)) and passes(route(L, score=1, bias=7 * A)) and passes(combine(L, o=4 * A)) and passes(combine(L, base=0, bs=0))
     # one row's stride means nothing, nor one expert's
     assert passes(gemm(L, x=rows_of(rows=1, stride=HUGE, ss=HUGE), y=out(stride=HUGE))) and passes(gemm(L, w=weight(expert=HUGE, sexpert=HUGE)))
     assert passes(quant(L, rows=1, xs=HUGE, cs=HUGE, ss=HUGE)) and passes(route(L, T=1, stride=HUGE)) and passes(combine(L, T=1, bs=HUGE, os=HUGE))

@@ -80,7 +80,7 @@ def check_route(logits, k, **how):
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, F32])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 5, 5), (32, 128, 8), (33, 60, 4), (64, 256, 8), (257, 64, 6), (512, 32, 1), (513, 160, 6),
-                                   (700, 1000, 7), (100, 513, 32), (5000, 128, 8), (3000, 1024, 3)])
+                                   (700, 500, 7), (100, 257, 32), (5000, 128, 8), (3000, 512, 3)])
 def test_route(T, E, k, dtype, g):
     x = (2 * torch.randn((T, E), device="cuda", generator=g)).to(dtype)
     check_route(x, k)

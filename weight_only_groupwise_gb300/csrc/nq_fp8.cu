@@ -3,7 +3,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdlib>
 #include <mutex>
 
@@ -79,42 +78,11 @@ cudaError_t fp8_launch(Kern kern, int& set_for_device, int dev, int blocks, int 
     }
     return step_launch(kern, dim3(blocks), dim3(threads), (size_t)smem, stream, pdl, cluster, a);
 }
-template <bool GLU, bool PAIR>
+template <bool GLU>
 cudaError_t launch_rows(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
-    using Geo = Fp8RowsGeo<GLU, PAIR>;
+    using Geo = Fp8RowsGeo<GLU>;
     static thread_local int set = -1;
-    return fp8_launch(fp8_rows_kernel<GLU, PAIR>, set, dev, PAIR ? 2 * blocks : blocks, Geo::kThreads, Geo::smem(a.c.E), stream,
-                      pdl && !PAIR, PAIR ? 2 : 1, a);
-}
-
-// Pairs of blocks that can be resident at once (queried once; at most half of the SMs).
-int pair_capacity(int sms) {
-    static std::atomic<int> known{-1};
-    int n = known.load();
-    if (n >= 0) return n;
-    using Geo = Fp8RowsGeo<false, true>;
-    auto kern = fp8_rows_kernel<false, true>;
-    n = 0;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(sms / 2 * 2);
-        cfg.blockDim = dim3(Geo::kThreads);
-        cfg.dynamicSmemBytes = (size_t)Geo::smem(kMostExperts);
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            n = 0;
-        }
-    }
-    if (n > sms / 2) n = sms / 2;
-    known.store(n);
-    return n;
+    return fp8_launch(fp8_rows_kernel<GLU>, set, dev, blocks, Geo::kThreads, Geo::smem(a.c.E), stream, pdl, 1, a);
 }
 template <int BN, bool GLU>
 cudaError_t launch_cols(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
@@ -132,6 +100,54 @@ cudaError_t launch_cols_of(int bn, const Fp8Args& a, int dev, int blocks, cudaSt
     }
 }
 
+// Rows of x in the order of their experts: a warp a row, codes and scales, zeros for a row that x has not. Bound by memory.
+struct GatherArgs {
+    const uint8_t* x;
+    const float* xs;
+    const int* rows;
+    uint8_t* to;
+    float* to_scales;
+    long long x_stride, xs_stride;
+    int M, x_rows, K, blocks, stride, scale_stride;
+};
+constexpr int kGatherThreads = 256;
+
+__global__ void __launch_bounds__(kGatherThreads) fp8_gather_kernel(const GatherArgs a) {
+    const int i = blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (i >= a.M) return;
+    const int r = __ldg(a.rows + i);
+    const bool there = r >= 0 && r < a.x_rows;
+    const uint4* const from = reinterpret_cast<const uint4*>(a.x + (there ? r : 0) * a.x_stride);
+    uint4* const to = reinterpret_cast<uint4*>(a.to + (long long)i * a.stride);
+    for (int k = lane; k < a.K / 16; k += 4 * 32) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = there && k + 32 * j < a.K / 16 ? __ldg(from + k + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (k + 32 * j < a.K / 16) to[k + 32 * j] = v[j];
+    }
+    for (int b = lane; b < a.blocks; b += 32)
+        a.to_scales[(long long)i * a.scale_stride + b] = there ? __ldg(a.xs + r * a.xs_stride + b) : 0.f;
+}
+
+// Which kernel a call of M rows of E groups takes: rows of x a tile of fp8_cols_kernel, or 0 for fp8_rows_kernel.
+int fp8_plan(int M, int E, bool experts) {
+    const int each = (M + E - 1) / E;            // rows a group, on average
+    if (const char* f = getenv("NQ_F8")) return atoi(f);
+    if (!experts) return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 0;
+    return each <= 12 ? 16 : each <= 24 ? 32 : each <= 48 ? 64 : 0;
+}
+// Whether gathered rows are copied together first, where there is scratch memory.
+bool fp8_gathers(int M, int E) {
+    if (const char* f = getenv("NQ_F8G")) return atoi(f);
+    return fp8_plan(M, E, true) == 0;
+}
+long long scratch_stride(int K) { return (K + 15) / 16 * 16; }
+int scratch_scales(int K) { return ((K + kFp8Block - 1) / kFp8Block + 3) / 4 * 4; }
+
 // Bytes that a weight's codes and floats that its scales span; -1: more than a tensor can have.
 long long weight_span(const nq_fp8_weight* w, int E, int N, int K) {
     const long long rows = step_span(N, w->row_stride, K);
@@ -144,7 +160,8 @@ long long weight_scale_span(const nq_fp8_weight* w, int E, int N, int K) {
 
 // All of the four products. experts: rows and offsets count, else they are not given.
 int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const int* offsets, int E,
-             const nq_fp8_weight* w0, const nq_fp8_weight* w1, bool glu, const nq_fp8_out* y, int K, int N, void* stream) {
+             const nq_fp8_weight* w0, const nq_fp8_weight* w1, bool glu, const nq_fp8_out* y, int K, int N, void* scratch,
+             void* stream) {
     if (!x || !w0 || (glu && !w1) || !y) return NQ_ERR_NULL;
     if (x->rows < 0 || x->rows > kFp8MostRows || M < 0 || M > kFp8MostRows || E < 1 || E > kMostExperts) return NQ_ERR_SHAPE;
     if (K < 16 || K > kFp8MostCols || K % 16 || N < 1 || N > kFp8MostCols) return NQ_ERR_SHAPE;
@@ -188,7 +205,7 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     for (int g = 0; g < 2; ++g)
         if (!v[g].codes || !v[g].scales) return NQ_ERR_NULL;
     if (mis(x->codes, 16) || xst % 16 || mis(x->scales, 4) || mis(y->data, codes ? 16 : 2) || (codes && yst % 16) ||
-        mis(y->scales, 4) || mis(rows, 4) || mis(offsets, 4))
+        mis(y->scales, 4) || mis(rows, 4) || mis(offsets, 4) || mis(scratch, 16))
         return NQ_ERR_ALIGN;
     for (int g = 0; g < 2; ++g)
         if (mis(v[g].codes, 16) || v[g].row_stride % 16 || v[g].expert_stride % 16 || mis(v[g].scales, 4)) return NQ_ERR_ALIGN;
@@ -200,6 +217,13 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     for (const auto& i : in)
         if (meet(y->data, yb, i.p, i.n) || (codes && meet(y->scales, ysb, i.p, i.n))) return NQ_ERR_ALIAS;
     if (codes && meet(y->data, yb, y->scales, ysb)) return NQ_ERR_ALIAS;
+    const bool gathers = rows && scratch && fp8_gathers(M, E);
+    if (gathers) {
+        const long long sb = M * (scratch_stride(K) + 4ll * scratch_scales(K));
+        for (const auto& i : in)
+            if (meet(scratch, sb, i.p, i.n)) return NQ_ERR_ALIAS;
+        if (meet(scratch, sb, y->data, yb) || (codes && meet(scratch, sb, y->scales, ysb))) return NQ_ERR_ALIAS;
+    }
     StepDevice d;
     const int st = step_device(&d);
     if (st != NQ_OK) return st;
@@ -223,43 +247,62 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     c.y_stride = yst;
     c.ys_stride = yss;
     c.x_rows = x->rows;
-    c.x_past = x->rows > 0 ? x->rows : 1;
     c.E = E;
     c.M = M;
     c.K = K;
     c.N = N;
     c.dtype = y->dtype;
-    c.wide = !mis(y->data, 32) && yst % 16 == 0;
+    c.wide = !mis(y->data, 16) && yst % 8 == 0;
     c.quads = !mis(x->scales, 16) && xss % 4 == 0;
     c.wait_ns = d.wait_ns;
-    const int each = (M + E - 1) / E;            // rows a group, on average
-    int bn = each <= 12 ? 16 : each <= 24 ? 32 : each <= 48 ? 64 : 128;
-    if (!experts) bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    bool few = each <= 128;
-    bool pair = !few && each >= 512 && pair_capacity(d.sms) > 0;
-    if (const char* f = getenv("NQ_F8")) {
-        few = atoi(f) > 0;
-        if (few) bn = atoi(f);
-        pair = atoi(f) < 0;
+    const int bn = fp8_plan(M, E, experts);
+    const bool few = bn > 0;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const void* codes_at = x->codes;
+    int x_rows = x->rows;
+    if (gathers) {
+        GatherArgs g;
+        g.x = static_cast<const uint8_t*>(x->rows > 0 ? x->codes : v[0].codes);
+        g.xs = x->scales;
+        g.rows = rows;
+        g.to = static_cast<uint8_t*>(scratch);
+        g.to_scales = reinterpret_cast<float*>(g.to + M * scratch_stride(K));
+        g.x_stride = xst;
+        g.xs_stride = xss;
+        g.M = M;
+        g.x_rows = x->rows;
+        g.K = K;
+        g.blocks = kb;
+        g.stride = (int)scratch_stride(K);
+        g.scale_stride = scratch_scales(K);
+        const int per = kGatherThreads / 32;
+        if (step_launch(fp8_gather_kernel, dim3((M + per - 1) / per), dim3(kGatherThreads), 0, s, d.pdl, 1, g) != cudaSuccess)
+            return NQ_ERR_CUDA;
+        codes_at = scratch;
+        x_rows = M;
+        xst = g.stride;
+        c.rows = rows = nullptr;
+        c.xs = g.to_scales;
+        c.xs_stride = g.scale_stride;
+        c.x_rows = M;
+        c.quads = true;                          // (M codes rows are a multiple of 16 bytes)
     }
     // a map needs a row; of none, any memory that is there
-    const void* codes_at = x->rows > 0 ? x->codes : v[0].codes;
-    if (!encode_rows(&a.xmap, codes_at, x->rows > 1 ? xst : K, K, c.x_past, rows ? 1 : (few ? bn : kF8Tile))) return NQ_ERR_CUDA;
+    c.x_past = x_rows > 0 ? x_rows : 1;
+    if (x_rows == 0) codes_at = v[0].codes;
+    if (!encode_rows(&a.xmap, codes_at, x_rows > 1 ? xst : K, K, c.x_past, rows ? 1 : (few ? bn : kF8Tile))) return NQ_ERR_CUDA;
     for (int g = 0; g <= (int)glu; ++g)
-        if (!encode_weights(&a.wmap[g], v[g], K, N, E, few || glu || pair ? kF8Tile : 256)) return NQ_ERR_CUDA;
+        if (!encode_weights(&a.wmap[g], v[g], K, N, E, few || glu ? kF8Tile : 256)) return NQ_ERR_CUDA;
     if (!glu) a.wmap[1] = a.wmap[0];
     // a block an SM, or one a tile where the tiles cannot be more
-    const int wide = few || glu ? kF8Tile : 256, high = few ? bn : (pair ? 256 : kF8Tile);
+    const int wide = few || glu ? kF8Tile : 256, high = few ? bn : kF8Tile;
     const long long most = (long long)((N + wide - 1) / wide) * (experts ? (M + high - 1) / high + (E < M ? E : M) : (M + high - 1) / high);
     c.split = 1;
     if (few && !experts && getenv("NQ_F8S")) c.split = atoi(getenv("NQ_F8S"));
     const bool pdl = d.pdl && !(c.split > 1 && getenv("NQ_F8P"));
-    const int room = pair ? pair_capacity(d.sms) : d.sms;
-    const int blocks = c.split > 1 ? (int)(most * c.split) : (int)(most < room ? most : room);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int blocks = c.split > 1 ? (int)(most * c.split) : (int)(most < d.sms ? most : d.sms);
     const cudaError_t e = few ? (glu ? launch_cols_of<true>(bn, a, dev, blocks, s, pdl) : launch_cols_of<false>(bn, a, dev, blocks, s, pdl))
-                              : pair ? (glu ? launch_rows<true, true>(a, dev, blocks, s, pdl) : launch_rows<false, true>(a, dev, blocks, s, pdl))
-                                     : (glu ? launch_rows<true, false>(a, dev, blocks, s, pdl) : launch_rows<false, false>(a, dev, blocks, s, pdl));
+                              : (glu ? launch_rows<true>(a, dev, blocks, s, pdl) : launch_rows<false>(a, dev, blocks, s, pdl));
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
@@ -285,24 +328,29 @@ int nq::fp8_take_error(int dev) {
 
 extern "C" {
 
+size_t nq_fp8_scratch_bytes(int M, int E, int K) {
+    if (M <= 0 || M > kFp8MostRows || E < 1 || E > kMostExperts || K < 16 || K > kFp8MostCols || !fp8_gathers(M, E)) return 0;
+    return (size_t)M * (scratch_stride(K) + 4 * scratch_scales(K));
+}
+
 nq_status nq_gemm_fp8(const nq_fp8_rows* x, const nq_fp8_weight* w, const nq_fp8_out* y, int K, int N, void* stream) {
-    return fp8_call(x, false, nullptr, x ? x->rows : 0, nullptr, 1, w, nullptr, false, y, K, N, stream);
+    return fp8_call(x, false, nullptr, x ? x->rows : 0, nullptr, 1, w, nullptr, false, y, K, N, nullptr, stream);
 }
 
 nq_status nq_swiglu_fp8(const nq_fp8_rows* x, const nq_fp8_weight* wg, const nq_fp8_weight* wu, const nq_fp8_out* h,
                         int K, int N, void* stream) {
-    return fp8_call(x, false, nullptr, x ? x->rows : 0, nullptr, 1, wg, wu, true, h, K, N, stream);
+    return fp8_call(x, false, nullptr, x ? x->rows : 0, nullptr, 1, wg, wu, true, h, K, N, nullptr, stream);
 }
 
 nq_status nq_gemm_fp8_experts(const nq_fp8_rows* x, const int* rows, int M, const int* offsets, int E,
-                              const nq_fp8_weight* w, const nq_fp8_out* y, int K, int N, void* stream) {
-    return fp8_call(x, true, rows, M, offsets, E, w, nullptr, false, y, K, N, stream);
+                              const nq_fp8_weight* w, const nq_fp8_out* y, int K, int N, void* scratch, void* stream) {
+    return fp8_call(x, true, rows, M, offsets, E, w, nullptr, false, y, K, N, scratch, stream);
 }
 
 nq_status nq_swiglu_fp8_experts(const nq_fp8_rows* x, const int* rows, int M, const int* offsets, int E,
                                 const nq_fp8_weight* wg, const nq_fp8_weight* wu, const nq_fp8_out* h, int K, int N,
-                                void* stream) {
-    return fp8_call(x, true, rows, M, offsets, E, wg, wu, true, h, K, N, stream);
+                                void* scratch, void* stream) {
+    return fp8_call(x, true, rows, M, offsets, E, wg, wu, true, h, K, N, scratch, stream);
 }
 
 }  // extern "C"

@@ -11,7 +11,7 @@ namespace nq {
 constexpr int kFp8Block = 128;              // columns (and rows of a weight) of a scale
 constexpr int kFp8MostRows = 1 << 24;
 constexpr int kFp8MostCols = 1 << 20;       // K and N
-constexpr int kMostExperts = 1024;
+constexpr int kMostExperts = 512;
 
 inline bool mis(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 

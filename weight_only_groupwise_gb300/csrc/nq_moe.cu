@@ -230,7 +230,7 @@ __device__ __forceinline__ void route_place(const RouteArgs& a, int* sm) {
             if (b < rank) ahead += c;
             mine += c;
         }
-    // scan over experts: at most 1024, one a thread
+    // scan over experts: at most 512, one a thread
     int upto = mine;
     const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
@@ -482,8 +482,7 @@ nq_status nq_moe_route(const void* logits, int dtype, long long stride, const fl
                           : E <= 64  ? route_launch<2>(a, s, d.pdl)
                           : E <= 128 ? route_launch<4>(a, s, d.pdl)
                           : E <= 256 ? route_launch<8>(a, s, d.pdl)
-                          : E <= 512 ? route_launch<16>(a, s, d.pdl)
-                                     : route_launch<32>(a, s, d.pdl);
+                                     : route_launch<16>(a, s, d.pdl);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
