@@ -556,7 +556,8 @@ typedef struct nq_fp8_weight {
 
 /* A result: NQ_BF16 or NQ_FP16 [rows][N], `stride` apart (any; the alignment of the type will do, 16 bytes are
  * faster); or, of the SwiGLU calls with N a multiple of 16, NQ_E4M3: codes (16-byte aligned, stride a multiple of
- * 16) and fp32 scales [rows][ceil(N / 128)], `scale_stride` apart, quantised as nq_quant_fp8 does. */
+ * 16) and fp32 scales [rows][ceil(N / 128)], `scale_stride` apart, as nq_quant_fp8's of
+ * the fp32 results (times the reciprocal of their scale). */
 typedef struct nq_fp8_out {
     void* data;
     float* scales;

@@ -43,10 +43,11 @@ def product(x, w):
 
 
 def silu(g, dg, u, du):
-    """silu(g) u and its error: |silu'| < 1.1; the exponential, sum, quotient and product lose less than 8 half places."""
+    """silu(g) u and its error: |silu'| < 1.1; the exponential's rounded argument loses |g| 2^-23 (two roundings of it), the
+    exponential and the quotient two places each, sum and product a half."""
     s = g / (1 + torch.exp(-g))
     h = s * u
-    return h, 1.1 * dg * (u.abs() + du) + s.abs() * du + 8 * 2.0 ** -24 * h.abs()
+    return h, 1.1 * dg * (u.abs() + du) + s.abs() * du + (5 + g.abs()) * 2.0 ** -23 * h.abs()
 
 
 def close(y, ref, err):
@@ -66,7 +67,7 @@ def close_codes(codes, scales, ref, err):
     assert bool(((scales.double() - s_ref).abs() <= ds).all())
     s = spread(scales, N)
     # e4m3: half a step is 2^-4 of the value, 2^-10 below the smallest normal number; the quotient loses a place
-    step = s * torch.maximum(2.0 ** -4 * (ref.abs() + err) / s, torch.full_like(ref, 2.0 ** -10)) * (1 + 2.0 ** -20)
+    step = s * torch.maximum(2.0 ** -4 * (ref.abs() + err) / s, torch.full_like(ref, 2.0 ** -10)) * (1 + 2.0 ** -19)
     # the block's largest value may land above 448 by the scale's own rounding, and is cut
     cut = 2.0 ** -22 * s * 448
     assert bool(((codes.double() * s - ref).abs() <= err + step + cut).all())

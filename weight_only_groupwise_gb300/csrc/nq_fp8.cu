@@ -78,11 +78,11 @@ cudaError_t fp8_launch(Kern kern, int& set_for_device, int dev, int blocks, int 
     }
     return step_launch(kern, dim3(blocks), dim3(threads), (size_t)smem, stream, pdl, cluster, a);
 }
-template <bool GLU>
+template <bool GLU, bool BULK>
 cudaError_t launch_rows(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
-    using Geo = Fp8RowsGeo<GLU>;
+    using Geo = Fp8RowsGeo<GLU, BULK>;
     static thread_local int set = -1;
-    return fp8_launch(fp8_rows_kernel<GLU>, set, dev, blocks, Geo::kThreads, Geo::smem(a.c.E), stream, pdl, 1, a);
+    return fp8_launch(fp8_rows_kernel<GLU, BULK>, set, dev, blocks, Geo::kThreads, Geo::smem(a.c.E), stream, pdl, 1, a);
 }
 template <int BN, bool GLU>
 cudaError_t launch_cols(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
@@ -299,10 +299,14 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     const long long most = (long long)((N + wide - 1) / wide) * (experts ? (M + high - 1) / high + (E < M ? E : M) : (M + high - 1) / high);
     c.split = 1;
     if (few && !experts && getenv("NQ_F8S")) c.split = atoi(getenv("NQ_F8S"));
-    const bool pdl = d.pdl && !(c.split > 1 && getenv("NQ_F8P"));
+    bool bulk = c.wide && N % 8 == 0 && K <= 2048;
+    if (const char* f = getenv("NQ_F8P")) bulk = c.wide && N % 8 == 0 && atoi(f);
+    const bool pdl = d.pdl;
     const int blocks = c.split > 1 ? (int)(most * c.split) : (int)(most < d.sms ? most : d.sms);
     const cudaError_t e = few ? (glu ? launch_cols_of<true>(bn, a, dev, blocks, s, pdl) : launch_cols_of<false>(bn, a, dev, blocks, s, pdl))
-                              : (glu ? launch_rows<true>(a, dev, blocks, s, pdl) : launch_rows<false>(a, dev, blocks, s, pdl));
+                              : glu  ? launch_rows<true, false>(a, dev, blocks, s, pdl)
+                          : bulk ? launch_rows<false, true>(a, dev, blocks, s, pdl)
+                                 : launch_rows<false, false>(a, dev, blocks, s, pdl);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 

@@ -182,6 +182,11 @@ __device__ __forceinline__ uint32_t pack_16(float lo, float hi, bool bf16) {
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// silu(g) u with the exponential and the quotient of the special function unit: a tile's 16384 of them were a sixth of its time
+// (32 blocks of K) with expf and a division. The exponential's argument is rounded: an error of |g| 2^-23 at most,
+// with two places each of the two functions and one a product.
+__device__ __forceinline__ float f8_silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
 // Larger of two magnitudes by their bits: NaN is the largest of all.
 __device__ __forceinline__ uint32_t bits_max(uint32_t m, float v) { return max(m, __float_as_uint(v) & 0x7FFFFFFFu); }
 
@@ -370,26 +375,32 @@ __device__ __forceinline__ void f8_scales(const Fp8Call& c, const Fp8Groups& gro
 // tried: 8 epilogue warps of 128 sums a thread 320 us, without registers handed to them 751 (spills); sums two at a time
 // (fma.rn.f32x2) 307, its operands' pairing costs the moves that it saves; loads from TMEM issued during the sums 311; pairs
 // of blocks sharing a tile of 256 rows (cta_group::2) 334 to 359, with half of the copies.
-template <bool GLU>
+//
+// BULK, for short sums (K), of which a tile's 64 KB of results are a large part: results go to shared memory and from
+// there by bulk copies, a row each, while the next tile's sums are added. That takes the room of a stage.
+template <bool GLU, bool BULK>
 struct Fp8RowsGeo {
+    static_assert(!(GLU && BULK), "of SwiGLU results there is half as much");
     static constexpr int kOut = GLU ? 128 : 256; // columns of the result in a tile; D has 256: those, or gate and up
     static constexpr int kStageBytes = (kF8Tile + 256) * kF8Row;
-    static constexpr int kStages = 4;
+    static constexpr int kStages = BULK ? 3 : 4;
     static constexpr int kWarps = 16;            // of the epilogue
     static constexpr int kThreads = (kWarps + 4) * 32;
     static constexpr int kRegs = 104, kOtherRegs = 64;           // a block begins with 96 a thread
     static_assert(kWarps * 32 * kRegs + 4 * 32 * kOtherRegs == kThreads * 96, "registers of a block");
     static constexpr int kScaleBytes = f8_scale_bytes(kF8Tile, 2);
-    static constexpr int kPitch = 144;           // bytes of a row of turned results: 16 x odd, so that lanes meet no bank twice
-    static constexpr int kTurnBytes = kWarps * 8 * kPitch;       // 8 rows of a warp's 64 (GLU: 32) columns
+    // bytes of a row of results in shared memory, 16 x odd, so that lanes meet no bank twice: a tile's 256 columns, or the 64
+    // (GLU: 32) of a warp, 8 rows at a time
+    static constexpr int kPitch = BULK ? 528 : 144;
+    static constexpr int kTurnBytes = BULK ? kF8Tile * kPitch : kWarps * 8 * kPitch;
     static constexpr int kCtrlBytes = 512 + kScaleBytes + kTurnBytes;
     static_assert(kTurnBytes >= 4 * kF8Tile * 4, "room for the rows' largest values");
     static int smem(int E) { return 1024 + kStages * kStageBytes + kCtrlBytes + f8_group_bytes(E); }
 };
 
-template <bool GLU>
-__global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(const __grid_constant__ Fp8Args a) {
-    using Geo = Fp8RowsGeo<GLU>;
+template <bool GLU, bool BULK>
+__global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_kernel(const __grid_constant__ Fp8Args a) {
+    using Geo = Fp8RowsGeo<GLU, BULK>;
     constexpr int kStages = Geo::kStages, kWarps = Geo::kWarps;
     constexpr int kProducer = kWarps, kMma = kWarps + 1, kScales = kWarps + 2;
     const Fp8Call& c = a.c;
@@ -562,7 +573,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
             const int n = tile.col * Geo::kOut + d0;
             if constexpr (GLU) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) acc[i] = silu_mul(acc[i], acc[32 + i]);
+                for (int i = 0; i < 32; ++i) acc[i] = f8_silu_mul(acc[i], acc[32 + i]);
             }
             if (GLU && c.dtype == NQ_E4M3) {
                 uint32_t m = 0;
@@ -574,7 +585,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) m = max(m, largest[i * kF8Tile + row]);
                 named_bar_sync(1 + quarter, 128);        // the next tile's use the same place
-                const float s = fp8_scale(__uint_as_float(m));
+                const float s = fp8_scale(__uint_as_float(m)), r = 1.f / s;
                 if (ok && row < tile.rows) {
                     const long long my_row = tile.row0 + row;
                     if (group == 0) c.ys[my_row * c.ys_stride + tile.col] = s;
@@ -585,10 +596,32 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float* const p = acc + i + 4 * j;
-                            u[j] = fp8_codes(p[0] / s, p[1] / s, p[2] / s, p[3] / s);
+                            u[j] = fp8_codes(p[0] * r, p[1] * r, p[2] * r, p[3] * r);
                         }
                         *reinterpret_cast<uint4*>(c.y + my_row * c.y_stride + n + i) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
+                }
+            } else if (BULK) {
+                // (results aligned to 16 bytes, N a multiple of 8)
+                const bool bf16 = c.dtype == NQ_BF16;
+                uint8_t* const mine = turn + row * Geo::kPitch + 2 * d0;
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                named_bar_sync(1 + quarter, 128);        // the tile before has been read
+#pragma unroll
+                for (int j = 0; j < kMine; j += 8)
+                    *reinterpret_cast<uint4*>(mine + 2 * j) =
+                        make_uint4(pack_16(acc[j], acc[j + 1], bf16), pack_16(acc[j + 2], acc[j + 3], bf16),
+                                   pack_16(acc[j + 4], acc[j + 5], bf16), pack_16(acc[j + 6], acc[j + 7], bf16));
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                named_bar_sync(1 + quarter, 128);
+                const int r = 32 * quarter + 8 * group + lane;   // each of the row's four warps has 8 rows to send
+                if (lane < 8 && ok && r < tile.rows) {
+                    const int n1 = tile.col * Geo::kOut;
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                     reinterpret_cast<uint16_t*>(c.y) + (long long)(tile.row0 + r) * c.y_stride + n1),
+                                 "r"(smem_u32(turn + r * Geo::kPitch)), "r"(2 * min(Geo::kOut, c.N - n1))
+                                 : "memory");
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             } else {
                 // Turned in shared memory, 8 rows at a time, so that a store writes whole lines (of 4 or 8 rows, or, where rows
@@ -638,6 +671,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU>::kThreads, 1) fp8_rows_kernel(
                 }
             }
         }
+        if (BULK) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     tc_fence_before();
@@ -872,7 +906,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
             const int rows_here = ok ? min(kMine, tile.rows - half * kMine) : 0;
             if constexpr (GLU) {
 #pragma unroll
-                for (int i = 0; i < kMine; ++i) acc[0][i] = silu_mul(acc[0][i], acc[1][i]);
+                for (int i = 0; i < kMine; ++i) acc[0][i] = f8_silu_mul(acc[0][i], acc[1][i]);
             }
             const long long first = tile.row0 + half * kMine;
             if (GLU && c.dtype == NQ_E4M3) {
@@ -889,9 +923,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
                         uint32_t m = 0;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) m = max(m, largest[q * BN + half * kMine + i]);
-                        const float s = fp8_scale(__uint_as_float(m));
+                        const float s = fp8_scale(__uint_as_float(m)), r = 1.f / s;
                         if (row == 0) c.ys[(first + i) * c.ys_stride + tile.col] = s;
-                        if (n < c.N) c.y[(first + i) * c.y_stride + n] = (uint8_t)fp8_codes(acc[0][i] / s, 0.f, 0.f, 0.f);
+                        if (n < c.N) c.y[(first + i) * c.y_stride + n] = (uint8_t)fp8_codes(acc[0][i] * r, 0.f, 0.f, 0.f);
                     }
                 }
                 named_bar_sync(1 + half, 128);   // the next tile's largest use the same place
@@ -934,16 +968,16 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
                     }
                 if constexpr (GLU)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[0][j] = silu_mul(v[0][j], v[kParts - 1][j]);
+                    for (int j = 0; j < 4; ++j) v[0][j] = f8_silu_mul(v[0][j], v[kParts - 1][j]);
                 const long long at = (tile.row0 + i) * c.y_stride + n;
                 if (GLU && c.dtype == NQ_E4M3) {
                     uint32_t m = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) m = n < c.N ? bits_max(m, v[0][j]) : m;
-                    const float s = fp8_scale(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)));
+                    const float s = fp8_scale(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m))), r = 1.f / s;
                     if (lane == 0) c.ys[(tile.row0 + i) * c.ys_stride + tile.col] = s;
                     if (n < c.N)         // (N a multiple of 16)
-                        *reinterpret_cast<uint32_t*>(c.y + at) = fp8_codes(v[0][0] / s, v[0][1] / s, v[0][2] / s, v[0][3] / s);
+                        *reinterpret_cast<uint32_t*>(c.y + at) = fp8_codes(v[0][0] * r, v[0][1] * r, v[0][2] * r, v[0][3] * r);
                 } else {
                     uint16_t* const y = reinterpret_cast<uint16_t*>(c.y) + at;
                     const bool bf16 = c.dtype == NQ_BF16;
