@@ -590,7 +590,7 @@ nq_status nq_swiglu_fp8(const nq_fp8_rows* x, const nq_fp8_weight* wg, const nq_
  * offsets[e] <= i < offsets[e + 1] (device int32 [E + 1]) take expert e's weight.
  *   rows  device int32 [M]: row i is row rows[i] of x (any order, any number of times; one outside x reads
  *         as zeros); NULL: row i of x, and then M <= x->rows
- *   scratch  nq_fp8_scratch_bytes(M, E, K) bytes of device memory, 16-byte aligned, for many gathered rows, which are
+ *   scratch  nq_fp8_scratch_bytes(M, E, K, swiglu) bytes of device memory, 16-byte aligned, for many gathered rows, which are
  *         copied together there first; NULL: they are gathered by the product's own copies, which takes longer
  * offsets are clamped to 0..M and taken as non-decreasing. Rows of the result before offsets[0] and from offsets[E] on
  * are left as they are. 1 <= E <= 512. The tensors of experts without rows are not read.
@@ -601,8 +601,9 @@ nq_status nq_swiglu_fp8_experts(const nq_fp8_rows* x, const int* rows, int M, co
                                 const nq_fp8_weight* wg, const nq_fp8_weight* wu, const nq_fp8_out* h, int K, int N,
                                 void* scratch, void* stream);
 
-/* Bytes of scratch memory that an expert call with `rows` of this size makes use of; 0: none (host only). */
-size_t nq_fp8_scratch_bytes(int M, int E, int K);
+/* Bytes of scratch memory that an expert call (swiglu: the SwiGLU one) with `rows` of this size makes use of; 0: none
+ * (host only). */
+size_t nq_fp8_scratch_bytes(int M, int E, int K, int swiglu);
 
 enum { NQ_SOFTMAX = 0, NQ_SIGMOID = 1 };   /* score arguments */
 

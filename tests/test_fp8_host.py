@@ -123,8 +123,9 @@ def test_combine(L, change, status):  # noqa: F811
 
 
 def test_scratch_is_asked_for_where_groups_are_large(L):  # noqa: F811
-    assert L.nq_fp8_scratch_bytes(10000, 5, 528) == 10000 * (528 + 4 * 8)
-    assert L.nq_fp8_scratch_bytes(64, 64, 512) == 0 and L.nq_fp8_scratch_bytes(0, 5, 512) == 0 and L.nq_fp8_scratch_bytes(10000, 0, 512) == 0
+    for swiglu in (0, 1):
+        need = lambda *a: L.nq_fp8_scratch_bytes(*a, swiglu)  # noqa: E731, B023
+        assert need(10000, 5, 528) == 10000 * (528 + 4 * 8) and need(64, 64, 512) == need(0, 5, 512) == need(10000, 0, 512) == need(10000, 5, 0) == 0
 
 
 def test_empty_calls_are_accepted(L):  # noqa: F811

@@ -3,7 +3,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <cstdlib>
 #include <mutex>
 
 #include "nq.h"
@@ -96,7 +95,7 @@ cudaError_t launch_cols_of(int bn, const Fp8Args& a, int dev, int blocks, cudaSt
         case 16: return launch_cols<16, GLU>(a, dev, blocks, stream, pdl);
         case 32: return launch_cols<32, GLU>(a, dev, blocks, stream, pdl);
         case 64: return launch_cols<64, GLU>(a, dev, blocks, stream, pdl);
-        default: return launch_cols<128, GLU>(a, dev, blocks, stream, pdl);
+        default: return launch_cols<GLU ? 64 : 128, GLU>(a, dev, blocks, stream, pdl);
     }
 }
 
@@ -133,18 +132,82 @@ __global__ void __launch_bounds__(kGatherThreads) fp8_gather_kernel(const Gather
         a.to_scales[(long long)i * a.scale_stride + b] = there ? __ldg(a.xs + r * a.xs_stride + b) : 0.f;
 }
 
-// Which kernel a call of M rows of E groups takes: rows of x a tile of fp8_cols_kernel, or 0 for fp8_rows_kernel.
-int fp8_plan(int M, int E, bool experts) {
-    const int each = (M + E - 1) / E;            // rows a group, on average
-    if (const char* f = getenv("NQ_F8")) return atoi(f);
-    if (!experts) return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 0;
-    return each <= 12 ? 16 : each <= 24 ? 32 : each <= 48 ? 64 : 0;
+// Clusters of n blocks that can run at once, by n (queried once).
+const int* fp8_clusters(int sms) {
+    static std::once_flag once;
+    static int most[kF8MostSplit + 1] = {};
+    std::call_once(once, [sms] {
+        using Geo = Fp8ColsGeo<16, false>;
+        auto kern = fp8_cols_kernel<16, false>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) return;
+        for (int n = 2; n <= kF8MostSplit; ++n) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(sms / n * n);
+            cfg.blockDim = dim3(kF8Threads);
+            cfg.dynamicSmemBytes = (size_t)Geo::smem(1);
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)n;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&most[n], kern, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                most[n] = 0;
+            }
+        }
+    });
+    return most;
 }
-// Whether gathered rows are copied together first, where there is scratch memory.
-bool fp8_gathers(int M, int E) {
-    if (const char* f = getenv("NQ_F8G")) return atoi(f);
-    return fp8_plan(M, E, true) == 0;
+
+// Which kernel takes a call, and how. rows: of x in a tile of fp8_cols_kernel, or 0 for fp8_rows_kernel; split: blocks that
+// share a tile's K.
+struct Fp8Plan {
+    int rows, split;
+};
+
+// Rows a group on average up to which calls by expert go in tiles of 16 and 32 rows, plain and SwiGLU. Where weights of many
+// experts are read for few rows each, small tiles need fewer copies; 128 experts, us with tiles of 16, 32 rows and
+// fp8_rows_kernel: SwiGLU 2048 -> 768, 12 rows an expert 67.4, 70.8, 79.8; 24 rows 76.4, 70.8, 81.0; 32 rows 97, 88, 83; plain
+// 768 -> 2048, 6 rows 35.2, 39.9, 38.4; 12 rows 42.2, 41.7, 39.1; 24 rows 67.4, 50.4, 39.8.
+int fp8_experts_rows(int M, int E, bool glu) {
+    const int each = (M + E - 1) / E;
+    return each <= (glu ? 16 : 10) ? 16 : glu && each <= 28 ? 32 : 0;
 }
+
+// A dense call: the fewest microseconds by a count of the blocks of K that the busiest SM goes through, at what one of them
+// takes each kernel (measured at K = 4096 and 5120; a tile's blocks of K, 128 columns or 256, are one after
+// another): few tiles leave SMs idle, large ones are cheaper a row. A launch takes 4 us, the exchange of a split sum 1.5.
+// 333 x 4112 x 2501, us: tiles of 64 rows 15.9, of 128 shared by two blocks 14.6, fp8_rows_kernel 25.8; 256 x 4096 x 5120:
+// 26.5, 18.3, 20.0; 512 x 5120 x 17408: 118, 75, 46.
+Fp8Plan fp8_dense_plan(int M, int K, int N, bool glu, int sms, const int* clusters) {
+    static const struct {
+        int rows;
+        float us[2];                             // a block of K: plain, SwiGLU
+    } kinds[] = {{16, {0.25f, 0.35f}}, {32, {0.30f, 0.50f}}, {64, {0.35f, 0.70f}}, {128, {0.43f, 0.f}}, {0, {0.48f, 0.62f}}};
+    const long long blocks = (K + kFp8Block - 1) / kFp8Block;
+    Fp8Plan best = {0, 1};
+    float least = 1e30f;
+    for (const auto& k : kinds) {
+        if (k.us[glu] == 0.f) continue;
+        const int high = k.rows ? k.rows : kF8Tile, wide = k.rows || glu ? 128 : 256;
+        const long long tiles = (long long)((M + high - 1) / high) * ((N + wide - 1) / wide), rounds = (tiles + sms - 1) / sms;
+        long long split = 1;                     // as many as can run at once
+        for (int n = 2; k.rows && n <= kF8MostSplit && n <= blocks / 2; ++n)
+            if (tiles <= clusters[n]) split = n;
+        const float us = 4.f + (split > 1 ? 1.5f : 0.f) + k.us[glu] * rounds * ((blocks + split - 1) / split);
+        if (us < least) {
+            least = us;
+            best = {k.rows, (int)split};
+        }
+    }
+    return best;
+}
+
+// Whether gathered rows are copied together first, where there is scratch memory: for fp8_rows_kernel, whose 128 rows a block
+// of K take the copy engine longer to gather than to multiply (4096 tokens x 8 of 64 experts: 1014 us, 497 so).
+bool fp8_gathers(int M, int E, bool glu) { return fp8_experts_rows(M, E, glu) == 0; }
 long long scratch_stride(int K) { return (K + 15) / 16 * 16; }
 int scratch_scales(int K) { return ((K + kFp8Block - 1) / kFp8Block + 3) / 4 * 4; }
 
@@ -217,7 +280,7 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     for (const auto& i : in)
         if (meet(y->data, yb, i.p, i.n) || (codes && meet(y->scales, ysb, i.p, i.n))) return NQ_ERR_ALIAS;
     if (codes && meet(y->data, yb, y->scales, ysb)) return NQ_ERR_ALIAS;
-    const bool gathers = rows && scratch && fp8_gathers(M, E);
+    const bool gathers = rows && scratch && fp8_gathers(M, E, glu);
     if (gathers) {
         const long long sb = M * (scratch_stride(K) + 4ll * scratch_scales(K));
         for (const auto& i : in)
@@ -255,7 +318,8 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     c.wide = !mis(y->data, 16) && yst % 8 == 0;
     c.quads = !mis(x->scales, 16) && xss % 4 == 0;
     c.wait_ns = d.wait_ns;
-    const int bn = fp8_plan(M, E, experts);
+    const Fp8Plan plan = experts ? Fp8Plan{fp8_experts_rows(M, E, glu), 1} : fp8_dense_plan(M, K, N, glu, d.sms, fp8_clusters(d.sms));
+    const int bn = plan.rows;
     const bool few = bn > 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const void* codes_at = x->codes;
@@ -297,16 +361,15 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     // a block an SM, or one a tile where the tiles cannot be more
     const int wide = few || glu ? kF8Tile : 256, high = few ? bn : kF8Tile;
     const long long most = (long long)((N + wide - 1) / wide) * (experts ? (M + high - 1) / high + (E < M ? E : M) : (M + high - 1) / high);
-    c.split = 1;
-    if (few && !experts && getenv("NQ_F8S")) c.split = atoi(getenv("NQ_F8S"));
-    bool bulk = c.wide && N % 8 == 0 && K <= 2048;
-    if (const char* f = getenv("NQ_F8P")) bulk = c.wide && N % 8 == 0 && atoi(f);
-    const bool pdl = d.pdl;
+    c.split = plan.split;
+    // results of sums of up to so many blocks of K go by bulk copies (us, stored by the threads and so, 24570 rows of
+    // 128 experts x 2048: K = 256 52.6, 41.9; 768 83.0, 73.3; 2304 166.8, 163.3; 4096 269.2, 272.6)
+    const bool bulk = c.wide && N % 8 == 0 && K <= 20 * kFp8Block;
     const int blocks = c.split > 1 ? (int)(most * c.split) : (int)(most < d.sms ? most : d.sms);
-    const cudaError_t e = few ? (glu ? launch_cols_of<true>(bn, a, dev, blocks, s, pdl) : launch_cols_of<false>(bn, a, dev, blocks, s, pdl))
-                              : glu  ? launch_rows<true, false>(a, dev, blocks, s, pdl)
-                          : bulk ? launch_rows<false, true>(a, dev, blocks, s, pdl)
-                                 : launch_rows<false, false>(a, dev, blocks, s, pdl);
+    const cudaError_t e = few ? (glu ? launch_cols_of<true>(bn, a, dev, blocks, s, d.pdl) : launch_cols_of<false>(bn, a, dev, blocks, s, d.pdl))
+                              : glu  ? launch_rows<true, false>(a, dev, blocks, s, d.pdl)
+                          : bulk ? launch_rows<false, true>(a, dev, blocks, s, d.pdl)
+                                 : launch_rows<false, false>(a, dev, blocks, s, d.pdl);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
@@ -332,8 +395,8 @@ int nq::fp8_take_error(int dev) {
 
 extern "C" {
 
-size_t nq_fp8_scratch_bytes(int M, int E, int K) {
-    if (M <= 0 || M > kFp8MostRows || E < 1 || E > kMostExperts || K < 16 || K > kFp8MostCols || !fp8_gathers(M, E)) return 0;
+size_t nq_fp8_scratch_bytes(int M, int E, int K, int swiglu) {
+    if (M <= 0 || M > kFp8MostRows || E < 1 || E > kMostExperts || K < 16 || K > kFp8MostCols || !fp8_gathers(M, E, swiglu != 0)) return 0;
     return (size_t)M * (scratch_stride(K) + 4 * scratch_scales(K));
 }
 

@@ -35,6 +35,7 @@ constexpr int kF8Threads = 12 * 32;              // (warp 11 only gives its regi
 constexpr int kF8EpilogueRegs = 216, kF8OtherRegs = 72;
 static_assert(256 * kF8EpilogueRegs + 128 * kF8OtherRegs == kF8Threads * 168, "registers of a block");
 constexpr int kF8MaxStages = 16;
+constexpr int kF8MostSplit = 8;                  // blocks that share a tile's K: a portable cluster
 constexpr int kF8Row = 128;                      // bytes (codes) of a stage's row: one block of K, one swizzled row
 constexpr int kF8Tile = 128;                     // rows of a block's MMA operand A
 

@@ -118,7 +118,7 @@ def lib() -> ctypes.CDLL:
         L.nq_swiglu_fp8.argtypes = [P, P, P, P, I, I, P]
         L.nq_gemm_fp8_experts.argtypes = [P, P, I, P, I, P, P, I, I, P, P]
         L.nq_swiglu_fp8_experts.argtypes = [P, P, I, P, I, P, P, P, I, I, P, P]
-        L.nq_fp8_scratch_bytes.argtypes = [I, I, I]
+        L.nq_fp8_scratch_bytes.argtypes = [I, I, I, I]
         L.nq_fp8_scratch_bytes.restype = S
         L.nq_moe_route.argtypes = [P, I, LL, P, I, I, I, I, I, F, P, P, P, P, P, P]
         L.nq_moe_combine.argtypes = [P, I, LL, I, P, P, I, I, I, P, LL, P, LL, P]
@@ -711,7 +711,7 @@ def _fp8(fn, xq, xs, weights, dtype, out, stream, experts=None):
     if experts is None:
         _check(fn(x, *packed, y, K, N, _raw_stream(stream)))
     else:
-        need = lib().nq_fp8_scratch_bytes(M, E, K) if rows is not None else 0
+        need = lib().nq_fp8_scratch_bytes(M, E, K, len(packed) - 1) if rows is not None else 0
         scratch = torch.empty(need, dtype=torch.uint8, device=xq.device) if need else None
         _check(fn(x, rows, M, offsets, E, *packed, y, K, N, scratch.data_ptr() if need else None, _raw_stream(stream)))
     return out
