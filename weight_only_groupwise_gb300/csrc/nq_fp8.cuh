@@ -209,8 +209,8 @@ struct Fp8Tile {
     int e, row0, rows, col;                      // expert, first row, rows of the tile, column tile
 };
 
-// All threads of a block: `sums` has room for a number of each warp. Waits for the preceding kernel, whose offsets they may
-// be. Returns the call's tiles.
+// All threads of a block: `sums` has room for a number of each warp. Returns the call's tiles. By expert, waits for the
+// preceding kernel, whose offsets they may be; a dense call's threads wait where they first read or write what it may have.
 __device__ __forceinline__ int fp8_groups(const Fp8Call& c, const Fp8Groups& g, int high, int cols, int* sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
     int total = 0;
@@ -221,7 +221,6 @@ __device__ __forceinline__ int fp8_groups(const Fp8Call& c, const Fp8Groups& g, 
             g.before[1] = total;
             g.end[0] = c.M;
         }
-        grid_dependency_wait();
         return total;
     }
     grid_dependency_wait();
@@ -314,6 +313,7 @@ __device__ __forceinline__ void f8_scales(const Fp8Call& c, const Fp8Groups& gro
     const int lane = threadIdx.x & 31;
     int step = 0, e = 0;
     bool ok = true;
+    grid_dependency_wait();
     for (int t = t0; t < total && ok; t += dt) {
         const Fp8Tile tile = fp8_tile(c, groups, t, e, ROWS, cols, even);
         e = tile.e;
@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
             F8Ring<kStages> in;
             int seq = 0, e = 0;
             bool ok = true;
+            const int late = c.offsets ? 0 : min(kStages, KB);
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 const Fp8Tile tile = fp8_tile(c, groups, t, e, kF8Tile, cols, false);
                 e = tile.e;
@@ -471,16 +472,22 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty0 + 8 * in.at, in.parity ^ 1, flags, err, wait_ns));
                     if (!ok) break;
                     const uint32_t xa = smem_u32(ring) + in.at * Geo::kStageBytes, wa = xa + kF8Tile * kF8Row, bar = full0 + 8 * in.at;
+                    const int k = kb * kFp8Block;
                     in.next();
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar, (uint32_t)((256 + (c.rows ? fours * 4 : kF8Tile)) * kF8Row));
-                        const int k = kb * kFp8Block;
                         tma_load_3d(wa, &a.wmap[0], k, tile.col * Geo::kOut, tile.e, bar);
                         if (GLU) tma_load_3d(wa + 128 * kF8Row, &a.wmap[1], k, tile.col * 128, tile.e, bar);
-                        if (!c.rows) f8_copy_2d(xa, &a.xmap, k, tile.row0, bar);
+                        // (the first stages' weights are on their way before the preceding kernel has ended: late)
+                        if (seq >= late && !c.rows) f8_copy_2d(xa, &a.xmap, k, tile.row0, bar);
+                        if (seq + 1 == late) {
+                            grid_dependency_wait();
+                            for (int j = 0; j < late; ++j)
+                                f8_copy_2d(smem_u32(ring) + j * Geo::kStageBytes, &a.xmap, j * kFp8Block, tile.row0, full0 + 8 * j);
+                        }
                     }
                     __syncwarp();
-                    if (lane < fours) f8_gather4(xa + 4 * lane * kF8Row, &a.xmap, kb * kFp8Block, at, bar);
+                    if (lane < fours) f8_gather4(xa + 4 * lane * kF8Row, &a.xmap, k, at, bar);
                 }
             }
             if (!ok)                             // aborted: the last copies into each stage
@@ -536,6 +543,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
         F8Ring<kF8ScaleSteps> sc;
         int e = 0;
         bool ok = true;
+        grid_dependency_wait();                  // the results may be in use
         for (int t = blockIdx.x; t < total; t += gridDim.x) {
             const Fp8Tile tile = fp8_tile(c, groups, t, e, kF8Tile, cols, false);
             e = tile.e;
@@ -770,6 +778,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
             F8Ring<kStages> in;
             int seq = 0, e = 0;
             bool ok = true;
+            const int late = c.offsets ? 0 : min(kStages, KB);   // (as in fp8_rows_kernel)
             for (int t = t0; t < total && ok; t += dt) {
                 const Fp8Tile tile = fp8_tile(c, groups, t, e, BN, cols, true);
                 e = tile.e;
@@ -786,7 +795,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
 #pragma unroll
                         for (int g = 0; g < kParts; ++g)
                             tma_load_3d(wa + g * kF8Tile * kF8Row, &a.wmap[g], k, tile.col * kF8Tile, tile.e, bar);
-                        if (!c.rows) f8_copy_2d(xa, &a.xmap, k, tile.row0, bar);
+                        if (seq >= late && !c.rows) f8_copy_2d(xa, &a.xmap, k, tile.row0, bar);
+                        if (seq + 1 == late) {
+                            grid_dependency_wait();
+                            for (int j = 0; j < late; ++j)
+                                f8_copy_2d(smem_u32(ring) + j * Geo::kStageBytes + kParts * kF8Tile * kF8Row, &a.xmap,
+                                           (k0 + j) * kFp8Block, tile.row0, full0 + 8 * j);
+                        }
                     }
                     __syncwarp();
                     if (lane < fours) f8_gather4(xa + 4 * lane * kF8Row, &a.xmap, k, at, bar);
@@ -842,6 +857,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16) + half * kMine;
         int step = 0, sstep = 0, e = 0;
         bool ok = true;
+        grid_dependency_wait();                  // the results may be in use
         for (int t = t0; t < total; t += dt) {
             const Fp8Tile tile = fp8_tile(c, groups, t, e, BN, cols, true);
             e = tile.e;
@@ -948,6 +964,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
     }
     if (split > 1) {
         // a warp a row: the blocks' sums of its 128 columns, four a lane
+        grid_dependency_wait();
         cluster_sync_all();
         if (t0 < total && !flags[0]) {
             const Fp8Tile tile = fp8_tile(c, groups, t0, 0, BN, cols, true);

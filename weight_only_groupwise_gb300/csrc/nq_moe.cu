@@ -18,24 +18,29 @@ namespace cg = cooperative_groups;
 // ---------------------------------------------------------------- router
 
 // Choice of experts: a warp a token, expert 32 v + lane in the lane's register v. Logits become whole numbers of
-// the same order, so that a round is one redux for the largest and one for the lowest index that has it.
+// the same order. The k-th largest of the lanes' largest is a bound below which nothing is chosen; what is not below it, a
+// few more than k, goes to a lane each, which counts those before it. (A round a choice, each a search of all registers and two
+// reductions, took 18 us for 16384 tokens x 256.) Where more than 32 are left (equal logits), rounds.
 //
-// With a bias the order is that of sigmoid(l) + b in 64 bits, which this GPU has few units for. It is computed in 32 bits with
-// an error below kRtTol (1 + |value|), and only where two neighbours of the chosen (or the best of the others) are
-// nearer than that, and not the same number twice, is the token done again in 64.
+// With a bias the order is that of sigmoid(l) + b in 64 bits, which this GPU has few units for (an exponential takes a warp
+// some 2 us). Values in 32 bits are off by less than half of kRtTol (1 + |value|): the fast exponential by 2^-22 and |l|
+// 2^-23 of itself, which reach the sigmoid times s (1 - s) <= 1/4 and |l| s (1 - s) < 1/4, the quotient by 2^-22, the bias's
+// addition by 2^-24 of the value: 2^-21 (1 + |value|) together. Only where neighbours among the chosen and the best of the others
+// are nearer than kRtTol (1 + |value|) are the candidates settled in 64 bits; those near the bound are among them.
 //
-// Places: a stable counting sort by expert, by one cluster of blocks, each with a share of the tokens in order. A
-// block counts its tokens' choices, the blocks exchange their counts, and each finds its tokens' places from a
-// bit set of tokens for each expert (the tokens before this one that chose it: a population count), so that no
-// order of atomics shows. Calls of few tokens choose and place in one launch.
+// Places: a stable counting sort by expert, by one cluster of blocks, each with a share of the tokens in order, cut
+// into a run for each warp. Warps count their runs' choices, the blocks exchange their counts, and each warp goes through its
+// run again, 32 choices at a time: a choice's place is its expert's next, plus those of the lanes before it with the same
+// expert. No order of atomics shows. (Bit sets of tokens for each expert instead took 36 us for 16384 x 8 of 256.)
+// Calls of few tokens choose and place in one launch.
 
 constexpr int kRtThreads = 1024;
 constexpr int kRtWarps = kRtThreads / 32;
 constexpr int kRtCluster = 8;                    // blocks of the placing cluster
+constexpr int kRtFew = 64;                       // tokens up to which one launch chooses and places
 constexpr int kRtChooseThreads = 256;            // of a choosing block of a large call
 constexpr int kRtMostChosen = 32;
 constexpr int kRtMostTokens = 1 << 20;
-constexpr int kRtBits = 24576;                   // words of bit sets in shared memory
 constexpr float kRtTol = 0x1p-20f;
 
 struct RouteArgs {
@@ -52,7 +57,6 @@ struct RouteArgs {
     int dtype;
     bool sigmoid, normalize;
     int share;                                   // tokens of a block of the placing cluster
-    int words;                                   // of a bit set: tokens of a pass / 32
 };
 
 __device__ __forceinline__ float route_load(const void* p, long long i, int dtype) {
@@ -79,32 +83,60 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// The choice of one token in 64 bits: lane j gets the j-th expert, or -1.
+// sigmoid(l) + b in 64 bits as a whole number of the same order (0: not above -inf).
+__device__ __noinline__ uint64_t route_key_64(float l, float b) {
+    const double v = 1.0 / (1.0 + exp(-(double)l)) + (double)b;
+    if (!(l > -INFINITY) || !(v > -INFINITY)) return 0;
+    const uint64_t bits = (uint64_t)__double_as_longlong(v + 0.0);
+    return (bits >> 63) ? ~bits : bits | (1ull << 63);
+}
+
+// The choice of one token in 64 bits among one candidate a lane (-1: none): lane j gets the j-th, or -1.
+__device__ __forceinline__ int route_settle(const RouteArgs& a, long long row, int candidate) {
+    const int lane = threadIdx.x & 31;
+    uint64_t key = 0;
+    if (candidate >= 0) key = route_key_64(route_load(a.logits, row + candidate, a.dtype), __ldg(a.bias + candidate));
+    int rank = key ? 0 : 32;
+    for (int i = 0; i < 32; ++i) {
+        const uint64_t other = __shfl_sync(0xFFFFFFFFu, key, i);
+        const int e = __shfl_sync(0xFFFFFFFFu, candidate, i);
+        if (key && other && (other > key || (other == key && e < candidate))) ++rank;
+    }
+    int mine = -1;
+    for (int j = 0; j < a.k; ++j) {
+        const unsigned who = __ballot_sync(0xFFFFFFFFu, rank == j);
+        if (!who) break;
+        const int e = __shfl_sync(0xFFFFFFFFu, candidate, __ffs(who) - 1);
+        if (lane == j) mine = e;
+    }
+    return mine;
+}
+
+// The same among all experts, a round a choice: where more than 32 are near (with a bias: in 64 bits throughout).
 template <int V>
-__device__ __noinline__ int route_choose_64(const RouteArgs& a, long long row) {
+__device__ __noinline__ int route_rounds(const RouteArgs& a, long long row) {
     const int lane = threadIdx.x & 31;
     uint32_t taken = 0;
     int mine = -1;
     for (int j = 0; j < a.k; ++j) {
-        double best = -INFINITY;
+        uint64_t best = 0;
         int at = -1;
         for (int v = 0; v < V; ++v) {
             const int e = 32 * v + lane;
             if (e >= a.E || ((taken >> v) & 1)) continue;
             const float l = route_load(a.logits, row + e, a.dtype);
-            if (!(l > -INFINITY)) continue;
-            const double s = 1.0 / (1.0 + exp(-(double)l)) + (double)__ldg(a.bias + e);
-            if (s > best) {
-                best = s;
+            const uint64_t key = a.bias ? route_key_64(l, __ldg(a.bias + e)) : route_key(l);
+            if (key > best) {
+                best = key;
                 at = e;
             }
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
-            const double s = __shfl_xor_sync(0xFFFFFFFFu, best, d);
+            const uint64_t key = __shfl_xor_sync(0xFFFFFFFFu, best, d);
             const int e = __shfl_xor_sync(0xFFFFFFFFu, at, d);
-            if (e >= 0 && (at < 0 || s > best || (s == best && e < at))) {
-                best = s;
+            if (e >= 0 && (at < 0 || key > best || (key == best && e < at))) {
+                best = key;
                 at = e;
             }
         }
@@ -115,9 +147,15 @@ __device__ __noinline__ int route_choose_64(const RouteArgs& a, long long row) {
     return mine;
 }
 
+// A warp's shared memory: the lanes' largest, the candidates (key, expert), and in order.
+struct RouteWarp {
+    uint32_t largest[32];
+    uint2 near[32], order[32];
+};
+
 // Chooses token t's experts and writes them with their weights.
 template <int V>
-__device__ __forceinline__ void route_choose(const RouteArgs& a, int t) {
+__device__ __forceinline__ void route_choose(const RouteArgs& a, int t, RouteWarp& sm) {
     const int lane = threadIdx.x & 31;
     const long long row = (long long)t * a.stride;
     float l[V];
@@ -128,45 +166,65 @@ __device__ __forceinline__ void route_choose(const RouteArgs& a, int t) {
         l[v] = e < a.E ? route_load(a.logits, row + e, a.dtype) : -INFINITY;
     }
     const bool biased = a.bias != nullptr;
+    uint32_t m = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = 32 * v + lane;
         float f = l[v];
-        if (biased && e < a.E && f > -INFINITY) f = sigmoid_f(f) + __ldg(a.bias + e);
+        if (biased && e < a.E && f > -INFINITY) f = __fdividef(1.f, 1.f + __expf(-f)) + __ldg(a.bias + e);
         key[v] = route_key(f);
+        m = max(m, key[v]);
     }
+    // the bound: as many lanes as are chosen (with a bias, one more) have something that is not below it
+    const int want = biased ? a.k + 1 : a.k;
+    sm.largest[lane] = m;
+    __syncwarp();
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(sm.largest + i);
+        before += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
+    }
+    // (lanes with equal values count alike: the smallest of those with fewer than `want` before them)
+    uint32_t bound = __reduce_min_sync(0xFFFFFFFFu, before < want ? m : 0xFFFFFFFFu);
+    if (want > 32) bound = 0;
+    if (biased && bound) {
+        const float f = route_value(bound);
+        bound = route_key(f - 2.f * kRtTol * (1.f + fabsf(f)));
+    }
+    bound = max(bound, 1u);
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const unsigned who = __ballot_sync(0xFFFFFFFFu, key[v] >= bound);
+        const int at = n + __popc(who & ((1u << lane) - 1));
+        if (key[v] >= bound && at < 32) sm.near[at] = make_uint2(key[v], 32 * v + lane);
+        n += __popc(who);
+    }
+    __syncwarp();
     int mine = -1;                               // lane j: the j-th choice
-    float value = 0.f;                           // biased: its value
-    uint32_t first = 0, last = 0;
-    bool unsure = false;
-    const int rounds = biased ? a.k + 1 : a.k;
-    for (int j = 0; j < rounds; ++j) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) m = max(m, key[v]);
-        m = __reduce_max_sync(0xFFFFFFFFu, m);
-        if (m == 0) break;
-        uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-        for (int v = V - 1; v >= 0; --v)
-            if (key[v] == m) at = 32 * v + lane;
-        at = __reduce_min_sync(0xFFFFFFFFu, at);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (at == 32 * v + lane) key[v] = 0;
-        if (biased && j > 0) {
-            // (the same number twice, a tie in any precision, is left to 64 bits too: what follows it could pass both)
-            const float hi = route_value(last), lo = route_value(m);
-            unsure = unsure || !(hi - lo > kRtTol * (1.f + fabsf(hi)));
+    if (n <= 32) {
+        const uint2 c = lane < n ? sm.near[lane] : make_uint2(0, 0);
+        int rank = 0;
+        for (int i = 0; i < n; ++i) {
+            const uint2 o = sm.near[i];
+            rank += o.x > c.x || (o.x == c.x && o.y < c.y);
         }
-        last = m;
-        if (j == 0) first = m;
-        if (lane == j && j < a.k) {
-            mine = (int)at;
-            value = route_value(m);
+        if (lane < n) sm.order[rank] = c;
+        __syncwarp();
+        mine = lane < min(n, a.k) ? (int)sm.order[lane].y : -1;
+        if (biased) {
+            bool unsure = false;
+            if (lane < a.k && lane + 1 < n) {
+                const float hi = route_value(sm.order[lane].x), lo = route_value(sm.order[lane + 1].x);
+                unsure = !(hi - lo > kRtTol * (1.f + fabsf(hi)));
+            }
+            if (__any_sync(0xFFFFFFFFu, unsure)) mine = route_settle(a, row, lane < n ? (int)c.y : -1);
         }
+    } else {
+        mine = route_rounds<V>(a, row);
     }
-    if (biased && unsure) mine = route_choose_64<V>(a, row);
+    __syncwarp();                                // the warp's next token uses the same memory
     // weights of the chosen
     const float c = mine >= 0 ? route_load(a.logits, row + mine, a.dtype) : -INFINITY;
     float w;
@@ -182,7 +240,7 @@ __device__ __forceinline__ void route_choose(const RouteArgs& a, int t) {
             if (mine >= 0) w = w / sum;
         }
     } else {
-        const float top = route_value(first);
+        const float top = __shfl_sync(0xFFFFFFFFu, c, 0);
         w = mine < 0 ? 0.f : (c == top ? 1.f : expf(c - top));
         float sum;
         if (a.normalize) {
@@ -200,26 +258,40 @@ __device__ __forceinline__ void route_choose(const RouteArgs& a, int t) {
         a.ids[(long long)t * a.k + lane] = mine;
         a.weights[(long long)t * a.k + lane] = w * a.scale;
     }
-    (void)value;
 }
 
-// Places of the tokens' rows, by a cluster of blocks (see above). Shared memory: counts of the block [E], places
-// [E], then bit sets [E][words] and their running counts [E][words].
+// Places of the tokens' rows, by a cluster of blocks (see above). Shared memory: the block's counts [E], and of each
+// warp its counts and then next places [warps][E].
+constexpr int kRtOnce = 8;                       // choices of a lane that are loaded at once
 __device__ __forceinline__ void route_place(const RouteArgs& a, int* sm) {
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), blocks = (int)cl.num_blocks(), tid = threadIdx.x;
+    const int lane = tid & 31, warp = tid >> 5;
     int* const count = sm;
-    int* const place = sm + a.E;
-    uint32_t* const bits = reinterpret_cast<uint32_t*>(sm + 2 * a.E);
-    int* const before = reinterpret_cast<int*>(bits + (size_t)a.E * a.words);
+    int* const next = sm + a.E;
+    int* const my_next = next + warp * a.E;
     __shared__ int warp_total[kRtWarps];
     const int t0 = min(a.T, rank * a.share), t1 = min(a.T, t0 + a.share);
-    const int total = a.T * a.k;
-    for (int e = tid; e < a.E; e += kRtThreads) count[e] = 0;
+    // the warp's run of tokens
+    const int run = (a.share + kRtWarps - 1) / kRtWarps;
+    const int r0 = min(t1, t0 + warp * run) * a.k, r1 = min(t1, t0 + (warp + 1) * run) * a.k;
+    for (int i = tid; i < kRtWarps * a.E; i += kRtThreads) next[i] = 0;
     __syncthreads();
-    for (int i = t0 * a.k + tid; i < t1 * a.k; i += kRtThreads) {
-        const int e = a.ids[i];
-        if (e >= 0) atomicAdd(count + e, 1);
+    for (int i0 = r0 + lane; i0 < r1; i0 += 32 * kRtOnce) {
+        int e[kRtOnce];
+#pragma unroll
+        for (int j = 0; j < kRtOnce; ++j) e[j] = i0 + 32 * j < r1 ? a.ids[i0 + 32 * j] : -1;
+#pragma unroll
+        for (int j = 0; j < kRtOnce; ++j)
+            if (e[j] >= 0) atomicAdd(my_next + e[j], 1);
+    }
+    __syncthreads();
+    // (at most 512 experts, one a thread)
+    if (tid < a.E) {
+        int sum = 0;
+#pragma unroll 8
+        for (int w = 0; w < kRtWarps; ++w) sum += next[w * a.E + tid];
+        count[tid] = sum;
     }
     cl.sync();
     // experts' totals and the rows of the blocks before this one
@@ -230,9 +302,7 @@ __device__ __forceinline__ void route_place(const RouteArgs& a, int* sm) {
             if (b < rank) ahead += c;
             mine += c;
         }
-    // scan over experts: at most 512, one a thread
     int upto = mine;
-    const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         const int u = __shfl_up_sync(0xFFFFFFFFu, upto, d);
@@ -248,64 +318,62 @@ __device__ __forceinline__ void route_place(const RouteArgs& a, int* sm) {
         all += c;
     }
     if (tid < a.E) {
-        place[tid] = base + upto - mine + ahead;
+        int at = base + upto - mine;
         if (rank == 0) {
-            a.offsets[tid] = base + upto - mine;
+            a.offsets[tid] = at;
             if (tid == a.E - 1) a.offsets[a.E] = all;
+        }
+        at += ahead;
+#pragma unroll 8
+        for (int w = 0; w < kRtWarps; ++w) {
+            const int c = next[w * a.E + tid];
+            next[w * a.E + tid] = at;
+            at += c;
         }
     }
     // the entries behind the last row
-    for (int i = all + rank * kRtThreads + tid; i < total; i += blocks * kRtThreads) a.rows[i] = -1;
-    const int pass = 32 * a.words;
-    for (int p0 = t0; p0 < t1; p0 += pass) {
-        const int p1 = min(t1, p0 + pass);
-        for (int i = tid; i < a.E * a.words; i += kRtThreads) bits[i] = 0;
-        __syncthreads();
-        for (int i = p0 * a.k + tid; i < p1 * a.k; i += kRtThreads) {
-            const int e = a.ids[i], t = i / a.k - p0;
-            if (e >= 0) atomicOr(bits + e * a.words + (t >> 5), 1u << (t & 31));
-        }
-        __syncthreads();
-        for (int e = tid; e < a.E; e += kRtThreads) {
-            int n = place[e];
-            for (int w = 0; w < a.words; ++w) {
-                before[e * a.words + w] = n;
-                n += __popc(bits[e * a.words + w]);
-            }
-            place[e] = n;
-        }
-        __syncthreads();
-        for (int i = p0 * a.k + tid; i < p1 * a.k; i += kRtThreads) {
-            const int e = a.ids[i], token = i / a.k, t = token - p0;
+    for (int i = all + rank * kRtThreads + tid; i < a.T * a.k; i += blocks * kRtThreads) a.rows[i] = -1;
+    __syncthreads();
+    for (int b0 = r0; b0 < r1; b0 += 32 * kRtOnce) {
+        int e[kRtOnce];
+#pragma unroll
+        for (int j = 0; j < kRtOnce; ++j) e[j] = b0 + 32 * j + lane < r1 ? a.ids[b0 + 32 * j + lane] : -1;
+#pragma unroll
+        for (int j = 0; j < kRtOnce; ++j) {
+            const int i = b0 + 32 * j + lane;
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, e[j]);
             int at = -1;
-            if (e >= 0) {
-                const int w = e * a.words + (t >> 5);
-                at = before[w] + __popc(bits[w] & ((1u << (t & 31)) - 1));
-                a.rows[at] = token;
+            if (e[j] >= 0) at = my_next[e[j]] + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (e[j] >= 0) {
+                if ((same >> lane) == 1) my_next[e[j]] = at + 1;     // the last of the same
+                a.rows[at] = i / a.k;
             }
-            a.slots[i] = at;
+            __syncwarp();
+            if (i < r1) a.slots[i] = at;
         }
-        __syncthreads();
     }
     cl.sync();                                   // no block leaves while another reads its counts
 }
 
 template <int V>
 __global__ void __launch_bounds__(kRtChooseThreads) route_choose_kernel(const RouteArgs a) {
-    const int t = blockIdx.x * (kRtChooseThreads / 32) + (threadIdx.x >> 5);
+    __shared__ __align__(16) RouteWarp sm[kRtChooseThreads / 32];
+    const int warp = threadIdx.x >> 5, t = blockIdx.x * (kRtChooseThreads / 32) + warp;
     grid_launch_dependents();
     grid_dependency_wait();
-    if (t < a.T) route_choose<V>(a, t);
+    if (t < a.T) route_choose<V>(a, t, sm[warp]);
 }
 
 template <int V>
 __global__ void __launch_bounds__(kRtThreads, 1) route_few_kernel(const RouteArgs a) {
     extern __shared__ int route_smem[];
-    const int rank = (int)cluster_rank();
+    __shared__ __align__(16) RouteWarp sm[kRtWarps];
+    const int rank = (int)cluster_rank(), warp = threadIdx.x >> 5;
     grid_launch_dependents();
     grid_dependency_wait();
     const int t0 = min(a.T, rank * a.share), t1 = min(a.T, t0 + a.share);
-    for (int t = t0 + (threadIdx.x >> 5); t < t1; t += kRtWarps) route_choose<V>(a, t);
+    for (int t = t0 + warp; t < t1; t += kRtWarps) route_choose<V>(a, t, sm[warp]);
     __syncthreads();
     route_place(a, route_smem);
 }
@@ -319,19 +387,18 @@ __global__ void __launch_bounds__(kRtThreads, 1) route_place_kernel(const RouteA
 
 template <int V>
 cudaError_t route_launch(RouteArgs a, cudaStream_t stream, bool pdl) {
-    // one launch while a warp of the cluster has few tokens
-    const bool few = a.T <= kRtCluster * kRtWarps * 2;
-    const int blocks = few ? min(kRtCluster, (a.T + kRtWarps - 1) / kRtWarps) : kRtCluster;
+    const bool few = a.T <= kRtFew;
+    const int blocks = few ? (a.T + kRtWarps - 1) / kRtWarps : min(kRtCluster, (a.T + kRtWarps - 1) / kRtWarps);
     a.share = (a.T + blocks - 1) / blocks;
-    a.words = min((a.share + 31) / 32, max(1, kRtBits / a.E));
-    const size_t smem = (size_t)(2 * a.E + 2 * a.E * a.words) * 4;
+    const size_t smem = (size_t)(kRtWarps + 1) * a.E * 4;
     const void* kern = few ? (const void*)route_few_kernel<V> : (const void*)route_place_kernel;
-    if (smem > 40 * 1024) {
+    if (smem > 24 * 1024) {
         static thread_local int set_for_device[2] = {-1, -1};
         int dev = 0;
         cudaGetDevice(&dev);
         if (set_for_device[few] != dev) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 208 * 1024);
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (kRtWarps + 1) * kMostExperts * 4);
             if (e != cudaSuccess) return e;
             set_for_device[few] = dev;
         }
