@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "nq.h"
 #include "nq_common.cuh"
 #include "nq_fp8.h"
@@ -36,7 +38,10 @@ namespace cg = cooperative_groups;
 
 constexpr int kRtThreads = 1024;
 constexpr int kRtWarps = kRtThreads / 32;
-constexpr int kRtCluster = 8;                    // blocks of the placing cluster
+// Blocks of the placing cluster: as many as are always there, or, for many tokens, 16 where the GPU takes such clusters
+// (16384 x 8 of 256: 35.5 us with 8 blocks, 27.6 with 16).
+constexpr int kRtCluster = 8, kRtClusterMany = 16;
+constexpr int kRtMany = 4096;                    // tokens from which on
 constexpr int kRtFew = 64;                       // tokens up to which one launch chooses and places
 constexpr int kRtChooseThreads = 256;            // of a choosing block of a large call
 constexpr int kRtMostChosen = 32;
@@ -385,10 +390,41 @@ __global__ void __launch_bounds__(kRtThreads, 1) route_place_kernel(const RouteA
     route_place(a, route_smem);
 }
 
+// Whether a cluster of kRtClusterMany blocks can run (queried once).
+bool route_wide_clusters() {
+    static std::once_flag once;
+    static int n = 0;
+    std::call_once(once, [] {
+        if (cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (kRtWarps + 1) * kMostExperts * 4) != cudaSuccess) {
+            cudaGetLastError();
+            return;
+        }
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kRtClusterMany);
+        cfg.blockDim = dim3(kRtThreads);
+        cfg.dynamicSmemBytes = (kRtWarps + 1) * kMostExperts * 4;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kRtClusterMany;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, route_place_kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+    });
+    return n > 0;
+}
+
 template <int V>
 cudaError_t route_launch(RouteArgs a, cudaStream_t stream, bool pdl) {
     const bool few = a.T <= kRtFew;
-    const int blocks = few ? (a.T + kRtWarps - 1) / kRtWarps : min(kRtCluster, (a.T + kRtWarps - 1) / kRtWarps);
+    int blocks = few ? (a.T + kRtWarps - 1) / kRtWarps : min(kRtCluster, (a.T + kRtWarps - 1) / kRtWarps);
+    if (a.T >= kRtMany && route_wide_clusters()) blocks = kRtClusterMany;
     a.share = (a.T + blocks - 1) / blocks;
     const size_t smem = (size_t)(kRtWarps + 1) * a.E * 4;
     const void* kern = few ? (const void*)route_few_kernel<V> : (const void*)route_place_kernel;
