@@ -581,7 +581,8 @@ nq_status nq_quant_fp8(const void* x, int dtype, long long x_stride, int rows, i
  * products g = x wg and u = x wu.
  *   K a multiple of 16, 16 <= K <= 2^20; 1 <= N <= 2^20; rows <= 2^24. Nothing may overlap the result.
  * As the projections above, these two start reading the weights' codes (not their scales) before the preceding kernel has
- * ended: the codes must not be written by a kernel that lets its dependents start before its writes are done.
+ * ended: the codes must not be written by a kernel that lets its dependents start before its writes are done (nq_quant_fp8
+ * does not; the products do: the codes that one writes are rows for the call behind it, not weights).
  */
 nq_status nq_gemm_fp8(const nq_fp8_rows* x, const nq_fp8_weight* w, const nq_fp8_out* y, int K, int N, void* stream);
 nq_status nq_swiglu_fp8(const nq_fp8_rows* x, const nq_fp8_weight* wg, const nq_fp8_weight* wu, const nq_fp8_out* h,

@@ -463,6 +463,12 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
             int seq = 0, e = 0;
             bool ok = true;
             const int late = c.offsets ? 0 : min(kStages, KB);
+            auto x_late = [&](int n) {           // rows of x of the first n stages, of a dense call's first tile
+                const Fp8Tile tile = fp8_tile(c, groups, blockIdx.x, 0, kF8Tile, cols, false);
+                grid_dependency_wait();
+                for (int j = 0; j < n; ++j)
+                    f8_copy_2d(smem_u32(ring) + j * Geo::kStageBytes, &a.xmap, j * kFp8Block, tile.row0, full0 + 8 * j);
+            };
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 const Fp8Tile tile = fp8_tile(c, groups, t, e, kF8Tile, cols, false);
                 e = tile.e;
@@ -480,16 +486,13 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
                         if (GLU) tma_load_3d(wa + 128 * kF8Row, &a.wmap[1], k, tile.col * 128, tile.e, bar);
                         // (the first stages' weights are on their way before the preceding kernel has ended: late)
                         if (seq >= late && !c.rows) f8_copy_2d(xa, &a.xmap, k, tile.row0, bar);
-                        if (seq + 1 == late) {
-                            grid_dependency_wait();
-                            for (int j = 0; j < late; ++j)
-                                f8_copy_2d(smem_u32(ring) + j * Geo::kStageBytes, &a.xmap, j * kFp8Block, tile.row0, full0 + 8 * j);
-                        }
+                        if (seq + 1 == late) x_late(late);
                     }
                     __syncwarp();
                     if (lane < fours) f8_gather4(xa + 4 * lane * kF8Row, &a.xmap, k, at, bar);
                 }
             }
+            if (!ok && lane == 0 && seq < late) x_late(seq);
             if (!ok)                             // aborted: the last copies into each stage
                 for (int j = seq > kStages ? seq - kStages : 0; j < seq; ++j)
                     mbar_wait_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kDrainNs);
@@ -779,6 +782,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
             int seq = 0, e = 0;
             bool ok = true;
             const int late = c.offsets ? 0 : min(kStages, KB);   // (as in fp8_rows_kernel)
+            auto x_late = [&](int n) {
+                const Fp8Tile tile = fp8_tile(c, groups, t0, 0, BN, cols, true);
+                grid_dependency_wait();
+                for (int j = 0; j < n; ++j)
+                    f8_copy_2d(smem_u32(ring) + j * Geo::kStageBytes + kParts * kF8Tile * kF8Row, &a.xmap, (k0 + j) * kFp8Block,
+                               tile.row0, full0 + 8 * j);
+            };
             for (int t = t0; t < total && ok; t += dt) {
                 const Fp8Tile tile = fp8_tile(c, groups, t, e, BN, cols, true);
                 e = tile.e;
@@ -796,17 +806,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
                         for (int g = 0; g < kParts; ++g)
                             tma_load_3d(wa + g * kF8Tile * kF8Row, &a.wmap[g], k, tile.col * kF8Tile, tile.e, bar);
                         if (seq >= late && !c.rows) f8_copy_2d(xa, &a.xmap, k, tile.row0, bar);
-                        if (seq + 1 == late) {
-                            grid_dependency_wait();
-                            for (int j = 0; j < late; ++j)
-                                f8_copy_2d(smem_u32(ring) + j * Geo::kStageBytes + kParts * kF8Tile * kF8Row, &a.xmap,
-                                           (k0 + j) * kFp8Block, tile.row0, full0 + 8 * j);
-                        }
+                        if (seq + 1 == late) x_late(late);
                     }
                     __syncwarp();
                     if (lane < fours) f8_gather4(xa + 4 * lane * kF8Row, &a.xmap, k, at, bar);
                 }
             }
+            if (!ok && lane == 0 && seq < late) x_late(seq);
             if (!ok)
                 for (int j = seq > kStages ? seq - kStages : 0; j < seq; ++j)
                     mbar_wait_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kDrainNs);

@@ -71,7 +71,7 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
 template <int DTYPE>
 __global__ void __launch_bounds__(kQtThreads) quant_kernel(const QuantArgs a) {
     const long long at = (long long)blockIdx.x * (kQtThreads / 32) + (threadIdx.x >> 5);
-    grid_launch_dependents();
+    // (the next kernel is not let start early: a product reads its weights' codes without waiting for what has been)
     grid_dependency_wait();
     if (at >= a.total) return;
     const int lane = threadIdx.x & 31;
