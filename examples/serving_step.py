@@ -2,10 +2,11 @@
 projections, page tables, KV append, paged attention and sampling, in the order a server makes
 them. Random weights; norms, rotary positions and the embedding lookup are plain torch.
 
-    python examples/serving_step.py
+    python examples/serving_step.py [--experts 16]
 
 serves four requests: their prompts in chunks (a step holds up to 64 tokens, what a projection
 call takes), then decode steps in which every request draws its next token with its own settings.
+With experts, the SwiGLU blocks are layers of experts with 8-bit weights, each token taking the best two.
 All lengths, tables and settings stay on the GPU; only the tokens come back.
 """
 from __future__ import annotations
@@ -32,18 +33,41 @@ def packed(bits: int, K: int, N: int, g):
     return nq.pack_q4(word(K // 8), s, K, N) if bits == 4 else nq.pack_q5(word(K // 8), word(K // 32), s, K, N)
 
 
-class Decoder:
-    """Layers of grouped-query attention (5-bit projections) and a SwiGLU block (4-bit)."""
+def coded(E: int, N: int, K: int, g):
+    """Random 8-bit weights of E experts with their block scales, outputs of about unit variance for unit inputs."""
+    codes = (105 * torch.randn((E, N, K), device="cuda", generator=g)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    return codes, torch.full((E, -(-N // 128), -(-K // 128)), K ** -0.5 / 105, device="cuda")
 
-    def __init__(self, layers=2, hidden=1024, heads=8, kv_heads=2, dim=128, inner=2816, vocab=32000, seed=0):
+
+class Decoder:
+    """Layers of grouped-query attention (5-bit projections) and a SwiGLU block (4-bit), or `experts` of them
+    (8-bit) of which each token takes `chosen`."""
+
+    def __init__(self, layers=2, hidden=1024, heads=8, kv_heads=2, dim=128, inner=2816, vocab=32000, seed=0, experts=0, chosen=2):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.heads, self.kv_heads, self.dim, self.inner, self.hidden, self.vocab = heads, kv_heads, dim, inner, hidden, vocab
+        self.experts, self.chosen = experts, chosen
         self.embed = torch.randn((vocab, hidden), device="cuda", generator=g).to(torch.bfloat16)
         self.layers = [{"q": packed(5, hidden, heads * dim, g), "k": packed(5, hidden, kv_heads * dim, g),
                         "v": packed(5, hidden, kv_heads * dim, g), "o": packed(5, heads * dim, hidden, g),
-                        "gate": packed(4, hidden, inner, g), "up": packed(4, hidden, inner, g),
-                        "down": packed(4, inner, hidden, g)} for _ in range(layers)]
+                        **self.block(g)} for _ in range(layers)]
         self.head = packed(4, hidden, vocab, g)
+
+    def block(self, g):
+        E, hidden, inner = self.experts, self.hidden, self.inner
+        if E:
+            return {"router": packed(5, hidden, E, g), "gate": coded(E, inner, hidden, g), "up": coded(E, inner, hidden, g),
+                    "down": coded(E, hidden, inner, g)}
+        return {"gate": packed(4, hidden, inner, g), "up": packed(4, hidden, inner, g), "down": packed(4, inner, hidden, g)}
+
+    def feed(self, x, w):
+        """x plus its SwiGLU block, or plus its experts'."""
+        h = self.norm(x)
+        if not self.experts:
+            return x + nq.gemm_q4(nq.swiglu_q4(h, *w["gate"], *w["up"], self.inner), *w["down"], self.hidden)
+        _, weights, offsets, rows, slots = nq.moe_route(nq.gemm_q5(h, *w["router"], self.experts), self.chosen)
+        inner = nq.swiglu_fp8_experts(*nq.quant_fp8(h), *w["gate"], *w["up"], offsets, rows=rows, dtype=torch.float8_e4m3fn)
+        return nq.moe_combine(nq.gemm_fp8_experts(*inner, *w["down"], offsets), slots, weights, base=x)
 
     @staticmethod
     def norm(x):
@@ -69,8 +93,7 @@ class Decoder:
             nq.kv_append(k, v.view(-1, self.kv_heads, self.dim), slots, k_cache, v_cache)
             a = nq.attn_paged(q, k_cache, v_cache, table, q_start, kv_lens)
             x = x + nq.gemm_q5(a.view(-1, self.heads * self.dim), *w["o"], self.hidden)
-            h = nq.swiglu_q4(self.norm(x), *w["gate"], *w["up"], self.inner)
-            x = x + nq.gemm_q4(h, *w["down"], self.hidden)
+            x = self.feed(x, w)
         return nq.gemm_q4(self.norm(x), *self.head, self.vocab)
 
 
@@ -119,8 +142,8 @@ class Server:
         return torch.stack(tokens, 1)
 
 
-def main():
-    model = Decoder()
+def main(experts: int = 0):
+    model = Decoder(experts=experts, inner=768 if experts else 2816)
     server = Server(model, 4)
     g = torch.Generator(device="cuda").manual_seed(1)
     prompts = [torch.randint(0, model.vocab, (n,), device="cuda", generator=g) for n in (5, 70, 130, 33)]
@@ -137,4 +160,4 @@ def main():
 
 
 if __name__ == "__main__":
-    main()
+    main(int(sys.argv[2]) if sys.argv[1:2] == ["--experts"] else 0)

@@ -235,3 +235,21 @@ def test_a_layer_of_experts(T, g):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(captured, layer()[0])
+
+
+def test_a_decoder_with_experts(capsys):
+    """The example's decoder with layers of experts: the same prompts and draws twice give the same tokens."""
+    from examples import serving_step as ex
+    model = ex.Decoder(layers=2, hidden=512, heads=8, kv_heads=2, dim=64, inner=384, vocab=2048, experts=32, chosen=4)
+    tokens = []
+    for _ in range(2):
+        draw = torch.Generator(device="cuda").manual_seed(5)
+        prompts = [torch.randint(0, 2048, (n,), device="cuda", generator=draw) for n in (3, 70, 129)]
+        server = ex.Server(model, 3, blocks=40, page=16, most_blocks=12)
+        logits = server.prompt(prompts, 21)
+        assert bool(logits.isfinite().all()) and float(logits.float().std()) > 0.1
+        tokens.append(server.generate(logits, 6, draw, temperature=torch.tensor([0.0, 0.8, 1.0], device="cuda")))
+        assert server.lens.tolist() == [9, 76, 135]
+    assert torch.equal(*tokens) and int(tokens[0].min()) >= 0
+    ex.main(16)
+    assert "blocks left" in capsys.readouterr().out
