@@ -264,3 +264,12 @@ def test_empty_calls(g):
     rows = torch.zeros(5, dtype=torch.int32, device="cuda")
     ends = torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda")
     assert bool((nq.gemm_fp8_experts(x[:0], xs[:0], w, ws, ends, rows=rows) == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("E,M,K,N", [(8, 200, 1040, 515), (16, 331, 256, 144), (40, 1280, 640, 272), (3, 96, 144, 1)])
+def test_sorted_rows_of_some_tens_an_expert(E, M, K, N, dtype, g):
+    """One expert has none, one two thirds of the rows."""
+    cuts = sorted(torch.randint(0, M // 3 + 1, (E - 2,), device="cuda", generator=g).tolist())
+    x, xs = ref.activations(M, K, g)
+    check_experts(x, xs * 2.0 ** -10, [ref.weights(E, N, K, g)], [0, 0, *cuts, M], None, dtype)

@@ -87,7 +87,7 @@ template <int BN, bool GLU>
 cudaError_t launch_cols(const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
     using Geo = Fp8ColsGeo<BN, GLU>;
     static thread_local int set = -1;
-    return fp8_launch(fp8_cols_kernel<BN, GLU>, set, dev, blocks, kF8Threads, Geo::smem(a.c.E), stream, pdl, a.c.split, a);
+    return fp8_launch(fp8_cols_kernel<BN, GLU>, set, dev, blocks, Geo::kThreads, Geo::smem(a.c.E), stream, pdl, a.c.split, a);
 }
 template <bool GLU>
 cudaError_t launch_cols_of(int bn, const Fp8Args& a, int dev, int blocks, cudaStream_t stream, bool pdl) {
@@ -143,7 +143,7 @@ const int* fp8_clusters(int sms) {
         for (int n = 2; n <= kF8MostSplit; ++n) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(sms / n * n);
-            cfg.blockDim = dim3(kF8Threads);
+            cfg.blockDim = dim3(Geo::kThreads);
             cfg.dynamicSmemBytes = (size_t)Geo::smem(1);
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -167,20 +167,23 @@ struct Fp8Plan {
     int rows, split;
 };
 
-// Rows a group on average up to which calls by expert go in tiles of 16 and 32 rows, plain and SwiGLU. Where weights of many
-// experts are read for few rows each, small tiles need fewer copies; 128 experts, us with tiles of 16, 32 rows and
-// fp8_rows_kernel: SwiGLU 2048 -> 768, 12 rows an expert 67.4, 70.8, 79.8; 24 rows 76.4, 70.8, 81.0; 32 rows 97, 88, 83; plain
-// 768 -> 2048, 6 rows 35.2, 39.9, 38.4; 12 rows 42.2, 41.7, 39.1; 24 rows 67.4, 50.4, 39.8.
-int fp8_experts_rows(int M, int E, bool glu) {
+// Rows a group on average up to which calls by expert go in small tiles. Where weights of many experts are read for few rows
+// each, these need fewer copies. SwiGLU, 128 experts of 2048 -> 768, us with tiles of 16, 32 rows and fp8_rows_kernel: 12
+// rows an expert 67.4, 70.8, 79.8; 24 rows 76.4, 70.8, 81.0; 32 rows 97, 88, 83. Plain, tiles of 16, 32, 64 rows and
+// fp8_rows_kernel: 128 experts of 768 -> 2048, 6 rows 35.2, 39.9, -, 38.4; 12 rows 42.2, 43.2, 40.3, 40.5; 28 rows 67, 56.1,
+// 41.9, 41.7; 64 experts, 24 rows -, 28.9, 22.9, 25.7; 56 rows -, 47.5, 30.2, 28.0; 256 of 2048 -> 4096, 20 rows -, 389, 321,
+// 332. Gathered rows of 64 take the copy engine longer than their weights, so that such plain calls leave them out.
+int fp8_experts_rows(int M, int E, bool glu, bool gathered) {
     const int each = (M + E - 1) / E;
-    return each <= (glu ? 16 : 10) ? 16 : glu && each <= 28 ? 32 : 0;
+    if (glu) return each <= 16 ? 16 : each <= 28 ? 32 : 0;
+    return each <= 10 ? 16 : each <= 32 && !gathered ? 64 : 0;
 }
 
 // A dense call: the fewest microseconds by a count of the blocks of K that the busiest SM goes through, at what one of them
 // takes each kernel (measured at K = 4096 and 5120; a tile's blocks of K, 128 columns or 256, are one after
 // another): few tiles leave SMs idle, large ones are cheaper a row. A launch takes 4 us, the exchange of a split sum 1.5.
-// 333 x 4112 x 2501, us: tiles of 64 rows 15.9, of 128 shared by two blocks 14.6, fp8_rows_kernel 25.8; 256 x 4096 x 5120:
-// 26.5, 18.3, 20.0; 512 x 5120 x 17408: 118, 75, 46.
+// 333 x 4112 x 2501, us: tiles of 64 rows 15.0, of 128 shared by two blocks 14.2, fp8_rows_kernel 28.4; 256 x 4096 x 5120:
+// 23.6, 16.5, 20.4; 512 x 5120 x 17408: 111, 67, 48.
 Fp8Plan fp8_dense_plan(int M, int K, int N, bool glu, int sms, const int* clusters) {
     static const struct {
         int rows;
@@ -207,7 +210,7 @@ Fp8Plan fp8_dense_plan(int M, int K, int N, bool glu, int sms, const int* cluste
 
 // Whether gathered rows are copied together first, where there is scratch memory: for fp8_rows_kernel, whose 128 rows a block
 // of K take the copy engine longer to gather than to multiply (4096 tokens x 8 of 64 experts: 1014 us, 497 so).
-bool fp8_gathers(int M, int E, bool glu) { return fp8_experts_rows(M, E, glu) == 0; }
+bool fp8_gathers(int M, int E, bool glu) { return fp8_experts_rows(M, E, glu, true) == 0; }
 long long scratch_stride(int K) { return (K + 15) / 16 * 16; }
 int scratch_scales(int K) { return ((K + kFp8Block - 1) / kFp8Block + 3) / 4 * 4; }
 
@@ -318,7 +321,7 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     c.wide = !mis(y->data, 16) && yst % 8 == 0;
     c.quads = !mis(x->scales, 16) && xss % 4 == 0;
     c.wait_ns = d.wait_ns;
-    const Fp8Plan plan = experts ? Fp8Plan{fp8_experts_rows(M, E, glu), 1} : fp8_dense_plan(M, K, N, glu, d.sms, fp8_clusters(d.sms));
+    const Fp8Plan plan = experts ? Fp8Plan{fp8_experts_rows(M, E, glu, rows != nullptr), 1} : fp8_dense_plan(M, K, N, glu, d.sms, fp8_clusters(d.sms));
     const int bn = plan.rows;
     const bool few = bn > 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -27,13 +27,6 @@
 
 namespace nq {
 
-constexpr int kF8Epilogue = 8;                   // epilogue warps of fp8_cols_kernel: 0..7, then
-constexpr int kF8Producer = 8, kF8Mma = 9, kF8Scales = 10;
-constexpr int kF8Threads = 12 * 32;              // (warp 11 only gives its registers away)
-// Registers a thread: a block begins with 168; warps 8..11 hand theirs to the epilogue's 128 sums and 64 loads:
-// 256 x 216 + 128 x 72 = 384 x 168.
-constexpr int kF8EpilogueRegs = 216, kF8OtherRegs = 72;
-static_assert(256 * kF8EpilogueRegs + 128 * kF8OtherRegs == kF8Threads * 168, "registers of a block");
 constexpr int kF8MaxStages = 16;
 constexpr int kF8MostSplit = 8;                  // blocks that share a tile's K: a portable cluster
 constexpr int kF8Row = 128;                      // bytes (codes) of a stage's row: one block of K, one swizzled row
@@ -699,6 +692,12 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
 template <int BN, bool GLU>
 struct Fp8ColsGeo {
     static constexpr int kParts = GLU ? 2 : 1;
+    // Warps of the epilogue: 16 where a tile has 64 rows or more (256 x 4096 x 5120: 18.8 us with 8, 16.5 so), else 8, which
+    // have registers for the loads of more blocks of K at a time.
+    static constexpr int kWarps = BN >= 64 ? 16 : 8;
+    static constexpr int kThreads = (kWarps + 4) * 32;
+    static constexpr int kRegs = kWarps == 16 ? 104 : 216, kOtherRegs = kWarps == 16 ? 64 : 72;
+    static_assert(kWarps * 32 * kRegs + 4 * 32 * kOtherRegs == kThreads * (kWarps == 16 ? 96 : 168), "registers of a block");
     static constexpr int kStageBytes = kParts * kF8Tile * kF8Row + BN * kF8Row;
     // Blocks of K of a hand-over from the tensor cores to the epilogue, which costs it about 400 cycles whatever it is of;
     // at most half of TMEM, so that the next is computed meanwhile.
@@ -716,9 +715,10 @@ struct Fp8ColsGeo {
 // split > 1: a cluster of so many blocks takes a tile, each a part of K; their sums are added on chip, in the blocks' order.
 // Such a launch has a cluster for every tile.
 template <int BN, bool GLU>
-__global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_constant__ Fp8Args a) {
+__global__ void __launch_bounds__(Fp8ColsGeo<BN, GLU>::kThreads, 1) fp8_cols_kernel(const __grid_constant__ Fp8Args a) {
     using Geo = Fp8ColsGeo<BN, GLU>;
-    constexpr int kStages = Geo::kStages, kParts = Geo::kParts, kBufs = Geo::kBufs, kStep = Geo::kStep;
+    constexpr int kStages = Geo::kStages, kParts = Geo::kParts, kBufs = Geo::kBufs, kStep = Geo::kStep, kWarps = Geo::kWarps;
+    constexpr int kProducer = kWarps, kMma = kWarps + 1, kScales = kWarps + 2;
     const Fp8Call& c = a.c;
     extern __shared__ uint8_t f8_smem[];
     uint8_t* const ring = f8_smem + ((1024u - (smem_u32(f8_smem) & 1023u)) & 1023u);
@@ -747,11 +747,11 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
         }
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(tfull0 + 8 * i, 1);
-            mbar_init(tempty0 + 8 * i, kF8Epilogue);
+            mbar_init(tempty0 + 8 * i, kWarps);
         }
         for (int i = 0; i < kF8ScaleSteps; ++i) {
             mbar_init(sfull0 + 8 * i, 1);
-            mbar_init(sempty0 + 8 * i, kF8Epilogue);
+            mbar_init(sempty0 + 8 * i, kWarps);
         }
         mbar_init(done, 1);
         flags[0] = 0;
@@ -774,9 +774,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
     const uint32_t tmem = (uint32_t)flags[3];
 
     // (each branch begins with its own count of registers: where the paths met again, everything would have to fit the smaller)
-    if (warp >= kF8Epilogue) {
-        regs_fewer<kF8OtherRegs>();
-        if (warp == kF8Producer) {
+    if (warp >= kWarps) {
+        regs_fewer<Geo::kOtherRegs>();
+        if (warp == kProducer) {
             // -------------------------------------------------------- copies
             F8Ring<kStages> in;
             int seq = 0, e = 0;
@@ -816,7 +816,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
             if (!ok)
                 for (int j = seq > kStages ? seq - kStages : 0; j < seq; ++j)
                     mbar_wait_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kDrainNs);
-        } else if (warp == kF8Mma) {
+        } else if (warp == kMma) {
             // -------------------------------------------------------- MMA issuer (one thread: see fp8_rows_kernel)
             if (elect_one()) {
                 F8Ring<kStages> in;
@@ -849,18 +849,19 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
                 mbar_wait_drain(done, 0, kDrainNs);
             }
             __syncwarp();
-        } else if (warp == kF8Scales) {
+        } else if (warp == kScales) {
             f8_scales<BN, kParts>(c, groups, t0, dt, total, cols, true, scales, sfull0, sempty0, flags, k0, KB,
                                   [&](const Fp8Tile& tile, int g) { return c.ws[g] + tile.e * c.ws_expert[g] + tile.col * c.ws_row[g]; });
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        // Thread: a column of the result (a row of the weight) for half of the tile's rows.
-        regs_more<kF8EpilogueRegs>();
-        constexpr int kMine = BN / 2, kChunk = kMine < 32 ? kMine : 32;
-        constexpr int kAtOnce = 64 / kChunk < kStep ? 64 / kChunk : kStep;   // blocks of K whose chunk is loaded before one wait
-        const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
-        const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16) + half * kMine;
+        // Thread: a column of the result (a row of the weight) for a part of the tile's rows.
+        regs_more<Geo::kRegs>();
+        constexpr int kMine = BN / (kWarps / 4), kChunk = kMine < 32 ? kMine : 32;
+        // blocks of K whose chunk is loaded before one wait, as far as registers go
+        constexpr int kRoom = (kWarps == 16 ? 32 : 64) / kChunk, kAtOnce = kRoom < kStep ? kRoom : kStep;
+        const int quarter = warp & 3, group = warp >> 2, row = 32 * quarter + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16) + group * kMine;
         int step = 0, sstep = 0, e = 0;
         bool ok = true;
         grid_dependency_wait();                  // the results may be in use
@@ -872,7 +873,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
             for (int g = 0; g < kParts; ++g)
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) acc[g][i] = 0.f;
-            const bool any = half * kMine < tile.rows;
+            const bool any = group * kMine < tile.rows;
             for (int kb = 0; kb < KB; kb += kStep, ++step) {
                 const int buf = step % kBufs, slot = sstep % kF8ScaleSteps, block = kb % kF8ScaleBlocks;
                 if (block == 0) ok = mbar_wait(sfull0 + 8 * slot, (sstep / kF8ScaleSteps) & 1, flags, err, wait_ns);
@@ -881,7 +882,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
                 if (any) {
                     // (of blocks past the last, sums and scales of an earlier step: not added)
                     const int here = min(kStep, KB - kb);
-                    const float* const s = scales + (slot * kF8ScaleBlocks + block) * kParts * BN + half * kMine;
+                    const float* const s = scales + (slot * kF8ScaleBlocks + block) * kParts * BN + group * kMine;
 #pragma unroll
                     for (int i0 = 0; i0 < kStep; i0 += kAtOnce)
 #pragma unroll
@@ -918,7 +919,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
             }
             if (split > 1) {
                 // partial sums [part][row of x][column] into the ring: its last copies have been used
-                float* const ex = reinterpret_cast<float*>(ring) + half * kMine * kF8Tile + row;
+                float* const ex = reinterpret_cast<float*>(ring) + group * kMine * kF8Tile + row;
 #pragma unroll
                 for (int g = 0; g < kParts; ++g)
 #pragma unroll
@@ -926,32 +927,32 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
                 break;
             }
             const int n = tile.col * kF8Tile + row;
-            const int rows_here = ok ? min(kMine, tile.rows - half * kMine) : 0;
+            const int rows_here = ok ? min(kMine, tile.rows - group * kMine) : 0;
             if constexpr (GLU) {
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) acc[0][i] = f8_silu_mul(acc[0][i], acc[1][i]);
             }
-            const long long first = tile.row0 + half * kMine;
+            const long long first = tile.row0 + group * kMine;
             if (GLU && c.dtype == NQ_E4M3) {
-                // a row's largest over the tile's 128 columns: the warp's, then the four warps' of this half
+                // a row's largest over the tile's 128 columns: the warp's, then the four warps' with these rows
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
                     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, n < c.N ? bits_max(0, acc[0][i]) : 0u);
-                    if (lane == 0) largest[quarter * BN + half * kMine + i] = m;
+                    if (lane == 0) largest[quarter * BN + group * kMine + i] = m;
                 }
-                named_bar_sync(1 + half, 128);
+                named_bar_sync(1 + group, 128);
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
                     if (i < rows_here) {
                         uint32_t m = 0;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) m = max(m, largest[q * BN + half * kMine + i]);
+                        for (int q = 0; q < 4; ++q) m = max(m, largest[q * BN + group * kMine + i]);
                         const float s = fp8_scale(__uint_as_float(m)), r = 1.f / s;
                         if (row == 0) c.ys[(first + i) * c.ys_stride + tile.col] = s;
                         if (n < c.N) c.y[(first + i) * c.y_stride + n] = (uint8_t)fp8_codes(acc[0][i] * r, 0.f, 0.f, 0.f);
                     }
                 }
-                named_bar_sync(1 + half, 128);   // the next tile's largest use the same place
+                named_bar_sync(1 + group, 128);  // the next tile's largest use the same place
             } else if (n < c.N) {
                 uint16_t* const y = reinterpret_cast<uint16_t*>(c.y) + first * c.y_stride + n;
                 const bool bf16 = c.dtype == NQ_BF16;
@@ -975,7 +976,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_cols_kernel(const __grid_co
         if (t0 < total && !flags[0]) {
             const Fp8Tile tile = fp8_tile(c, groups, t0, 0, BN, cols, true);
             const int n = tile.col * kF8Tile + 4 * lane;
-            for (int i = rank * (kF8Threads / 32) + warp; i < tile.rows; i += split * (kF8Threads / 32)) {
+            for (int i = rank * (Geo::kThreads / 32) + warp; i < tile.rows; i += split * (Geo::kThreads / 32)) {
                 float v[kParts][4] = {};
                 for (int q = 0; q < split; ++q)
 #pragma unroll

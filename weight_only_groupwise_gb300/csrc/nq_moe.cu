@@ -282,14 +282,15 @@ __device__ __forceinline__ void route_place(const RouteArgs& a, int* sm) {
     const int r0 = min(t1, t0 + warp * run) * a.k, r1 = min(t1, t0 + (warp + 1) * run) * a.k;
     for (int i = tid; i < kRtWarps * a.E; i += kRtThreads) next[i] = 0;
     __syncthreads();
-    for (int i0 = r0 + lane; i0 < r1; i0 += 32 * kRtOnce) {
-        int e[kRtOnce];
+    int e[kRtOnce];
+    for (int b0 = r0; b0 < r1; b0 += 32 * kRtOnce) {
 #pragma unroll
-        for (int j = 0; j < kRtOnce; ++j) e[j] = i0 + 32 * j < r1 ? a.ids[i0 + 32 * j] : -1;
+        for (int j = 0; j < kRtOnce; ++j) e[j] = b0 + 32 * j + lane < r1 ? a.ids[b0 + 32 * j + lane] : -1;
 #pragma unroll
         for (int j = 0; j < kRtOnce; ++j)
             if (e[j] >= 0) atomicAdd(my_next + e[j], 1);
     }
+    const bool once = r1 - r0 <= 32 * kRtOnce;   // then e still has them below
     __syncthreads();
     // (at most 512 experts, one a thread)
     if (tid < a.E) {
@@ -302,10 +303,15 @@ __device__ __forceinline__ void route_place(const RouteArgs& a, int* sm) {
     // experts' totals and the rows of the blocks before this one
     int mine = 0, ahead = 0;
     if (tid < a.E)
-        for (int b = 0; b < blocks; ++b) {
-            const int c = *cl.map_shared_rank(count + tid, b);
-            if (b < rank) ahead += c;
-            mine += c;
+        for (int b0 = 0; b0 < blocks; b0 += 8) {
+            int c[8];                            // (loads in flight together)
+#pragma unroll
+            for (int b = 0; b < 8; ++b) c[b] = b0 + b < blocks ? *cl.map_shared_rank(count + tid, b0 + b) : 0;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                if (b0 + b < rank) ahead += c[b];
+                mine += c[b];
+            }
         }
     int upto = mine;
 #pragma unroll
@@ -340,9 +346,9 @@ __device__ __forceinline__ void route_place(const RouteArgs& a, int* sm) {
     for (int i = all + rank * kRtThreads + tid; i < a.T * a.k; i += blocks * kRtThreads) a.rows[i] = -1;
     __syncthreads();
     for (int b0 = r0; b0 < r1; b0 += 32 * kRtOnce) {
-        int e[kRtOnce];
+        if (!once)
 #pragma unroll
-        for (int j = 0; j < kRtOnce; ++j) e[j] = b0 + 32 * j + lane < r1 ? a.ids[b0 + 32 * j + lane] : -1;
+            for (int j = 0; j < kRtOnce; ++j) e[j] = b0 + 32 * j + lane < r1 ? a.ids[b0 + 32 * j + lane] : -1;
 #pragma unroll
         for (int j = 0; j < kRtOnce; ++j) {
             const int i = b0 + 32 * j + lane;
