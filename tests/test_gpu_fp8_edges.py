@@ -124,6 +124,32 @@ def test_weights_quantised_just_before(g):
             assert same(nq.gemm_fp8(x, xs, nq.quant_fp8(v, out=out)[0], ws), y)
 
 
+@pytest.mark.parametrize("T", [48, 600])
+def test_weights_that_a_swiglu_has_just_written(T, g):
+    """nq_swiglu_fp8's codes as a weight, from either kernel."""
+    K, N = 1024, 512
+    x, xs = ref.activations(16, N, g)
+    a = [ref.activations(T, K, g) for _ in range(2)]
+    (wg, sg), (wu, su) = ref.weights(1, N, K, g), ref.weights(1, N, K, g)
+    ws = torch.ones((-(-T // 128), N // 128), device="cuda")
+    codes = lambda i, out=None: nq.swiglu_fp8(*a[i], wg[0], sg[0], wu[0], su[0], dtype=torch.float8_e4m3fn, out=out)  # noqa: E731
+    want = []
+    for i in range(2):
+        w = codes(i)[0].clone()
+        torch.cuda.synchronize()
+        want.append(nq.gemm_fp8(x, xs, w, ws))
+        torch.cuda.synchronize()
+    assert not same(*want)
+    out, got = codes(0), [torch.empty_like(y) for y in want]
+    graph = torch.cuda.CUDAGraph()           # kernels close behind each other
+    with torch.cuda.graph(graph):
+        for i in range(2):
+            nq.gemm_fp8(x, xs, codes(i, out)[0], ws, out=got[i])
+    for _ in range(20):
+        graph.replay()
+        assert all(same(a, b) for a, b in zip(got, want))
+
+
 def test_on_a_stream_that_is_not_the_current_one(g):
     call = CALLS["experts, many rows"](g)
     want = call()
