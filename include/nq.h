@@ -1,6 +1,7 @@
 /*
- * nq.h -- C ABI of the GB300 (sm_103a) groupwise int4/int5 small-batch projection library, and of
- * the serving step around the projections (paged KV cache, attention, sampling).
+ * nq.h -- C ABI of the GB300 (sm_103a) groupwise int4/int5 small-batch projection library, of the
+ * serving step around the projections (paged KV cache, attention, sampling), and of 8-bit products
+ * of any number of rows with the layers of experts that use them.
  *
  * The operation (what the pages tune for single-GPU decode and speculative verify rounds):
  *
@@ -581,8 +582,8 @@ nq_status nq_quant_fp8(const void* x, int dtype, long long x_stride, int rows, i
  * products g = x wg and u = x wu.
  *   K a multiple of 16, 16 <= K <= 2^20; 1 <= N <= 2^20; rows <= 2^24. Nothing may overlap the result.
  * As the projections above, these two start reading the weights' codes (not their scales) before the preceding kernel has
- * ended: the codes must not be written by a kernel that lets its dependents start before its writes are done (nq_quant_fp8
- * does not; the products do: the codes that one writes are rows for the call behind it, not weights).
+ * ended: the codes must not be written by a kernel that lets its dependents start before its writes are done (this
+ * library's calls that write codes do not).
  */
 nq_status nq_gemm_fp8(const nq_fp8_rows* x, const nq_fp8_weight* w, const nq_fp8_out* y, int K, int N, void* stream);
 nq_status nq_swiglu_fp8(const nq_fp8_rows* x, const nq_fp8_weight* wg, const nq_fp8_weight* wu, const nq_fp8_out* h,
@@ -653,7 +654,8 @@ nq_status nq_reserve(int T_max, int K_max, int N_max);
 
 /*
  * nq_device_error: synchronise the current device, then report and clear the device-side
- * error flags of its workspaces (nq_attn_paged's among them) and of nq_gemm_q4_noalloc's fixed scratch: NQ_OK, or
+ * error flags of its workspaces (nq_attn_paged's among them) and of nq_gemm_q4_noalloc's fixed scratch
+ * and the 8-bit products: NQ_OK, or
  * NQ_ERR_TIMEOUT if a bounded wait inside a kernel ran out since the last check (that
  * call's outputs are then undefined). Clears the split-K tickets as well, so later calls
  * start clean.
@@ -661,8 +663,8 @@ nq_status nq_reserve(int T_max, int K_max, int N_max);
 nq_status nq_device_error(void);
 
 /*
- * nq_wait_limit: the bound, in nanoseconds, of every device-side wait of later projection and
- * attention calls (a pipeline stage, an activation slab, a cluster peer). ns > 0 sets it; ns <= 0 only
+ * nq_wait_limit: the bound, in nanoseconds, of every device-side wait of later projection,
+ * attention and 8-bit product calls (a pipeline stage, an activation slab, a cluster peer). ns > 0 sets it; ns <= 0 only
  * queries. Returns the previous bound. Default 2 s, or the environment variable NQ_WAIT_NS
  * read at the first call. A wait that runs out aborts its thread block (its outputs are
  * undefined, nq_device_error reports NQ_ERR_TIMEOUT) after the block has waited, on a

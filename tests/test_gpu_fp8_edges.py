@@ -165,6 +165,24 @@ def test_on_a_stream_that_is_not_the_current_one(g):
         del junk
 
 
+def test_on_a_stream_while_the_current_one_still_writes_freed_memory(g):
+    call = CALLS["experts, many rows"](g)
+    want = call()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    other, need = torch.cuda.Stream(), nq.lib().nq_fp8_scratch_bytes(1500, 4, 2048, 0)
+    for _ in range(5):
+        out = torch.empty_like(want)
+        torch.cuda.synchronize()
+        junk = torch.empty(need, dtype=torch.uint8, device="cuda")
+        for _ in range(200):
+            junk.fill_(255)
+        del junk                             # its memory is free for the current stream's next tensors
+        call(out=out, stream=other)
+        torch.cuda.synchronize()
+        assert same(out, want)
+
+
 def test_experts_that_share_a_weight(g):
     (w, ws), (x, xs) = ref.weights(1, 200, 256, g), ref.activations(30, 256, g)
     ends = torch.tensor([0, 4, 4, 30], dtype=torch.int32, device="cuda")

@@ -396,11 +396,15 @@ __global__ void __launch_bounds__(kRtThreads, 1) route_place_kernel(const RouteA
     route_place(a, route_smem);
 }
 
-// Whether a cluster of kRtClusterMany blocks can run (queried once).
+// Whether a cluster of kRtClusterMany blocks can run (queried once a device, which allows them there).
+constexpr int kDevices = 64;
 bool route_wide_clusters() {
-    static std::once_flag once;
-    static int n = 0;
-    std::call_once(once, [] {
+    static std::once_flag once[kDevices];
+    static int most[kDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return false;
+    int& n = most[dev];
+    std::call_once(once[dev], [&n] {
         if (cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
             cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (kRtWarps + 1) * kMostExperts * 4) != cudaSuccess) {

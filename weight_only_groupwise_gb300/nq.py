@@ -712,9 +712,9 @@ def _fp8(fn, xq, xs, weights, dtype, out, stream, experts=None):
         _check(fn(x, *packed, y, K, N, _raw_stream(stream)))
     else:
         need = lib().nq_fp8_scratch_bytes(M, E, K, len(packed) - 1) if rows is not None else 0
-        scratch = torch.empty(need, dtype=torch.uint8, device=xq.device) if need else None
-        if need and stream is not None:
-            scratch.record_stream(stream)
+        if need:
+            with torch.cuda.stream(stream):      # (its memory may have been in use on the current one; None: that one)
+                scratch = torch.empty(need, dtype=torch.uint8, device=xq.device)
         _check(fn(x, rows, M, offsets, E, *packed, y, K, N, scratch.data_ptr() if need else None, _raw_stream(stream)))
     return out
 
