@@ -173,14 +173,17 @@ def test_on_a_stream_while_the_current_one_still_writes_freed_memory(g):
     other, need = torch.cuda.Stream(), nq.lib().nq_fp8_scratch_bytes(1500, 4, 2048, 0)
     for _ in range(5):
         out = torch.empty_like(want)
-        torch.cuda.synchronize()
         junk = torch.empty(need, dtype=torch.uint8, device="cuda")
-        for _ in range(200):
-            junk.fill_(255)
+        writes = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(writes):
+            for _ in range(2000):
+                junk.fill_(255)
+        writes.replay()                      # some milliseconds
         del junk                             # its memory is free for the current stream's next tensors
         call(out=out, stream=other)
         torch.cuda.synchronize()
         assert same(out, want)
+        del writes
 
 
 def test_experts_that_share_a_weight(g):
