@@ -3,9 +3,10 @@
 //   s[r, b] = max(max over the block of |x| / 448, 2^-126),   c[r, k] = e4m3(x[r, k] / s[r, k / 128])
 //
 // 448 is e4m3's largest value; the floor keeps s normal, so that x / s is at most 448 for any x and a block of zeros
-// needs no case of its own. Bound by memory: x once, a byte an element and 4 / 128 for the scales. Nothing is
-// reused, so a warp takes 1024 columns of a row straight from memory: its lanes have 8 columns of four pairs of
-// blocks, all loads in flight at once, and 16 lanes find a block's largest by shuffles.
+// needs no case of its own. Bound by memory: x once, a byte an element and 4 / 128 for the scales (8191 x 17408 in
+// 16 bits: 69 us, 6.2 TB/s; issue slots, which the arithmetic fills to some 70 %, come next). Nothing is reused, so a
+// warp takes 1024 columns of a row straight from memory: its lanes have 8 columns of four pairs of blocks, all loads in
+// flight at once, and 16 lanes find a block's largest by shuffles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -18,8 +19,8 @@
 namespace nq {
 namespace {
 
-constexpr int kQtThreads = 256;
-constexpr int kQtSteps = 4;                      // loads of 8 columns a lane
+constexpr int kQtThreads = 64;                   // (8191 x 17408, us: 64 69.2, 128 70.5, 256 72.2, 512 83.6)
+constexpr int kQtSteps = 4;                      // loads of 8 columns a lane (with 256 threads: 2 83.1, 4 72.2, 8 72.7)
 constexpr int kQtCols = 32 * 8 * kQtSteps;       // columns of a warp
 
 struct QuantArgs {
@@ -41,6 +42,26 @@ struct Eight {
         if (DTYPE == NQ_FP32) hi = __ldg(reinterpret_cast<const uint4*>(p) + 1);
     }
     __device__ __forceinline__ void zero() { lo = hi = make_uint4(0, 0, 0, 0); }
+    // The largest magnitude of the 16 lanes' columns, by the order of bits: a NaN is the largest of all, so that it reaches
+    // the scale. 16-bit values two at a time.
+    __device__ __forceinline__ float largest() const {
+        if constexpr (DTYPE == NQ_FP32) {
+            const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            return __uint_as_float(m);
+        } else {
+            const uint32_t sign = 0x7FFF7FFFu;
+            uint32_t m = __vmaxu2(__vmaxu2(lo.x & sign, lo.y & sign), __vmaxu2(lo.z & sign, lo.w & sign));
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            m = max(m & 0xFFFFu, m >> 16);
+            return DTYPE == NQ_BF16 ? __uint_as_float(m << 16) : __half2float(__ushort_as_half((unsigned short)m));
+        }
+    }
     __device__ __forceinline__ void floats(float (&f)[8]) const {
         const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
@@ -60,12 +81,22 @@ struct Eight {
     }
 };
 
-// x / s, with r = 1 / s rounded: the product and one correction by its residual, which is exact in an fma. (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990: rounded as the quotient
-// is. A division each took 92 us for 8191 x 17408 in 16 bits where this takes 74.)
-__device__ __forceinline__ float quotient(float x, float s, float r) {
-    const float q = x * r;
-    return fmaf(fmaf(-q, s, x), r, q);
+// x / s for two, with r = 1 / s rounded: the product and one correction by its residual, which is exact in an fma.
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990: rounded as the quotient
+// is. A division each took 92 us for 8191 x 17408 in 16 bits, single ones of this 74, two at a time and the largest of two
+// at a time 72.)
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ void quotients(float& a, float& b, uint64_t minus_s, uint64_t r) {
+    const uint64_t x = two(a, b);
+    uint64_t q, e;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(r));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(minus_s), "l"(x));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(r), "l"(q));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
 }
 
 template <int DTYPE>
@@ -90,19 +121,14 @@ __global__ void __launch_bounds__(kQtThreads) quant_kernel(const QuantArgs a) {
     for (int i = 0; i < kQtSteps; ++i) {
         float f[8];
         v[i].floats(f);
-        // magnitudes in the order of their bits: a NaN is the largest of all, so that it reaches the scale
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        const float s = fp8_scale(__uint_as_float(m));
+        const float s = fp8_scale(v[i].largest());
         const int col = col0 + i * 256;
         if (col < a.K) {
             if (s > 0x1p-60f && s < 0x1p60f) {
                 const float r = 1.f / s;
+                const uint64_t minus_s = two(-s, -s), rr = two(r, r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = quotient(f[j], s, r);
+                for (int j = 0; j < 8; j += 2) quotients(f[j], f[j + 1], minus_s, rr);
             } else {                             // residuals out of range, an infinite scale
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] /= s;

@@ -713,8 +713,11 @@ def _fp8(fn, xq, xs, weights, dtype, out, stream, experts=None):
     else:
         need = lib().nq_fp8_scratch_bytes(M, E, K, len(packed) - 1) if rows is not None else 0
         if need:
-            with torch.cuda.stream(stream):      # (its memory may have been in use on the current one; None: that one)
+            if stream is None:
                 scratch = torch.empty(need, dtype=torch.uint8, device=xq.device)
+            else:                                # (the current one's free memory may still be written there)
+                with torch.cuda.stream(stream):
+                    scratch = torch.empty(need, dtype=torch.uint8, device=xq.device)
         _check(fn(x, rows, M, offsets, E, *packed, y, K, N, scratch.data_ptr() if need else None, _raw_stream(stream)))
     return out
 
