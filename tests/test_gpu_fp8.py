@@ -273,3 +273,22 @@ def test_sorted_rows_of_some_tens_an_expert(E, M, K, N, dtype, g):
     cuts = sorted(torch.randint(0, M // 3 + 1, (E - 2,), device="cuda", generator=g).tolist())
     x, xs = ref.activations(M, K, g)
     check_experts(x, xs * 2.0 ** -10, [ref.weights(E, N, K, g)], [0, 0, *cuts, M], None, dtype)
+
+
+@pytest.mark.parametrize("E,M,K,N", [(8, 200, 1040, 515), (16, 331, 256, 144), (3, 96, 144, 1)])
+def test_gathered_rows_of_some_tens_an_expert(E, M, K, N, g):
+    """Copied together first; rows that x has not are zeros."""
+    cuts = sorted(torch.randint(0, M // 3 + 1, (E - 2,), device="cuda", generator=g).tolist())
+    x, xs = ref.activations(50, K, g)
+    rows = torch.randint(-1, 52, (M,), device="cuda", generator=g, dtype=torch.int32)
+    check_experts(x, xs * 2.0 ** -10, [ref.weights(E, N, K, g)], [0, 0, *cuts, M], rows, BF16)
+
+
+@pytest.mark.parametrize("dtype,glu", [(BF16, False), (E4M3, True)])
+@pytest.mark.parametrize("E,M,K,N", [(8, 200, 1040, 512), (2, 700, 256, 272), (1, 130, 144, 48)])
+def test_gathered_rows_without_scratch_memory(E, M, K, N, dtype, glu, g, monkeypatch):
+    monkeypatch.setattr(nq.lib(), "nq_fp8_scratch_bytes", lambda *a: 0)
+    x, xs = ref.activations(50, K, g)
+    rows = torch.randint(-1, 52, (M,), device="cuda", generator=g, dtype=torch.int32)
+    cuts = sorted(torch.randint(0, M + 1, (E - 1,), device="cuda", generator=g).tolist())
+    check_experts(x, xs * 2.0 ** -10, [ref.weights(E, N, K, g) for _ in range(1 + glu)], [0, *cuts, M], rows, dtype)

@@ -172,7 +172,8 @@ struct Fp8Plan {
 // rows an expert 67.4, 70.8, 79.8; 24 rows 76.4, 70.8, 81.0; 32 rows 97, 88, 83. Plain, tiles of 16, 32, 64 rows and
 // fp8_rows_kernel: 128 experts of 768 -> 2048, 6 rows 35.2, 39.9, -, 38.4; 12 rows 42.2, 43.2, 40.3, 40.5; 28 rows 67, 56.1,
 // 41.9, 41.7; 64 experts, 24 rows -, 28.9, 22.9, 25.7; 56 rows -, 47.5, 30.2, 28.0; 256 of 2048 -> 4096, 20 rows -, 389, 321,
-// 332. Gathered rows of 64 take the copy engine longer than their weights, so that such plain calls leave them out.
+// 332. Tiles of 64 rows that the copy engine gathers take it longer than their weights, so that calls with `gathered` rows,
+// which have not been copied together, leave them out.
 int fp8_experts_rows(int M, int E, bool glu, bool gathered) {
     const int each = (M + E - 1) / E;
     if (glu) return each <= 16 ? 16 : each <= 28 ? 32 : 0;
@@ -208,8 +209,8 @@ Fp8Plan fp8_dense_plan(int M, int K, int N, bool glu, int sms, const int* cluste
     return best;
 }
 
-// Whether gathered rows are copied together first, where there is scratch memory: for fp8_rows_kernel, whose 128 rows a block
-// of K take the copy engine longer to gather than to multiply (4096 tokens x 8 of 64 experts: 1014 us, 497 so).
+// Whether gathered rows are copied together first, where there is scratch memory: for tiles of 64 rows and more, whose rows
+// take the copy engine longer to gather than to multiply (4096 tokens x 8 of 64 experts: 1014 us, 497 so).
 bool fp8_gathers(int M, int E, bool glu) { return fp8_experts_rows(M, E, glu, true) == 0; }
 long long scratch_stride(int K) { return (K + 15) / 16 * 16; }
 int scratch_scales(int K) { return ((K + kFp8Block - 1) / kFp8Block + 3) / 4 * 4; }
@@ -321,7 +322,7 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     c.wide = !mis(y->data, 16) && yst % 8 == 0;
     c.quads = !mis(x->scales, 16) && xss % 4 == 0;
     c.wait_ns = d.wait_ns;
-    const Fp8Plan plan = experts ? Fp8Plan{fp8_experts_rows(M, E, glu, rows != nullptr), 1} : fp8_dense_plan(M, K, N, glu, d.sms, fp8_clusters(d.sms));
+    const Fp8Plan plan = experts ? Fp8Plan{fp8_experts_rows(M, E, glu, rows && !gathers), 1} : fp8_dense_plan(M, K, N, glu, d.sms, fp8_clusters(d.sms));
     const int bn = plan.rows;
     const bool few = bn > 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
