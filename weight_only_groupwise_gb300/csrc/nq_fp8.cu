@@ -366,9 +366,10 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     const int wide = few || glu ? kF8Tile : 256, high = few ? bn : kF8Tile;
     const long long most = (long long)((N + wide - 1) / wide) * (experts ? (M + high - 1) / high + (E < M ? E : M) : (M + high - 1) / high);
     c.split = plan.split;
-    // results of sums of up to so many blocks of K go by bulk copies (us, stored by the threads and so, 24570 rows of
-    // 128 experts x 2048: K = 256 52.6, 41.9; 768 83.0, 73.3; 2304 166.8, 163.3; 4096 269.2, 272.6)
-    const bool bulk = c.wide && N % 8 == 0 && K <= 20 * kFp8Block;
+    // results of sums of up to so many blocks of K go by bulk copies, at the price of a stage (us, stored by the threads and so:
+    // 24570 rows of 128 experts x 2048, K = 256 52.6, 45.3; 768 83.0, 74.3; 2304 166.8, 166.0; 4096 281.4, 273.8; 4096 x 5120 x
+    // 17408 327.1, 329.3; 2048 x 17408 x 5120 204.3, 209.8)
+    const bool bulk = c.wide && N % 8 == 0 && K <= 32 * kFp8Block;
     const int blocks = c.split > 1 ? (int)(most * c.split) : (int)(most < d.sms ? most : d.sms);
     const cudaError_t e = few ? (glu ? launch_cols_of<true>(bn, a, dev, blocks, s, d.pdl) : launch_cols_of<false>(bn, a, dev, blocks, s, d.pdl))
                               : glu  ? launch_rows<true, false>(a, dev, blocks, s, d.pdl)

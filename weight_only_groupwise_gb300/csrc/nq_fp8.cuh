@@ -542,6 +542,20 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
         int e = 0;
         bool ok = true;
         grid_dependency_wait();                  // the results may be in use
+        // BULK: eight lanes of a warp have a row each of the finished tile to send. Results leave an SM at some 32 bytes a cycle
+        // and hold up the copies' requests behind them, so that they go one by one during the first half of the next tile's
+        // blocks of K (24570 rows of 128 experts x 2048, us, at once and so: K = 256 44.2, 45.3; 384 59.9, 51.7; 512 66.1,
+        // 59.3; 768 80.2, 74.3; 1536 125.8, 118.4).
+        const int my_row = 32 * quarter + 8 * group + lane, due_at = lane * KB / 16;
+        uint16_t* due = nullptr;
+        int due_bytes = 0;
+        auto send = [&] {
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(due), "r"(smem_u32(turn + my_row * Geo::kPitch)),
+                         "r"(due_bytes)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            due = nullptr;
+        };
         for (int t = blockIdx.x; t < total; t += gridDim.x) {
             const Fp8Tile tile = fp8_tile(c, groups, t, e, kF8Tile, cols, false);
             e = tile.e;
@@ -569,6 +583,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
 #pragma unroll
                     for (int j = 0; j < 16; ++j) acc[16 * i + j] = fmaf(__uint_as_float(v[j]), i < 2 ? f0 : f1, acc[16 * i + j]);
                 }
+                if (BULK && due && kb == due_at) send();
                 in.next();
                 if (block == kF8ScaleBlocks - 1 || kb + 1 == KB) {
                     __syncwarp();
@@ -621,15 +636,10 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
                                    pack_16(acc[j + 4], acc[j + 5], bf16), pack_16(acc[j + 6], acc[j + 7], bf16));
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 named_bar_sync(1 + quarter, 128);
-                const int r = 32 * quarter + 8 * group + lane;   // each of the row's four warps has 8 rows to send
-                if (lane < 8 && ok && r < tile.rows) {
-                    const int n1 = tile.col * Geo::kOut;
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                                     reinterpret_cast<uint16_t*>(c.y) + (long long)(tile.row0 + r) * c.y_stride + n1),
-                                 "r"(smem_u32(turn + r * Geo::kPitch)), "r"(2 * min(Geo::kOut, c.N - n1))
-                                 : "memory");
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                }
+                const int n1 = tile.col * Geo::kOut;
+                if (lane < 8 && ok && my_row < tile.rows)
+                    due = reinterpret_cast<uint16_t*>(c.y) + (long long)(tile.row0 + my_row) * c.y_stride + n1;
+                due_bytes = 2 * min(Geo::kOut, c.N - n1);
             } else {
                 // Turned in shared memory, 8 rows at a time, so that a store writes whole lines (of 4 or 8 rows, or, where rows
                 // are not aligned, 64 bytes of one) instead of a sector of each of 32.
@@ -678,6 +688,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
                 }
             }
         }
+        if (BULK && due) send();
         if (BULK) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
