@@ -186,6 +186,23 @@ def test_on_a_stream_while_the_current_one_still_writes_freed_memory(g):
         del writes
 
 
+def test_on_two_streams_at_once(g):
+    """All kinds of calls on one stream in order, and in the opposite order on another, many of them in flight."""
+    calls = [make(g) for make in CALLS.values()]
+    flat = lambda y: y if isinstance(y, torch.Tensor) else y[0]  # noqa: E731
+    want = [flat(call()).clone() for call in calls]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(5):
+        for s, order in ((0, 1), (1, -1)):
+            with torch.cuda.stream(streams[s]):
+                got[s] += [flat(call()) for call in calls[::order]]
+    torch.cuda.synchronize()
+    nq.device_error()
+    for s, order in ((0, 1), (1, -1)):
+        assert all(same(y, want[::order][i % len(calls)]) for i, y in enumerate(got[s]))
+
+
 def test_experts_that_share_a_weight(g):
     (w, ws), (x, xs) = ref.weights(1, 200, 256, g), ref.activations(30, 256, g)
     ends = torch.tensor([0, 4, 4, 30], dtype=torch.int32, device="cuda")

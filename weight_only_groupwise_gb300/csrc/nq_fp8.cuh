@@ -609,8 +609,8 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
                 named_bar_sync(1 + quarter, 128);        // the next tile's use the same place
                 const float s = fp8_scale(__uint_as_float(m)), r = 1.f / s;
                 if (ok && row < tile.rows) {
-                    const long long my_row = tile.row0 + row;
-                    if (group == 0) c.ys[my_row * c.ys_stride + tile.col] = s;
+                    const long long at = tile.row0 + row;
+                    if (group == 0) c.ys[at * c.ys_stride + tile.col] = s;
 #pragma unroll
                     for (int i = 0; i < 32; i += 16) {
                         if (n + i >= c.N) break;
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
                             const float* const p = acc + i + 4 * j;
                             u[j] = fp8_codes(p[0] * r, p[1] * r, p[2] * r, p[3] * r);
                         }
-                        *reinterpret_cast<uint4*>(c.y + my_row * c.y_stride + n + i) = make_uint4(u[0], u[1], u[2], u[3]);
+                        *reinterpret_cast<uint4*>(c.y + at * c.y_stride + n + i) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 }
             } else if (BULK) {
