@@ -1,0 +1,27 @@
+"""What the 8-bit products must have in their source and no run can show for certain. No GPU."""
+import re
+
+import pytest
+
+from tests.test_step_source import body
+
+KERNELS = ["fp8_rows_kernel", "fp8_cols_kernel"]
+
+
+def role(text: str, begin: str, end: str) -> str:
+    """A warp's part of a kernel."""
+    at = text.index(begin)
+    return text[at:text.index(end, at)]
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_no_block_leaves_while_its_copies_are_on_their_way(kernel):
+    """Any warp can give up waiting, also after the producer has asked for its last copies: it waits for them in any case."""
+    producer = role(body("nq_fp8.cuh", kernel), "if (warp == kProducer)", "else if (warp == kMma)")
+    tail = producer[producer.rindex("f8_gather4("):]
+    drain = re.search(r"for \(int j = seq > kStages \? seq - kStages : 0; j < seq; \+\+j\)\s*mbar_wait_drain\(full0", tail)
+    assert drain
+    # a statement of its own, behind the one for an aborted call's first rows
+    assert tail[:drain.start()].rstrip().endswith("__syncwarp();") and "x_late(seq);" in tail[:drain.start()]
+    assert not re.search(r"(if|else|while|for)\s*(\([^;{}]*\))?\s*$", tail[:drain.start()].rstrip())
+    assert tail.count("mbar_wait_drain") == 1

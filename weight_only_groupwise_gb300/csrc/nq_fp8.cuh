@@ -488,9 +488,11 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
                 }
             }
             if (!ok && lane == 0 && seq < late) x_late(seq);
-            if (!ok)                             // aborted: the last copies into each stage
-                for (int j = seq > kStages ? seq - kStages : 0; j < seq; ++j)
-                    mbar_wait_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kDrainNs);
+            __syncwarp();
+            // The last copies into each stage: the block must not leave while they are on their way, and any warp may give up
+            // waiting for them after this one has asked for them all. (Otherwise they have long been waited for.)
+            for (int j = seq > kStages ? seq - kStages : 0; j < seq; ++j)
+                mbar_wait_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kDrainNs);
         } else if (warp == kMma) {
             // -------------------------------------------------------- MMA issuer: one thread
             if (elect_one()) {
@@ -826,9 +828,9 @@ __global__ void __launch_bounds__(Fp8ColsGeo<BN, GLU>::kThreads, 1) fp8_cols_ker
                 }
             }
             if (!ok && lane == 0 && seq < late) x_late(seq);
-            if (!ok)
-                for (int j = seq > kStages ? seq - kStages : 0; j < seq; ++j)
-                    mbar_wait_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kDrainNs);
+            __syncwarp();
+            for (int j = seq > kStages ? seq - kStages : 0; j < seq; ++j)   // (as in fp8_rows_kernel)
+                mbar_wait_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kDrainNs);
         } else if (warp == kMma) {
             // -------------------------------------------------------- MMA issuer (one thread: see fp8_rows_kernel)
             if (elect_one()) {
