@@ -60,3 +60,19 @@ def test_paired_attention_publishes_zeroed_rows_at_cluster_scope():
     zeros = text[text.index("auto zero ="):]
     order = [zeros.index(x) for x in ("fence_proxy_async_smem();", "published = true;", "__syncwarp();", "arrive_leader(pready0")]
     assert order == sorted(order)
+
+
+def test_no_attention_block_leaves_while_its_copies_are_on_their_way():
+    """Any warp can give up waiting, also after the producers have asked for their last copies: they wait in any case, for the last
+    into each slot, which is that of either of the two; the query tiles' warp for its last."""
+    text = body("nq_attn.cuh", "attn_kernel")
+    roles = text[text.index("if (warp == kAttnProducerK || warp == kAttnProducerV)"):]
+    producer = roles[:roles.index("else if (PAIR && rank == 1 && warp == kAttnMma)")]
+    assert "int* const mine = last_fill + (int)is_v * kAttnMaxSlots;" in producer and producer.count("if (lane < kSlots) mine[lane] = -1;") == 1
+    loop = producer[producer.index("for (; w.more()"):]
+    assert loop.index("__syncwarp();") < loop.index("tma_load_4d(") < loop.index("if (lane == 0) mine[slot] = seq;") < loop.index("id = id_next;")
+    assert re.search(r"\}\s*named_bar_sync\(5, 64\);\s*const int last = lane < kSlots \? max\(last_fill\[lane\], last_fill\[kAttnMaxSlots \+ lane\]\) : -1;\s*"
+                     r"if \(last >= 0\) mbar_wait_drain\(full0 \+ 8 \* lane, \(last / kSlots\) & 1, kDrainNs\);\s*\}\s*$", producer)
+    assert text.count("named_bar_sync(5,") == 1 and "return" not in loop
+    loader = roles[roles.index("else if (warp == kAttnLoader)"):]
+    assert re.search(r"\}\s*if \(seg > 0\) mbar_wait_drain\(qfull, \(seg - 1\) & 1, kDrainNs\);\s*\} else \{", loader)

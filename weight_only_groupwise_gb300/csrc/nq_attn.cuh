@@ -508,6 +508,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     volatile int* const flags = reinterpret_cast<volatile int*>(ctrl + 2048 + 320);
     // flags: [0] abort, [3] TMEM base
     long long* const warp_sums = reinterpret_cast<long long*>(ctrl + 2048 + 384);
+    int* const last_fill = reinterpret_cast<int*>(ctrl + 2048 + 384);      // [2 producers][8 slots], after the plan
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t wait_ns = a.wait_ns;
@@ -693,7 +694,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         const int ids_of = kAttnKeys >> page_bits, page_mask = (1 << a.page_shift) - 1, panels = slot_cols / 64;
         const CUtensorMap* const map = is_v ? &a.vmap : &a.kmap;
         int base = 0;                      // slots filled by the segments before, by both producers
-        uint32_t filled = 0, parity = 0;   // per slot: whether this warp filled it, and the phase
+        int* const mine = last_fill + (int)is_v * kAttnMaxSlots;         // this warp's last fill of each slot
+        if (lane < kSlots) mine[lane] = -1;
         bool ok = flags[0] == 0;
         // block ids of key tile kt, one a lane: -1, which reads as zeros, where no row sees any of the keys
         auto ids = [&](const AttnWalk& k, int kt) {
@@ -733,17 +735,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                             tma_load_4d(dst + panel * (slot_keys * 128) + box * rows * 128, map, col0 + panel * 64,
                                         (key0 + box * rows) & page_mask, w.h, block, bar);
                     }
-                    filled |= 1u << slot;
-                    parity = (parity & ~(1u << slot)) | ((uint32_t)((seq / kSlots) & 1) << slot);
+                    if (lane == 0) mine[slot] = seq;
                 }
                 id = id_next;
                 id_next = id_after;
             }
             base += n * (kKS + kVS);
         }
-        if (!ok)                           // aborted: this warp's last copy into each slot
-            for (int i = 0; i < kSlots; ++i)
-                if ((filled >> i) & 1) mbar_wait_drain(full0 + 8 * i, (parity >> i) & 1, kDrainNs);
+        // The last copy into each slot, by whichever of the two: the block must not leave while one is on its way, and any warp
+        // may give up waiting for it after this one has asked for them all. (Otherwise they have long been waited for.)
+        named_bar_sync(5, 64);
+        const int last = lane < kSlots ? max(last_fill[lane], last_fill[kAttnMaxSlots + lane]) : -1;
+        if (last >= 0) mbar_wait_drain(full0 + 8 * lane, (last / kSlots) & 1, kDrainNs);
     } else if (PAIR && rank == 1 && warp == kAttnMma) {
         // ------------------------------------------------------------ the second block's copies, passed on
         int seq = 0, seg = 0;
@@ -877,7 +880,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             __syncwarp();
             ++seg;
         }
-        if (!ok && seg > 0) mbar_wait_drain(qfull, (seg - 1) & 1, kDrainNs);
+        if (seg > 0) mbar_wait_drain(qfull, (seg - 1) & 1, kDrainNs);    // (has long come, unless the block aborted)
     } else {
         // ------------------------------------------------------------ softmax
         // pv_done of a buffer may be waited for in any of its phases or in none: S of tile g is full
