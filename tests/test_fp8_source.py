@@ -25,3 +25,18 @@ def test_no_block_leaves_while_its_copies_are_on_their_way(kernel):
     assert tail[:drain.start()].rstrip().endswith("__syncwarp();") and "x_late(seq);" in tail[:drain.start()]
     assert not re.search(r"(if|else|while|for)\s*(\([^;{}]*\))?\s*$", tail[:drain.start()].rstrip())
     assert tail.count("mbar_wait_drain") == 1
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_bounded_waits_begin_when_the_call_ahead_has_ended(kernel):
+    """Every warp of a dense call: waits count their own time alone. The producer's first turn through its stages needs no wait,
+    and ends with the rows of x, which it asks for when the call ahead has ended."""
+    text = body("nq_fp8.cuh", kernel)
+    mma = role(text, "else if (warp == kMma)", "else if (warp == kScales)")
+    assert mma.index("grid_dependency_wait();") < mma.index("mbar_wait(")
+    epilogue = role(text, "regs_more<", "tmem_dealloc")
+    assert epilogue.index("grid_dependency_wait();") < epilogue.index("mbar_wait(")
+    producer = role(text, "if (warp == kProducer)", "else if (warp == kMma)")
+    late = role(producer, "auto x_late", "};")
+    assert late.index("grid_dependency_wait();") < late.index("f8_copy_2d(")
+    assert "if (seq + 1 == late) x_late(late);" in producer

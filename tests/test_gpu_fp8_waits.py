@@ -29,18 +29,20 @@ def same(a, b):
 
 def dense(T, K, N, glu, g, **how):
     x, xs = ref.activations(T, K, g)
+    xs *= 2.0 ** -10                     # (here, so that no other kernel runs ahead of the call's)
     w = [ref.weights(1, N, K, g) for _ in range(1 + glu)]
     fn = nq.swiglu_fp8 if glu else nq.gemm_fp8
-    return lambda: fn(x, xs * 2.0 ** -10, *[t for c, s in w for t in (c[0], s[0])], **how)
+    return lambda: fn(x, xs, *[t for c, s in w for t in (c[0], s[0])], **how)
 
 
 def experts(E, M, K, N, glu, g, **how):
     x, xs = ref.activations(M, K, g)
+    xs *= 2.0 ** -10
     w = [ref.weights(E, N, K, g) for _ in range(1 + glu)]
     ends = torch.linspace(0, M, E + 1, device="cuda").to(torch.int32)
     rows = torch.randperm(M, device="cuda", generator=g).to(torch.int32)
     fn = nq.swiglu_fp8_experts if glu else nq.gemm_fp8_experts
-    return lambda: fn(x, xs * 2.0 ** -10, *[t for p in w for t in p], ends, rows=rows, **how)
+    return lambda: fn(x, xs, *[t for p in w for t in p], ends, rows=rows, **how)
 
 
 def limited(ns, call):
@@ -82,3 +84,27 @@ def test_a_call_right_behind_one_that_gave_up_is_right(name, g):
         assert all(same(y, want) for y in got)
     assert gave_up
     nq.device_error()
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if not n.startswith("experts")])
+def test_a_long_call_ahead_is_not_charged_to_the_next(name, g):
+    """A dense call whose blocks start while the call ahead of it still runs, for longer than the limit of a wait."""
+    call = CALLS[name](g)
+    want = call()
+    x, xs = ref.activations(100, 1 << 19, g)
+    w, ws = ref.weights(1, 200, 1 << 19, g)
+    xs *= 2.0 ** -12
+    ends = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+    ahead = lambda: nq.gemm_fp8_experts(x, xs, w, ws, ends)   # one tile of 4096 blocks of K: some 2 ms on one SM  # noqa: E731
+    ahead()
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    ahead()
+    end.record()
+    nq.device_error()
+    assert begin.elapsed_time(end) > 1.0
+    for _ in range(5):
+        ahead()
+        got = limited(300_000, call)
+        nq.device_error()
+        assert same(got, want)

@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(Fp8RowsGeo<GLU, BULK>::kThreads, 1) fp8_rows_k
                 int e = 0;
                 bool ok = true;
                 const uint32_t x0 = f8_desc(smem_u32(ring));
+                grid_dependency_wait();          // (a wait's time is its own: x's rows are asked for from then on)
                 for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                     const Fp8Tile tile = fp8_tile(c, groups, t, e, kF8Tile, cols, false);
                     e = tile.e;
@@ -839,6 +840,7 @@ __global__ void __launch_bounds__(Fp8ColsGeo<BN, GLU>::kThreads, 1) fp8_cols_ker
                 int e = 0;
                 bool ok = true;
                 const uint32_t w0 = f8_desc(smem_u32(ring));
+                grid_dependency_wait();          // (as in fp8_rows_kernel)
                 for (int t = t0; t < total && ok; t += dt) {
                     const Fp8Tile tile = fp8_tile(c, groups, t, e, BN, cols, true);
                     e = tile.e;
