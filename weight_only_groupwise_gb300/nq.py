@@ -2,6 +2,9 @@
 the projection runs in the library's CUDA kernels. PyTorch provides device memory and the
 current stream. There is no fallback: if the library is missing or the device is not a GB300
 (sm_103), the calls raise.
+
+`stream`: where a call runs (None: the current stream). The caller orders it behind what writes the call's
+inputs, and what reads the results behind it. Results that a call makes itself are memory of that stream.
 """
 from __future__ import annotations
 
@@ -153,6 +156,25 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _own(stream):
+    """A context in which tensors are made for kernels on `stream`, of its own memory: the current stream's free memory may
+    still be written by what waits there."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+def _empty(stream):
+    """torch.empty for a call's results on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty
+
+    def empty(*shape, dtype, device):
+        with _own(stream):
+            t = torch.empty(*shape, dtype=dtype, device=device)
+        t.record_stream(torch.cuda.current_stream(device))   # (read there: used again only after that)
+        return t
+    return empty
+
+
 def _cuda(t: torch.Tensor, name: str) -> torch.Tensor:
     if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
@@ -175,9 +197,10 @@ def scale_bytes(K: int, N: int) -> int:
 
 # ---------------------------------------------------------------- repack
 
-def _packed_pair(code_bytes: int, K: int, N: int, dev):
-    wq = torch.empty(max(code_bytes, 16), dtype=torch.uint8, device=dev)
-    s = torch.empty(max(scale_bytes(K, N), 16), dtype=torch.uint8, device=dev)
+def _packed_pair(code_bytes: int, K: int, N: int, dev, stream):
+    empty = _empty(stream)
+    wq = empty(max(code_bytes, 16), dtype=torch.uint8, device=dev)
+    s = empty(max(scale_bytes(K, N), 16), dtype=torch.uint8, device=dev)
     return wq, s
 
 
@@ -186,7 +209,7 @@ def pack_q4(wq_canon: torch.Tensor, s_canon: torch.Tensor, K: int, N: int, strea
     (packed codes, packed scales), two uint8 device tensors."""
     dev = _cuda(wq_canon, "wq_canon").device
     _cuda(s_canon, "s_canon")
-    wq, s = _packed_pair(packed_bytes_q4(K, N), K, N, dev)
+    wq, s = _packed_pair(packed_bytes_q4(K, N), K, N, dev, stream)
     _check(lib().nq_pack_q4(_ptr(wq_canon), _ptr(s_canon), K, N, _ptr(wq), _ptr(s), _stream(stream)))
     return wq, s
 
@@ -196,7 +219,7 @@ def pack_q5(wn_canon, wh_canon, s_canon, K: int, N: int, stream=None):
     dev = _cuda(wn_canon, "wn_canon").device
     _cuda(wh_canon, "wh_canon")
     _cuda(s_canon, "s_canon")
-    wq, s = _packed_pair(packed_bytes_q5(K, N), K, N, dev)
+    wq, s = _packed_pair(packed_bytes_q5(K, N), K, N, dev, stream)
     _check(lib().nq_pack_q5(_ptr(wn_canon), _ptr(wh_canon), _ptr(s_canon), K, N, _ptr(wq), _ptr(s),
                             _stream(stream)))
     return wq, s
@@ -204,10 +227,10 @@ def pack_q5(wn_canon, wh_canon, s_canon, K: int, N: int, stream=None):
 
 # ---------------------------------------------------------------- projections
 
-def _out(x: torch.Tensor, N: int, out):
+def _out(x: torch.Tensor, N: int, out, stream=None):
     T = x.shape[0]
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        out = _empty(stream)((T, N), dtype=torch.bfloat16, device=x.device)
     return _cuda(out, "out")
 
 
@@ -215,7 +238,7 @@ def gemm_q4(x: torch.Tensor, wq: torch.Tensor, s: torch.Tensor, N: int, out=None
     """Y[T,N] (bf16) = X[T,K] (bf16) * dequant(packed Q4 codes wq, packed scales s)."""
     _cuda(x, "x")
     T, K = x.shape
-    y = _out(x, N, out)
+    y = _out(x, N, out, stream)
     _check(lib().nq_gemm_q4(_ptr(x), _ptr(wq), _ptr(s), _ptr(y), T, K, N, _stream(stream)))
     return y
 
@@ -224,7 +247,7 @@ def gemm_q5(x: torch.Tensor, wq: torch.Tensor, s: torch.Tensor, N: int, out=None
     """Y[T,N] (bf16) = X[T,K] (bf16) * dequant(packed Q5 codes wq, packed scales s)."""
     _cuda(x, "x")
     T, K = x.shape
-    y = _out(x, N, out)
+    y = _out(x, N, out, stream)
     _check(lib().nq_gemm_q5(_ptr(x), _ptr(wq), _ptr(s), _ptr(y), T, K, N, _stream(stream)))
     return y
 
@@ -234,7 +257,7 @@ def gemm_q4_noalloc(x: torch.Tensor, wq: torch.Tensor, s: torch.Tensor, N: int, 
     library; `out` is allocated here by torch when not given)."""
     _cuda(x, "x")
     T, K = x.shape
-    y = _out(x, N, out)
+    y = _out(x, N, out, stream)
     _check(lib().nq_gemm_q4_noalloc(_ptr(x), _ptr(wq), _ptr(s), _ptr(y), T, K, N, _stream(stream)))
     return y
 
@@ -243,7 +266,8 @@ def _grouped(fn, x, groups, outs, stream):
     _cuda(x, "x")
     T, K = x.shape
     if outs is None:
-        outs = [torch.empty((T, N), dtype=torch.bfloat16, device=x.device) for (_, _, N) in groups]
+        empty = _empty(stream)
+        outs = [empty((T, N), dtype=torch.bfloat16, device=x.device) for (_, _, N) in groups]
     arr = (NqGroup * len(groups))()
     for i, ((wq, s, N), y) in enumerate(zip(groups, outs)):
         _cuda(y, "out")
@@ -265,7 +289,7 @@ def swiglu_q4(x, wg, sg, wu, su, N: int, out=None, stream=None):
     """H[T,N] = bf16(silu(X*Wg) * (X*Wu)) with both weights packed Q4 (codes, scales)."""
     _cuda(x, "x")
     T, K = x.shape
-    h = _out(x, N, out)
+    h = _out(x, N, out, stream)
     _check(lib().nq_swiglu_q4(_ptr(x), _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su), _ptr(h), T, K, N,
                               _stream(stream)))
     return h
@@ -275,14 +299,14 @@ def swiglu_q5(x, wg, sg, wu, su, N: int, out=None, stream=None):
     """H[T,N] = bf16(silu(X*Wg) * (X*Wu)) with both weights packed Q5 (codes, scales)."""
     _cuda(x, "x")
     T, K = x.shape
-    h = _out(x, N, out)
+    h = _out(x, N, out, stream)
     _check(lib().nq_swiglu_q5(_ptr(x), _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su), _ptr(h), T, K, N,
                               _stream(stream)))
     return h
 
 
 def _dequant(fn, wq, s, K: int, N: int, stream):
-    out = torch.empty((N, K), dtype=torch.float32, device=wq.device)
+    out = _empty(stream)((N, K), dtype=torch.float32, device=wq.device)
     _check(fn(_ptr(wq), _ptr(s), _ptr(out), K, N, _stream(stream)))
     return out
 
@@ -314,8 +338,9 @@ def pack_fp4(codes_canon: torch.Tensor, sf_canon: torch.Tensor, K: int, N: int, 
     GPU -> (packed codes, packed scales), two uint8 device tensors."""
     dev = _cuda(codes_canon, "codes_canon").device
     _cuda(sf_canon, "sf_canon")
-    wq = torch.empty(max(packed_bytes_fp4(K, N), 16), dtype=torch.uint8, device=dev)
-    s = torch.empty(max(scale_bytes_fp4(K, N), 16), dtype=torch.uint8, device=dev)
+    empty = _empty(stream)
+    wq = empty(max(packed_bytes_fp4(K, N), 16), dtype=torch.uint8, device=dev)
+    s = empty(max(scale_bytes_fp4(K, N), 16), dtype=torch.uint8, device=dev)
     _check(lib().nq_pack_fp4(_ptr(codes_canon), _ptr(sf_canon), K, N, _ptr(wq), _ptr(s), _stream(stream)))
     return wq, s
 
@@ -326,7 +351,7 @@ def gemm_fp4(x: torch.Tensor, wq: torch.Tensor, s: torch.Tensor, global_scale: f
     scale global_scale)."""
     _cuda(x, "x")
     T, K = x.shape
-    y = _out(x, N, out)
+    y = _out(x, N, out, stream)
     _check(lib().nq_gemm_fp4(_ptr(x), _ptr(wq), _ptr(s), ctypes.c_float(global_scale), _ptr(y), T, K, N,
                              _stream(stream)))
     return y
@@ -337,14 +362,14 @@ def swiglu_fp4(x, wg, sg, gate_scale: float, wu, su, up_scale: float, N: int, ou
     scales, tensor scale each)."""
     _cuda(x, "x")
     T, K = x.shape
-    h = _out(x, N, out)
+    h = _out(x, N, out, stream)
     _check(lib().nq_swiglu_fp4(_ptr(x), _ptr(wg), _ptr(sg), ctypes.c_float(gate_scale), _ptr(wu), _ptr(su),
                                ctypes.c_float(up_scale), _ptr(h), T, K, N, _stream(stream)))
     return h
 
 
 def dequant_fp4_debug(wq, s, global_scale: float, K: int, N: int, stream=None) -> torch.Tensor:
-    out = torch.empty((N, K), dtype=torch.float32, device=wq.device)
+    out = _empty(stream)((N, K), dtype=torch.float32, device=wq.device)
     _check(lib().nq_dequant_fp4_debug(_ptr(wq), _ptr(s), ctypes.c_float(global_scale), _ptr(out), K, N,
                                       _stream(stream)))
     return out
@@ -542,10 +567,10 @@ def page_tables(lens, new_lens, free_blocks, num_free, block_table, page: int, m
     R = lens.numel()
     table, max_blocks, stride = _rows(block_table, "block_table", i32, R)
     if out is None:
-        dev = lens.device
-        out = (torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev),
-               torch.empty(max_tokens, dtype=i32, device=dev), torch.empty(max_tokens, dtype=torch.int64, device=dev),
-               torch.empty(3, dtype=i32, device=dev))
+        dev, empty = lens.device, _empty(stream)
+        out = (empty(R + 1, dtype=i32, device=dev), empty(R, dtype=i32, device=dev),
+               empty(max_tokens, dtype=i32, device=dev), empty(max_tokens, dtype=torch.int64, device=dev),
+               empty(3, dtype=i32, device=dev))
     q_start, kv_lens, positions, slots, counts = out
     free = free_blocks.numel()
     _check(lib().nq_page_tables(_flat(lens, "lens", i32, R), _flat(new_lens, "new_lens", i32, R), R,
@@ -578,7 +603,7 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, kv_lens, scale: float 
     cache, dt, _, dim = _kv_cache(k_cache, v_cache)
     qp, tokens, heads, qs = _tokens(q, "q", dt, None, dim)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=dt, device=q.device)
+        out = _empty(stream)((tokens, heads, dim), dtype=dt, device=q.device)
     op, tokens_o, _, os_ = _tokens(out, "out", dt, heads, dim)
     if tokens_o != tokens:
         raise ValueError("out must have q's shape")
@@ -610,7 +635,7 @@ def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, 
     if V_noise != V:
         raise ValueError("noise must have the shape of logits")
     if out is None:
-        out = torch.empty(B, dtype=torch.int32, device=logits.device)
+        out = _empty(stream)(B, dtype=torch.int32, device=logits.device)
     _check(lib().nq_sample(lp, dtype, stride, np_, noise_stride, B, V,
                            None if temperature is None else _flat(temperature, "temperature", f32, B),
                            None if top_k is None else _flat(top_k, "top_k", torch.int32, B),
@@ -639,8 +664,9 @@ def quant_fp8(x, out=None, stream=None):
     rows = x.shape[0]
     xp, K, stride = _rows(x, "x", x.dtype, rows)
     if out is None:
-        out = (torch.empty((rows, K), dtype=_E4M3, device=x.device),
-               torch.empty((rows, -(-K // 128)), dtype=torch.float32, device=x.device))
+        empty = _empty(stream)
+        out = (empty((rows, K), dtype=_E4M3, device=x.device),
+               empty((rows, -(-K // 128)), dtype=torch.float32, device=x.device))
     codes, scales = out
     cp, K_c, cs = _rows(codes, "codes", _E4M3, rows)
     sp, blocks, ss = _rows(scales, "scales", torch.float32, rows)
@@ -693,9 +719,10 @@ def _fp8(fn, xq, xs, weights, dtype, out, stream, experts=None):
     if kb != -(-K // 128):
         raise ValueError("xs must have a column for each 128 of xq")
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=xq.device)
+        empty = _empty(stream)
+        out = empty((M, N), dtype=dtype, device=xq.device)
         if dtype is _E4M3:
-            out = (out, torch.empty((M, -(-N // 128)), dtype=torch.float32, device=xq.device))
+            out = (out, empty((M, -(-N // 128)), dtype=torch.float32, device=xq.device))
     if dtype is _E4M3:
         yp, N_y, ys = _rows(out[0], "out", dtype, M)
         yc, nb, yss = _rows(out[1], "out's scales", torch.float32, M)
@@ -715,8 +742,8 @@ def _fp8(fn, xq, xs, weights, dtype, out, stream, experts=None):
         if need:
             if stream is None:
                 scratch = torch.empty(need, dtype=torch.uint8, device=xq.device)
-            else:                                # (the current one's free memory may still be written there)
-                with torch.cuda.stream(stream):
+            else:                                # (used there alone)
+                with _own(stream):
                     scratch = torch.empty(need, dtype=torch.uint8, device=xq.device)
         _check(fn(x, rows, M, offsets, E, *packed, y, K, N, scratch.data_ptr() if need else None, _raw_stream(stream)))
     return out
@@ -756,10 +783,10 @@ def moe_route(logits, k: int, bias=None, score: str = "softmax", normalize: bool
     T, i32 = logits.shape[0], torch.int32
     lp, E, stride = _rows(logits, "logits", logits.dtype, T)
     if out is None:
-        dev = logits.device
-        out = (torch.empty((T, k), dtype=i32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev),
-               torch.empty(E + 1, dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev),
-               torch.empty((T, k), dtype=i32, device=dev))
+        dev, empty = logits.device, _empty(stream)
+        out = (empty((T, k), dtype=i32, device=dev), empty((T, k), dtype=torch.float32, device=dev),
+               empty(E + 1, dtype=i32, device=dev), empty(T * k, dtype=i32, device=dev),
+               empty((T, k), dtype=i32, device=dev))
     ids, weights, offsets, rows, slots = out
     n = T * k
     _check(lib().nq_moe_route(lp, dtype, stride, None if bias is None else _flat(bias, "bias", torch.float32, E), T, E, k,
@@ -784,7 +811,7 @@ def moe_combine(y, slots, weights, base=None, out=None, stream=None):
         if N_b != N:
             raise ValueError("base must have y's columns")
     if out is None:
-        out = torch.empty((T, N), dtype=dt, device=y.device)
+        out = _empty(stream)((T, N), dtype=dt, device=y.device)
     op, N_o, os_ = _rows(out, "out", dt, T)
     if N_o != N:
         raise ValueError("out must have y's columns")
