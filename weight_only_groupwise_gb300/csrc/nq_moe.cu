@@ -80,8 +80,6 @@ __device__ __forceinline__ float route_value(uint32_t key) {
     return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
 }
 
-__device__ __forceinline__ float sigmoid_f(float l) { return 1.f / (1.f + expf(-l)); }
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
@@ -237,9 +235,10 @@ __device__ __forceinline__ void route_choose(const RouteArgs& a, int t, RouteWar
         float top = c;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        // far below zero the sigmoid is e^l: taken relative to the largest, it does not vanish
-        const bool far = a.normalize && top < -60.f;
-        w = mine < 0 ? 0.f : (far ? expf(c - top) : sigmoid_f(c));
+        // e^c / (1 + e^c) of a score below one half. Where only ratios count, all scores without the factor that the largest
+        // has in e^c, so that those which fp32 cannot hold do not vanish.
+        const float m = a.normalize ? fminf(top, 0.f) : 0.f;
+        w = mine < 0 ? 0.f : (c > 0.f ? 1.f : expf(c - m)) / (1.f + expf(-fabsf(c)));
         if (a.normalize) {
             const float sum = warp_sum(w);
             if (mine >= 0) w = w / sum;
