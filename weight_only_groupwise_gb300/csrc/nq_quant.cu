@@ -81,7 +81,9 @@ struct Eight {
     }
 };
 
-// x / s for two, with r = 1 / s rounded: the product and one correction by its residual, which is exact in an fma.
+// x / s for two, with r = 1 / s rounded: the product and one correction by its residual, which is exact in an fma. Rounding
+// the residual down makes no difference to it but for its sign where it is zero: -0, which added to a quotient of either zero
+// leaves that as it is (+0 turns -0 into +0).
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990: rounded as the quotient
 // is. A division each took 92 us for 8191 x 17408 in 16 bits, single ones of this 74, two at a time and the largest of two
 // at a time 72.)
@@ -94,7 +96,7 @@ __device__ __forceinline__ void quotients(float& a, float& b, uint64_t minus_s, 
     const uint64_t x = two(a, b);
     uint64_t q, e;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(r));
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(minus_s), "l"(x));
+    asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(minus_s), "l"(x));
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(r), "l"(q));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
 }
