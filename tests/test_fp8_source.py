@@ -1,9 +1,10 @@
 """What the 8-bit products must have in their source and no run can show for certain. No GPU."""
+import os
 import re
 
 import pytest
 
-from tests.test_step_source import body
+from tests.test_step_source import CSRC, body
 
 KERNELS = ["fp8_rows_kernel", "fp8_cols_kernel"]
 
@@ -40,3 +41,15 @@ def test_bounded_waits_begin_when_the_call_ahead_has_ended(kernel):
     late = role(producer, "auto x_late", "};")
     assert late.index("grid_dependency_wait();") < late.index("f8_copy_2d(")
     assert "if (seq + 1 == late) x_late(late);" in producer
+
+
+def test_resident_clusters_are_counted_on_each_device():
+    """What is asked of the driver once is asked for the device that is current, as devices differ; a failure on one stays there."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "nq_fp8.cu")).read())
+    at = text.index("fp8_clusters(int ")
+    f = text[at:text.index("\n}\n", at)]
+    assert re.match(r"fp8_clusters\(int dev, int sms\)", f)
+    assert "static std::once_flag once[kDevices];" in f and "static int most[kDevices][kF8MostSplit + 1]" in f
+    assert "std::call_once(once[dev]," in f and "most[dev]" in f
+    assert re.search(r"dev < 0 \|\| dev >= kDevices", f)
+    assert re.findall(r"fp8_clusters\(([^)]*)\)", text)[1:] == ["dev, d.sms"]

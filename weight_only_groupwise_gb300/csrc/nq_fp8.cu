@@ -132,14 +132,20 @@ __global__ void __launch_bounds__(kGatherThreads) fp8_gather_kernel(const Gather
         a.to_scales[(long long)i * a.scale_stride + b] = there ? __ldg(a.xs + r * a.xs_stride + b) : 0.f;
 }
 
-// Clusters of n blocks that can run at once, by n (queried once).
-const int* fp8_clusters(int sms) {
-    static std::once_flag once;
-    static int most[kF8MostSplit + 1] = {};
-    std::call_once(once, [sms] {
+// Clusters of n blocks that can run at once, by n (queried once a device, which is the current one; none of a device past the
+// last that is counted).
+const int* fp8_clusters(int dev, int sms) {
+    static std::once_flag once[kDevices];
+    static int most[kDevices][kF8MostSplit + 1] = {};
+    static const int none[kF8MostSplit + 1] = {};
+    if (dev < 0 || dev >= kDevices) return none;
+    std::call_once(once[dev], [sms, n_of = most[dev]] {
         using Geo = Fp8ColsGeo<16, false>;
         auto kern = fp8_cols_kernel<16, false>;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) return;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) {
+            cudaGetLastError();
+            return;
+        }
         for (int n = 2; n <= kF8MostSplit; ++n) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(sms / n * n);
@@ -152,13 +158,13 @@ const int* fp8_clusters(int sms) {
             attr[0].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&most[n], kern, &cfg) != cudaSuccess) {
+            if (cudaOccupancyMaxActiveClusters(&n_of[n], kern, &cfg) != cudaSuccess) {
                 cudaGetLastError();
-                most[n] = 0;
+                n_of[n] = 0;
             }
         }
     });
-    return most;
+    return most[dev];
 }
 
 // Which kernel takes a call, and how. rows: of x in a tile of fp8_cols_kernel, or 0 for fp8_rows_kernel; split: blocks that
@@ -322,7 +328,7 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     c.wide = !mis(y->data, 16) && yst % 8 == 0;
     c.quads = !mis(x->scales, 16) && xss % 4 == 0;
     c.wait_ns = d.wait_ns;
-    const Fp8Plan plan = experts ? Fp8Plan{fp8_experts_rows(M, E, glu, rows && !gathers), 1} : fp8_dense_plan(M, K, N, glu, d.sms, fp8_clusters(d.sms));
+    const Fp8Plan plan = experts ? Fp8Plan{fp8_experts_rows(M, E, glu, rows && !gathers), 1} : fp8_dense_plan(M, K, N, glu, d.sms, fp8_clusters(dev, d.sms));
     const int bn = plan.rows;
     const bool few = bn > 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
