@@ -142,3 +142,12 @@ def test_good_calls_pass_the_checks(L):  # noqa: F811
     # one row's stride means nothing, nor one expert's
     assert passes(gemm(L, x=rows_of(rows=1, stride=HUGE, ss=HUGE), y=out(stride=HUGE))) and passes(gemm(L, w=weight(expert=HUGE, sexpert=HUGE)))
     assert passes(quant(L, rows=1, xs=HUGE, cs=HUGE, ss=HUGE)) and passes(route(L, T=1, stride=HUGE)) and passes(combine(L, T=1, bs=HUGE, os=HUGE))
+
+
+def test_scales_of_results_that_have_none_do_not_count(L):  # noqa: F811
+    """Results in 16 bits: whatever the field holds."""
+    if gpu():
+        pytest.skip("fake addresses: only where no GPU could be reached")
+    for scales, ss in ((8 * A + 1, 0), (7 * A, -5), (A, HUGE)):
+        y = out(scales=scales, ss=ss)
+        assert passes(gemm(L, y=y)) and passes(swiglu(L, y=y)) and passes(experts(L, y=y))

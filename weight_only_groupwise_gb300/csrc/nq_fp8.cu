@@ -278,7 +278,7 @@ int fp8_call(const nq_fp8_rows* x, bool experts, const int* rows, int M, const i
     for (int g = 0; g < 2; ++g)
         if (!v[g].codes || !v[g].scales) return NQ_ERR_NULL;
     if (mis(x->codes, 16) || xst % 16 || mis(x->scales, 4) || mis(y->data, codes ? 16 : 2) || (codes && yst % 16) ||
-        mis(y->scales, 4) || mis(rows, 4) || mis(offsets, 4) || mis(scratch, 16))
+        (codes && mis(y->scales, 4)) || mis(rows, 4) || mis(offsets, 4) || mis(scratch, 16))
         return NQ_ERR_ALIGN;
     for (int g = 0; g < 2; ++g)
         if (mis(v[g].codes, 16) || v[g].row_stride % 16 || v[g].expert_stride % 16 || mis(v[g].scales, 4)) return NQ_ERR_ALIGN;
