@@ -74,3 +74,28 @@ def test_results_are_not_in_memory_that_the_current_stream_still_writes(name):
         torch.cuda.synchronize()
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(read, want))
         del writes, junk, j
+
+
+@pytest.mark.parametrize("name", ["quant", "gemm", "experts' swiglu", "route", "combine"])
+def test_a_branch_of_a_captured_graph(name):
+    call = calls(torch.Generator(device="cuda").manual_seed(4))[name]
+    want = several(call())
+    torch.cuda.synchronize()
+    other, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        current = torch.cuda.current_stream()
+        other.wait_stream(current)
+        for _ in range(3):               # results made and dropped
+            got = several(call(stream=other))
+        current.wait_stream(other)
+        read = [y.clone() for y in got]
+        del got
+        more = several(call())
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for y in (read, more):
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(y, want))
+    again = several(call(stream=torch.cuda.default_stream()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(again, want))
