@@ -535,7 +535,7 @@ nq_status nq_sample(const void* logits, int dtype, long long stride, const float
  *   x[t, k] = sx[t, k / 128] * e4m3(cx[t, k]),   w[n, k] = sw[n / 128, k / 128] * e4m3(cw[n, k])
  *
  * The last block of a row or column may be short. Codes are bytes (e4m3 "fn": no infinity, S.1111.111 is NaN),
- * scales fp32.
+ * scales fp32; the product of x's scale and the weight's is formed in fp32, with its range.
  */
 
 /* Rows of activations: codes [rows][K], `stride` apart (a multiple of 16), scales [rows][ceil(K / 128)],
@@ -569,7 +569,7 @@ typedef struct nq_fp8_out {
 /*
  * nq_quant_fp8: x (dtype NQ_BF16, NQ_FP16 or NQ_FP32) [rows][K] as codes and scales:
  *   s[r, b] = max(max_{k in b} |x[r, k]| / 448, 2^-126),   c[r, k] = e4m3(x[r, k] / s[r, b]),
- * in fp32, rounded to nearest even. A block with a NaN gets scale NaN and codes NaN; one with an infinity scale inf
+ * in fp32, rounded to nearest even (both zeros keep their signs). A block with a NaN gets scale NaN and codes NaN; one with an infinity scale inf
  * (codes NaN where x is infinite, else 0): its products are NaN. K a multiple of 16, at most 2^20; rows <= 2^24. Rows of x
  * and codes 16-byte aligned.
  */
@@ -596,7 +596,8 @@ nq_status nq_swiglu_fp8(const nq_fp8_rows* x, const nq_fp8_weight* wg, const nq_
  *         as zeros); NULL: row i of x, and then M <= x->rows
  *   scratch  nq_fp8_scratch_bytes(M, E, K, swiglu) bytes of device memory, 16-byte aligned, for many gathered rows, which are
  *         copied together there first; NULL: they are gathered by the product's own copies, which takes longer
- * offsets are clamped to 0..M and taken as non-decreasing. Rows of the result before offsets[0] and from offsets[E] on
+ * offsets are clamped to 0..M and taken as non-decreasing (where they are not, the results of rows
+ * that several experts get are undefined). Rows of the result before offsets[0] and from offsets[E] on
  * are left as they are. 1 <= E <= 512. The tensors of experts without rows are not read.
  */
 nq_status nq_gemm_fp8_experts(const nq_fp8_rows* x, const int* rows, int M, const int* offsets, int E,
@@ -669,7 +670,9 @@ nq_status nq_device_error(void);
  * read at the first call. A wait that runs out aborts its thread block (its outputs are
  * undefined, nq_device_error reports NQ_ERR_TIMEOUT) after the block has waited, on a
  * separate fixed bound, for the copies it already issued. A bound far below a kernel's run
- * time makes calls abort: that is how the tests reach this path.
+ * time makes calls abort: that is how the tests reach this path. The waits of attention and of the
+ * 8-bit products begin when the call ahead has ended; a projection's for its activations may also
+ * count what the call ahead has left to run when its blocks start.
  */
 long long nq_wait_limit(long long ns);
 

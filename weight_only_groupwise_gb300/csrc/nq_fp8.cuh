@@ -180,7 +180,8 @@ __device__ __forceinline__ uint32_t pack_16(float lo, float hi, bool bf16) {
 // function unit: a tile's 16384 of them were a sixth of its time (32 blocks of K) with expf and a division. The divisor stays
 // between 1 and 2: that quotient is 0 for divisors above 2^126, which 1 + e^-g is for gates below -87.3. The
 // exponential's argument is rounded: an error of |g| 2^-23 at most, with two places each of the two functions and a half
-// of the sum and of each product.
+// of the sum and of each product. (2048 x 5120 x 17408: 324.8 us, 323.0 with g u / (1 + e^-g) for all; 324.2 with that
+// where a thread has no gate below -87.)
 __device__ __forceinline__ float f8_silu_mul(float g, float u) {
     const float e = __expf(-fabsf(g));
     return __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;
